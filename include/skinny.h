@@ -385,6 +385,123 @@ skinny_status skinny_select_table(const skinny_tactic *cand, const double *times
                                   int count, skinny_tactic *table);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Products in 8-bit integers
+ * ---------------------------------------------------------------------------
+ *
+ *   out[m][n] = (sum_k xq[m][k] Wq[n][k]) x_scale[m] w_scale[n] (+ residual[m][n])
+ *
+ * with xq and Wq 8-bit integers, one fp32 scale for each token and for each
+ * output channel.  The integers' sum is exact (32 bits); it is rounded to fp32
+ * once, then scaled and rounded to the output type.
+ */
+typedef enum {
+    SKINNY_TYPE_BF16 = 0,
+    SKINNY_TYPE_F32 = 1,
+    SKINNY_TYPE_F16 = 2
+} skinny_type;
+
+/*
+ * skinny_quantize_rows -- rows of x [M][K] (element m * ldx + k, `type`) to
+ * 8-bit integers q[m][k] (element m * ldq + k) and scale[m]:
+ *
+ *   scale = max_k |x| / 127,   q = round to nearest even (x * (127 / max_k |x|))
+ *
+ * in fp32.  A row of zeros has scale 0 and q = 0; a row with an infinity or
+ * NaN has scale NaN and q = 0.  Rows whose largest value is below 2^-60 are
+ * multiplied by 2^64 on the way, so that 127 / max stays finite.  M = 0 does
+ * nothing.  Any K >= 1 and any pitch >= K; x must be aligned to its elements.
+ * Pitches and pointers that are multiples of 16 bytes (x) and 8 bytes (q) are
+ * read and written in whole vectors.  Asynchronous on `stream`; one launch.
+ */
+skinny_status skinny_quantize_rows(const void *x, skinny_type type, int M, int K, long long ldx, void *q,
+                                   long long ldq, float *scale, void *stream);
+
+typedef struct skinny_int8_plan skinny_int8_plan;
+
+/*
+ * skinny_int8_prepare -- a plan for an 8-bit weight Wq [N][K] (element
+ * n * ldw + k) with w_scale [N].  Both are copied (Wq laid out in the order in
+ * which the matrix units take it) on `stream`, which is waited for, so the
+ * caller may free them afterwards.  Must not be called during graph capture.  Requires N >= 1,
+ * 16 <= K < 131072 (the largest sum of products then fits 32 bits),
+ * K % 16 == 0 and ldw >= K.
+ */
+skinny_status skinny_int8_prepare(const void *Wq, int N, int K, long long ldw, const float *w_scale,
+                                  skinny_type out_type, void *stream, skinny_int8_plan **plan);
+
+/*
+ * skinny_int8_run -- the product above for M >= 0 tokens on `stream`,
+ * asynchronously.  xq: element m * ldx + k, 16-byte aligned, ldx % 16 == 0;
+ * x_scale [M]; residual (NULL for none) and out have the plan's out type,
+ * elements m * ldr + n and m * ldo + n; residual may be out itself (ldr == ldo)
+ * but must not otherwise overlap out.  No allocation or synchronisation: may
+ * be captured in a graph.  A plan holds the workspace of its K splits: one plan must
+ * not run on two streams at once.  Different plans may.
+ */
+skinny_status skinny_int8_run(const skinny_int8_plan *plan, const void *xq, long long ldx, const float *x_scale,
+                              const void *residual, long long ldr, void *out, long long ldo, int M,
+                              void *stream);
+
+/* skinny_int8_destroy -- frees the plan after synchronising its device.  NULL is a no-op. */
+void skinny_int8_destroy(skinny_int8_plan *plan);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head and token
+ * ---------------------------------------------------------------------------
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t
+ *
+ * q, k [tokens][key_heads][dk] and v, out [tokens][heads][dv] in BF16 or FP16,
+ * log decays g [tokens][heads] and states S [pool][heads][dk][dv] in fp32;
+ * value head h reads key head h / (heads / key_heads).  g is a log of a decay:
+ * at most 0, -inf for a state that is forgotten (larger values are taken as
+ * they are, as far as fp32 goes).  All arithmetic on states, decays and sums
+ * is fp32 or wider.  A value that is not finite reaches the outputs and states
+ * that depend on it by the formulas above and no others.
+ */
+typedef struct {
+    const void *q, *k, *v;      /* 16-byte aligned, last dimension contiguous */
+    void *out;                  /* must not overlap the inputs */
+    const float *log_decay;
+    const float *state_in;      /* [pool] states, NULL: every sequence starts from zero */
+    float *state_out;           /* [pool] states, NULL: the new states are not kept; may be state_in */
+    const int *starts;          /* prompt: [sequences + 1], token range i is starts[i] .. starts[i + 1] */
+    const int *slots;           /* [sequences] rows of the state pools, all different; NULL: 0, 1, 2, ...
+                                   A slot outside the pool is no state: zero in, not written */
+    void *workspace;            /* prompt: skinny_linear_workspace bytes, 16-byte aligned */
+    size_t workspace_bytes;
+    /* strides in elements: multiples of 8 below 2^24 for q, k, v and out, of 4 for the states */
+    long long q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+    long long decay_token, decay_head;
+    long long in_state_slot, in_state_head, out_state_slot, out_state_head;
+    int type;                   /* skinny_in_dtype of q, k, v and out */
+    int tokens, sequences, heads, key_heads, dk, dv, pool;
+    float scale;
+} skinny_linear_args;
+
+/*
+ * skinny_linear_workspace -- bytes of workspace a prompt of these sizes needs
+ * (0 for short ones): the states between the parts that long sequences are cut
+ * into.  Its contents do not matter before a call and mean nothing after it.
+ */
+size_t skinny_linear_workspace(int tokens, int sequences, int heads, int dk, int dv);
+
+/*
+ * skinny_linear_prompt -- the recurrence over packed sequences of any lengths,
+ * zero included, from state_in (or zero) to state_out.  dk <= 256 and
+ * dv <= 1024, multiples of 8.  starts is read on the device, clamped to
+ * 0 .. tokens; it should rise from 0 to tokens (tokens outside every sequence
+ * are not written).  Asynchronous on `stream`; one launch, or three where a
+ * sequence may be long; capturable.
+ */
+skinny_status skinny_linear_prompt(const skinny_linear_args *args, void *stream);
+
+/* skinny_linear_step -- one new token of each sequence: token i is sequence i (tokens == sequences). */
+skinny_status skinny_linear_step(const skinny_linear_args *args, void *stream);
+
+/*
  * Measurement helpers (not part of the projection).  They put the projection's
  * timings in context: the decode-step cost the pages care about is streaming
  * the weight at HBM speed, so a bench compares against what a plain stream of

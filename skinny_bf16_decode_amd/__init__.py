@@ -93,7 +93,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             f"{path} is missing: build it with `python -m skinny_bf16_decode_amd.build` "
             "(there is no non-HIP fallback)")
     lib = ctypes.CDLL(path)
-    vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, i, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
     planp = ctypes.c_void_p
     tp = ctypes.POINTER(Tactic)
     sig = {
@@ -114,6 +114,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "skinny_enumerate_tactics_ex": (i, [i, i, i, tp, i]),
         "skinny_select_table": (i, [tp, ctypes.POINTER(ctypes.c_double), i, tp]),
         "skinny_run_static": (i, [vp, i, i, i, i, i, tp, vp, i, vp, i, vp, i, i, vp]),
+        "skinny_quantize_rows": (i, [vp, i, i, i, ll, vp, ll, vp, vp]),
+        "skinny_int8_prepare": (i, [vp, i, i, ll, vp, i, vp, ctypes.POINTER(planp)]),
+        "skinny_int8_run": (i, [planp, vp, ll, vp, vp, ll, vp, ll, i, vp]),
+        "skinny_int8_destroy": (None, [planp]),
+        "skinny_linear_workspace": (sz, [i, i, i, i, i]),
+        "skinny_linear_prompt": (i, [vp, vp]),
+        "skinny_linear_step": (i, [vp, vp]),
         "skinny_probe_read": (i, [vp, sz, vp, vp]),
         "skinny_probe_read_blocks": (i, []),
         "skinny_probe_empty": (i, [vp]),
@@ -172,6 +179,14 @@ def _stream_handle(stream):
         import torch
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def stream_handle(stream, device):
+    """hipStream_t of the given stream (an object or a handle), or of the device's current one."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def probe_read(buf_ptr: int, nbytes: int, sink_ptr: int, stream=None) -> None:

@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libskinny.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
-SOURCES = ["kernels.hip", "plan.cpp", "tactics.cpp", "tables.cpp"]
+SOURCES = ["kernels.hip", "plan.cpp", "tactics.cpp", "tables.cpp", "int8.hip", "linear_attention.hip"]
 
 COMMON = [
     f"--offload-arch={ARCH}",

@@ -1,0 +1,1176 @@
+// HIP kernels and entry points of linear attention with a decay for each head
+// and token, for gfx950 (CDNA4):
+//
+//   S_t = exp(g_t) S_{t-1} + k_t v_t^T        S [dk][dv], fp32
+//   o_t = scale q_t^T S_t
+//
+// for every value head, over packed sequences (prompt) or one new token of
+// each sequence (step).
+//
+// The prompt works in chunks of 64 tokens.  With G_t the sum of the log decays
+// of a chunk through token t and S the state before it,
+//
+//   o_t   = scale (exp(G_t) q_t^T S + sum_{s <= t} exp(G_t - G_s) (q_t . k_s) v_s)
+//   S_new = exp(G_63) S + sum_s k_s (exp(G_63 - G_s) v_s)^T
+//
+// which are four matrix products a chunk.  A workgroup of four waves walks the
+// chunks of one (sequence part, head, 64 NV value columns); each wave keeps the
+// state of its own 16 NV columns in registers, in the result layout of the
+// 16x16x32 MFMA, from one chunk to the next.
+#include <hip/hip_runtime.h>
+
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "linear_places.h"
+#include "skinny_internal.h"
+
+namespace skinny {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
+typedef __attribute__((ext_vector_type(2))) unsigned int u32x2;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+
+constexpr int kChunk = 64;
+constexpr int kThreads = 256;
+
+// Kernel arguments.  Strides are in elements.
+struct LArgs {
+    const void *q, *k, *v;
+    void *out;
+    const float *g;
+    const float *state_in;
+    float *state_out;
+    const int *starts;          // prompt: [sequences + 1]
+    const int *slots;           // [sequences], or NULL: sequence i holds slot i
+    float *ws_state;            // prompt in parts: [place][head][dk][dv]
+    double *ws_decay;           // [place][head], sums of log2 decays
+    int *ws_serial;             // [sequence][head], the part from which on the sequence is taken in one go
+    long long q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head, g_token, g_head;
+    long long in_slot, in_head, so_slot, so_head;
+    int tokens, sequences, heads, share, dk, dv, pool;
+    int part;                   // tokens of a part of a sequence, a multiple of 64
+    int places;                 // parts a launch provides for
+    int col_tiles;              // workgroups along dv
+    int multi;                  // a sequence may have more than one part
+    float scale;
+};
+
+template <bool H>
+__device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c)
+{
+    if constexpr (H)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
+                                                      0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+}
+
+// One 16-bit value of an LDS tile or of a register half, as fp32.
+template <bool H>
+__device__ __forceinline__ float to_float(unsigned short bits)
+{
+    if constexpr (H)
+        return (float)__builtin_bit_cast(_Float16, bits);
+    else
+        return __uint_as_float((unsigned)bits << 16);
+}
+
+template <bool H>
+__device__ __forceinline__ unsigned short to_bits(float v)
+{
+    if constexpr (H)
+        return __builtin_bit_cast(unsigned short, (_Float16)v);
+    else
+        return __builtin_bit_cast(unsigned short, (__bf16)v);
+}
+
+template <bool H>
+__device__ __forceinline__ void unpack2(unsigned int w, float &lo, float &hi)
+{
+    lo = to_float<H>((unsigned short)(w & 0xFFFFu));
+    hi = to_float<H>((unsigned short)(w >> 16));
+}
+
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+
+// Two fp32 values as the sum of TERMS pairs of 16-bit values.  BF16 (8 bits a
+// term, cut off, so that what is left is exact): 16 bits for two terms, all 24
+// for three.  FP16 (11 bits a term, the caller scales into its range): 22 bits.
+template <bool H, int TERMS>
+__device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[TERMS])
+{
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        if constexpr (H) {
+            const auto p = __builtin_amdgcn_cvt_pkrtz(a, b);
+            w[i] = __builtin_bit_cast(unsigned int, p);
+            a -= (float)p[0];
+            b -= (float)p[1];
+        } else {
+            w[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+            a -= cut(a);
+            b -= cut(b);
+        }
+    }
+}
+
+// Eight fp32 values into TERMS MFMA operands.
+template <bool H, int TERMS>
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[TERMS])
+{
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        unsigned int w[TERMS];
+        split2<H, TERMS>(x[2 * p], x[2 * p + 1], w);
+#pragma unroll
+        for (int i = 0; i < TERMS; ++i)
+            f[i][p] = w[i];
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float x)
+{
+    return fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true)));
+}
+
+// Largest value over the wave, in every lane (values >= 0; NaN is passed over).
+__device__ __forceinline__ float wave_max(float x)
+{
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    x = dpp_max<0x140>(x);      // row_mirror
+    x = dpp_max<0x141>(x);      // row_half_mirror
+    x = dpp_max<0x4E>(x);       // quad_perm [2,3,0,1]
+    return dpp_max<0xB1>(x);    // quad_perm [1,0,3,2]
+}
+
+// Power of two that brings values of at most `top` below 2^15, and its inverse:
+// an FP16 split of the scaled values is good to 2^-40 of `top`.
+__device__ __forceinline__ void half_range(float top, float &mul, float &back)
+{
+    unsigned e = __float_as_uint(top) >> 23;
+    e = e < 15u ? 15u : (e > 254u ? 254u : e);
+    mul = __uint_as_float((268u - e) << 23);
+    back = __uint_as_float((e - 14u) << 23);
+}
+
+// Whether any lane of the wave saw a value that is not finite: acc gathers x * 0.
+__device__ __forceinline__ bool wave_any_nan(float acc) { return __ballot(acc != 0.0f) != 0ull; }
+
+// The place of a workgroup: its sequence is the last that starts at or before it.
+__device__ __forceinline__ bool locate(const LArgs &a, int place, Place &p)
+{
+    const int lane = threadIdx.x & 63;
+    int count = 0;
+    for (int i0 = 0; i0 < a.sequences; i0 += 64) {
+        const int i = i0 + lane;
+        bool at = false;
+        if (i < a.sequences)
+            at = first_place(a.starts[i], a.tokens, a.part, i) <= place;
+        count += __popcll(__ballot(at));
+    }
+    if (count == 0)
+        return false;
+    const int seq = __builtin_amdgcn_readfirstlane(count - 1);
+    return place_of(a.starts[seq], a.starts[seq + 1], a.tokens, a.part, place, seq, p);
+}
+
+// Slot of a sequence, or -1 where the pool has none of that number.
+__device__ __forceinline__ int slot_of(const LArgs &a, int seq)
+{
+    const int s = a.slots ? a.slots[seq] : seq;
+    return s >= 0 && s < a.pool ? s : -1;
+}
+
+// A tile of 64 token rows of COLS 16-bit columns on its way from global memory
+// through registers to LDS.  Rows from `rows` on and columns from `cols` on
+// are zero.
+template <int COLS>
+struct Tile {
+    static constexpr int kPerRow = COLS / 8;
+    static constexpr int kVecs = kChunk * kPerRow / kThreads;
+    static constexpr int kRowStep = kThreads / kPerRow;
+    u32x4 r[kVecs];
+
+    __device__ __forceinline__ void load(const unsigned short *base, long long stride, int rows, int cols)
+    {
+        const int row = threadIdx.x / kPerRow, col = (threadIdx.x % kPerRow) * 8;
+        const unsigned off = (unsigned)(row * (int)stride + col);     // strides are below 2^24
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const unsigned short *p = base + (long long)i * kRowStep * stride;
+            r[i] = u32x4{0u, 0u, 0u, 0u};
+            if (row + i * kRowStep < rows && col < cols)
+                r[i] = *reinterpret_cast<const u32x4 *>(p + off);
+        }
+    }
+
+    __device__ __forceinline__ void store(unsigned short *lds, int pitch) const
+    {
+        const int row = threadIdx.x / kPerRow, col = (threadIdx.x % kPerRow) * 8;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            *reinterpret_cast<u32x4 *>(lds + (row + i * kRowStep) * pitch + col) = r[i];
+    }
+};
+
+// MFMA operand from 16 token rows: lane (row l % 16) holds columns
+// 32 j + 4 (l / 16) + 0..3 and the 4 columns 16 further on, the order in
+// which the state's result registers hold dk.
+__device__ __forceinline__ u32x4 row_operand(const unsigned short *lds, int pitch, int row0, int j)
+{
+    const int lane = threadIdx.x & 63;
+    const unsigned short *p = lds + (row0 + (lane & 15)) * pitch + 32 * j + 4 * (lane >> 4);
+    const u32x2 a = *reinterpret_cast<const u32x2 *>(p), b = *reinterpret_cast<const u32x2 *>(p + 16);
+    return u32x4{a.x, a.y, b.x, b.y};
+}
+
+// MFMA operand from 16 columns over the 32 tokens 32 j..: lane (column l % 16)
+// holds tokens 32 j + 4 (l / 16) + 0..3 and the 4 tokens 16 further on.  The
+// transposing LDS read gives each lane of 16 four rows of its own column.
+__device__ __forceinline__ u32x4 column_operand(const unsigned short *lds, int pitch, int col0, int j)
+{
+    const int lane = threadIdx.x & 63, in = lane & 15;
+    const unsigned short *p = lds + (32 * j + 4 * (lane >> 4) + (in >> 2)) * pitch + col0 + 4 * (in & 3);
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * pitch));
+    const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+    return u32x4{x.x, x.y, y.x, y.y};
+}
+
+// Per-token decay values of a chunk, in LDS.
+struct alignas(16) Decays {
+    float hi[kChunk], lo[kChunk];   // G_t log2 e as a sum of two fp32 values
+    float grown[kChunk];            // exp(G_t)
+    float rest[kChunk];             // exp(G_63 - G_t)
+    float own[kChunk];              // exp(g_t)
+    float total;                    // exp(G_63)
+};
+
+// Wave 0: lane t has g_t (0 past the end).  Sums are in 64 bits, so that the
+// differences of far-decayed chunks keep their bits.  Finite sums are wanted
+// of -inf too: -200 gives 0 as well.  NaN stays.
+__device__ __forceinline__ double chunk_decays(float g, Decays &d)
+{
+    const int lane = threadIdx.x & 63;
+    double x = (double)(g < -200.0f ? -200.0f : g) * 1.44269504088896340736;
+    const float own = (float)x;
+#pragma unroll
+    for (int step = 1; step < 64; step *= 2) {
+        const double y = __shfl_up(x, step, 64);
+        if (lane >= step)
+            x += y;
+    }
+    const double all = __shfl(x, 63, 64);
+    const float hi = (float)x;
+    d.hi[lane] = hi;
+    d.lo[lane] = (float)(x - (double)hi);
+    d.grown[lane] = __builtin_amdgcn_exp2f(hi);
+    d.rest[lane] = __builtin_amdgcn_exp2f((float)(all - x));
+    d.own[lane] = __builtin_amdgcn_exp2f(own);
+    if (lane == 63)
+        d.total = __builtin_amdgcn_exp2f(hi);
+    return all;
+}
+
+// The (t-tile, 32-token step) operands of the masked scores that the causal
+// mask leaves: tiles 0 and 1 have one, 2 and 3 two.
+__device__ __host__ constexpr int score_slot(int tile, int j) { return (tile < 2 ? tile : 2 * tile - 2) + j; }
+constexpr int kScoreSlots = 6;
+
+template <int DK, int NV, bool OUT>
+struct Layout {
+    static constexpr int kQPitch = DK + 8;      // row reads: 16 rows x 16 bytes on all banks
+    static constexpr int kKPitch = DK + 16;     // transposing reads: 8 rows x 32 bytes on all banks
+    static constexpr int kVPitch = 64 * NV + 16;
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + (OUT ? kChunk * kQPitch * 2 : 0);
+    static constexpr int kV = kK + kChunk * kKPitch * 2;
+    static constexpr int kScores = kV + kChunk * kVPitch * 2;
+    static constexpr int kBytes = kScores + (OUT ? kScoreSlots * 2 * 64 * 16 : 0);
+};
+
+// The recurrence token by token, as it is defined, for one wave's columns of a
+// chunk in LDS: used where a value is not finite, since 0 * inf in a product
+// over masked tokens, or in a split into terms, would spread NaN to outputs
+// that the definition leaves alone.
+template <bool H, int DK, int NV, bool OUT>
+__device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds, const Decays &d, int rows,
+                                   f32x4 (&S)[DK / 16][NV], unsigned short *out, int col0)
+{
+    using L = Layout<DK, NV, OUT>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
+    for (int t = 0; t < rows; ++t) {
+        const float e = d.own[t];
+        int dk = a.dk;
+        asm volatile("" : "+s"(dk));                // compared anew: 4 DK / 16 lane masks are not kept over the loop
+        float v[NV], o[NV];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            v[n] = to_float<H>(vs[t * L::kVPitch + 16 * (NV * wave + n) + (lane & 15)]);
+            o[n] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i) {
+            __builtin_amdgcn_sched_barrier(0);      // few loads in flight: the path is rare, registers are not
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int c = 16 * i + 4 * g + r;
+                const float k = to_float<H>(ks[t * L::kKPitch + c]);
+                float q = 0.0f;
+                if constexpr (OUT)
+                    q = to_float<H>(qs[t * L::kQPitch + c]);
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    // columns past dk hold no state: 0 * a non-finite v is not theirs to add
+                    const float s = c < dk ? S[i][n][r] * e + k * v[n] : 0.0f;
+                    S[i][n][r] = s;
+                    if constexpr (OUT)
+                        o[n] += c < dk ? q * s : 0.0f;
+                }
+            }
+        }
+        if constexpr (OUT) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                float x = o[n];
+                x += __shfl_xor(x, 16, 64);
+                x += __shfl_xor(x, 32, 64);
+                const int c = col0 + 16 * (NV * wave + n) + (lane & 15);
+                if (g == 0 && c < a.dv)
+                    out[t * a.out_token + c] = to_bits<H>(x * a.scale);
+            }
+        }
+    }
+}
+
+// Natural [dk][dv] state <-> result registers of the wave's columns.
+template <int DK, int NV>
+__device__ __forceinline__ void load_state(const LArgs &a, const float *p, int col0, f32x4 (&S)[DK / 16][NV])
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned dk = (unsigned)a.dk, dv = (unsigned)a.dv;
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const unsigned row = 16 * i + 4 * (lane >> 4) + r, c = col0 + 16 * (NV * wave + n) + (lane & 15);
+                S[i][n][r] = p && row < dk && c < dv ? p[row * dv + c] : 0.0f;
+            }
+    }
+}
+
+template <int DK, int NV>
+__device__ __forceinline__ void store_state(const LArgs &a, float *p, int col0, const f32x4 (&S)[DK / 16][NV])
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned dk = (unsigned)a.dk, dv = (unsigned)a.dv;
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const unsigned row = 16 * i + 4 * (lane >> 4) + r, c = col0 + 16 * (NV * wave + n) + (lane & 15);
+                if (row < dk && c < dv)
+                    p[row * dv + c] = S[i][n][r];
+            }
+    }
+}
+
+// S = exp(G_63) S + sum_s k_s (exp(G_63 - G_s) v_s)^T over the chunk in LDS.
+// k is exact in 16 bits; the decayed v is fp32 and goes in as three BF16 terms
+// (24 bits), or two FP16 terms after a power of two (22 bits), so the state
+// keeps fp32's accuracy on the matrix units.
+template <bool H, int DK, int NV, bool OUT>
+__device__ __forceinline__ void update_state(const unsigned short *lds, const Decays &d, f32x4 (&S)[DK / 16][NV])
+{
+    using L = Layout<DK, NV, OUT>;
+    constexpr int kTerms = H ? 2 : 3;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const unsigned short *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
+    const float total = d.total;
+    if constexpr (H) {
+        float x[2][NV][8], top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 4 * g]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 16 + 4 * g]);
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const u32x4 v = column_operand(vs, L::kVPitch, 16 * (NV * wave + n), j);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    float lo, hi;
+                    const unsigned int w = v[p];
+                    unpack2<H>(w, lo, hi);
+                    x[j][n][2 * p] = lo * (p < 2 ? w0[2 * p] : w1[2 * p - 4]);
+                    x[j][n][2 * p + 1] = hi * (p < 2 ? w0[2 * p + 1] : w1[2 * p - 3]);
+                    top = fmaxf(top, fmaxf(fabsf(x[j][n][2 * p]), fabsf(x[j][n][2 * p + 1])));
+                }
+            }
+        }
+        float mul, back;
+        half_range(wave_max(top), mul, back);
+        u32x4 f[2][NV][kTerms];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    x[j][n][p] *= mul;
+                split8<H, kTerms>(x[j][n], f[j][n]);
+            }
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i) {
+            if (i % 2 == 0)
+                __builtin_amdgcn_sched_barrier(0);
+            f32x4 add[NV];
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+                add[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x4 k = column_operand(ks, L::kKPitch, 16 * i, j);
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                    for (int m = 0; m < kTerms; ++m)
+                        add[n] = mma16<H>(k, f[j][n][m], add[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[i][n][r] = S[i][n][r] * total + add[n][r] * back;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[i][n][r] *= total;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 4 * g]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 16 + 4 * g]);
+            u32x4 f[NV][kTerms];
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const u32x4 v = column_operand(vs, L::kVPitch, 16 * (NV * wave + n), j);
+                float x[8];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    float lo, hi;
+                    const unsigned int w = v[p];
+                    unpack2<H>(w, lo, hi);
+                    x[2 * p] = lo * (p < 2 ? w0[2 * p] : w1[2 * p - 4]);
+                    x[2 * p + 1] = hi * (p < 2 ? w0[2 * p + 1] : w1[2 * p - 3]);
+                }
+                split8<H, kTerms>(x, f[n]);
+            }
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i) {
+                if (i % 4 == 0)
+                    __builtin_amdgcn_sched_barrier(0);
+                const u32x4 k = column_operand(ks, L::kKPitch, 16 * i, j);
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                    for (int m = 0; m < kTerms; ++m)
+                        S[i][n] = mma16<H>(k, f[n][m], S[i][n]);
+            }
+        }
+    }
+}
+
+// One part of a sequence for one head and 64 NV value columns.  OUT: outputs,
+// and the sequence's new state after its last part.  Otherwise: what the part
+// alone adds to the state, for the parts after it.
+template <bool H, int DK, int NV, bool OUT>
+__global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
+{
+    using L = Layout<DK, NV, OUT>;
+    extern __shared__ __align__(16) unsigned short lds[];
+    __shared__ Decays decays[2];
+    __shared__ float score_back[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
+    u32x4 *scores = reinterpret_cast<u32x4 *>(lds + L::kScores / 2);
+
+    // consecutive logical ids -- the column tiles of a head, the heads that
+    // share keys -- on one XCD, whose L2 then serves their common q and k
+    const unsigned xcd = blockIdx.x & 7u, turn = blockIdx.x >> 3, q8 = gridDim.x >> 3, r8 = gridDim.x & 7u;
+    const unsigned id = xcd * q8 + (xcd < r8 ? xcd : r8) + turn;
+    const int tile = (int)(id % (unsigned)a.col_tiles);
+    const unsigned hp = id / (unsigned)a.col_tiles;
+    const int head = (int)(hp % (unsigned)a.heads), place = (int)(hp / (unsigned)a.heads);
+
+    Place p;
+    if (!locate(a, place, p))
+        return;
+    const int parts = parts_of(p.len, a.part);
+    if (!OUT && p.part == parts - 1)
+        return;                                 // nothing follows it
+    const int t0 = p.part * a.part;
+    int n_tok = min(p.len - t0, a.part);
+    bool last = p.part == parts - 1;
+    if (OUT && a.multi && parts > 1) {
+        // a join that is no sum (see linear_join): the part before it goes on to the end
+        const int serial = a.ws_serial[(long long)p.seq * a.heads + head];
+        if (serial < p.part)
+            return;
+        if (serial == p.part) {
+            n_tok = p.len - t0;
+            last = true;
+        }
+    }
+    const int chunks = (n_tok + kChunk - 1) / kChunk;
+    const int col0 = tile * 64 * NV, cols = min(a.dv - col0, 64 * NV);
+    const int khead = head / a.share;
+    const int slot = slot_of(a, p.seq);
+
+    const long long tok = (long long)p.first + t0;
+    const unsigned short *qp = static_cast<const unsigned short *>(a.q) + tok * a.q_token + khead * a.q_head;
+    const unsigned short *kp = static_cast<const unsigned short *>(a.k) + tok * a.k_token + khead * a.k_head;
+    const unsigned short *vp = static_cast<const unsigned short *>(a.v) + tok * a.v_token + head * a.v_head + col0;
+    const float *gp = a.g + tok * a.g_token + head * a.g_head;
+    unsigned short *op = static_cast<unsigned short *>(a.out) + tok * a.out_token + head * a.out_head;
+    const long long ws_off = ((long long)place * a.heads + head) * a.dk * a.dv;
+
+    f32x4 S[DK / 16][NV];
+    if constexpr (OUT) {
+        const float *from = nullptr;
+        if (a.multi && parts > 1)
+            from = a.ws_state + ws_off;
+        else if (a.state_in && slot >= 0)
+            from = a.state_in + slot * a.in_slot + head * a.in_head;
+        load_state<DK, NV>(a, from, col0, S);
+    }
+
+    // the parts-only kernel takes a second, token by token, pass if its state is not finite
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        if constexpr (!OUT)
+            load_state<DK, NV>(a, nullptr, col0, S);
+        Tile<DK> tq, tk;
+        Tile<64 * NV> tv;
+        double sum = 0.0;
+        float gate = 0.0f;
+        if (chunks > 0) {
+            if constexpr (OUT)
+                tq.load(qp, a.q_token, n_tok, a.dk);
+            tk.load(kp, a.k_token, n_tok, a.dk);
+            tv.load(vp, a.v_token, n_tok, cols);
+            if (wave == 0) {
+                gate = lane < n_tok ? gp[lane * a.g_token] : 0.0f;
+                sum = chunk_decays(gate, decays[0]);
+                gate = kChunk + lane < n_tok ? gp[(kChunk + lane) * a.g_token] : 0.0f;
+            }
+        }
+        for (int c = 0; c < chunks; ++c) {
+            const int rows = min(n_tok - c * kChunk, kChunk);
+            const Decays &d = decays[c & 1];
+            if constexpr (OUT)
+                tq.store(qs, L::kQPitch);
+            tk.store(ks, L::kKPitch);
+            tv.store(vs, L::kVPitch);
+            __syncthreads();
+            if (c + 1 < chunks) {
+                const long long at = (long long)(c + 1) * kChunk;
+                const int left = n_tok - (c + 1) * kChunk;
+                if constexpr (OUT)
+                    tq.load(qp + at * a.q_token, a.q_token, left, a.dk);
+                tk.load(kp + at * a.k_token, a.k_token, left, a.dk);
+                tv.load(vp + at * a.v_token, a.v_token, left, cols);
+                if (wave == 0) {
+                    sum += chunk_decays(gate, decays[(c + 1) & 1]);
+                    gate = kChunk + lane < left ? gp[(at + kChunk + lane) * a.g_token] : 0.0f;
+                }
+            }
+            if constexpr (OUT) {
+                // masked, decayed scores of the 16 tokens 16 wave + l % 16 with the tokens up to them
+                {
+                    f32x4 sc[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < DK / 32; ++j) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        const u32x4 qf = row_operand(qs, L::kQPitch, 16 * wave, j);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i <= wave)
+                                sc[i] = mma16<H>(row_operand(ks, L::kKPitch, 16 * i, j), qf, sc[i]);
+                    }
+                    const int t = 16 * wave + (lane & 15);
+                    const float th = d.hi[t], tl = d.lo[t];
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i > wave)
+                            continue;
+                        const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * i + 4 * g]);
+                        const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * i + 4 * g]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const bool seen = 16 * i + 4 * g + r <= t;
+                            const float e = __builtin_amdgcn_exp2f((th - sh[r]) + (tl - sl[r]));
+                            sc[i][r] = seen ? sc[i][r] * e : 0.0f;
+                            top = fmaxf(top, fabsf(sc[i][r]));
+                        }
+                    }
+                    if constexpr (H) {
+                        float mul, back;
+                        half_range(wave_max(top), mul, back);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                sc[i][r] *= mul;
+                        if (lane == 0)
+                            score_back[wave] = back;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (2 * j > wave)
+                            continue;
+                        const float x[8] = {sc[2 * j][0], sc[2 * j][1], sc[2 * j][2], sc[2 * j][3],
+                                            sc[2 * j + 1][0], sc[2 * j + 1][1], sc[2 * j + 1][2], sc[2 * j + 1][3]};
+                        u32x4 f[2];
+                        split8<H, 2>(x, f);
+                        scores[(score_slot(wave, j) * 2 + 0) * 64 + lane] = f[0];
+                        scores[(score_slot(wave, j) * 2 + 1) * 64 + lane] = f[1];
+                    }
+                }
+                // S^T q of all 64 tokens, the state in two terms
+                f32x4 acc[4][NV];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+                        acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                float s_mul = 1.0f, s_back = 1.0f;
+                if constexpr (H) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+                        for (int n = 0; n < NV; ++n)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                top = fmaxf(top, fabsf(S[i][n][r]));
+                    half_range(wave_max(top), s_mul, s_back);
+                }
+#pragma unroll
+                for (int j = 0; j < DK / 32; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    u32x4 f[NV][2];
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) {
+                        float x[8];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            x[r] = S[2 * j][n][r];
+                            x[4 + r] = S[2 * j + 1][n][r];
+                        }
+                        if constexpr (H) {
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                x[r] *= s_mul;
+                        }
+                        split8<H, 2>(x, f[n]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const u32x4 qf = row_operand(qs, L::kQPitch, 16 * i, j);
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            acc[i][n] = mma16<H>(f[n][0], qf, acc[i][n]);
+                            acc[i][n] = mma16<H>(f[n][1], qf, acc[i][n]);
+                        }
+                    }
+                }
+                __syncthreads();
+                // + scores V
+                float back[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    back[i] = 1.0f;
+                    float f = d.grown[16 * i + (lane & 15)];
+                    if constexpr (H) {
+                        back[i] = score_back[i];
+                        f *= s_back / back[i];          // powers of two: exact
+                    }
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[i][n][r] *= f;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    u32x4 vf[NV];
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+                        vf[n] = column_operand(vs, L::kVPitch, 16 * (NV * wave + n), j);
+#pragma unroll
+                    for (int i = 2 * j; i < 4; ++i) {
+                        const u32x4 p0 = scores[(score_slot(i, j) * 2 + 0) * 64 + lane];
+                        const u32x4 p1 = scores[(score_slot(i, j) * 2 + 1) * 64 + lane];
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            acc[i][n] = mma16<H>(vf[n], p0, acc[i][n]);
+                            acc[i][n] = mma16<H>(vf[n], p1, acc[i][n]);
+                        }
+                    }
+                }
+                float odd = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            odd = fmaf(acc[i][n][r], 0.0f, odd);
+                unsigned short *o = op + (long long)c * kChunk * a.out_token;
+                if (wave_any_nan(odd)) {
+                    recur<H, DK, NV, OUT>(a, lds, d, rows, S, o, col0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = 16 * i + (lane & 15);
+                        const float f = a.scale * back[i];
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            const int col = col0 + 16 * (NV * wave + n) + 4 * g;
+                            if (t < rows && col < a.dv) {
+                                u32x2 w;
+                                w.x = to_bits<H>(acc[i][n][0] * f) | (unsigned)to_bits<H>(acc[i][n][1] * f) << 16;
+                                w.y = to_bits<H>(acc[i][n][2] * f) | (unsigned)to_bits<H>(acc[i][n][3] * f) << 16;
+                                *reinterpret_cast<u32x2 *>(o + t * a.out_token + col) = w;
+                            }
+                        }
+                    }
+                    update_state<H, DK, NV, OUT>(lds, d, S);
+                }
+            } else {
+                if (attempt)
+                    recur<H, DK, NV, OUT>(a, lds, d, rows, S, nullptr, col0);
+                else
+                    update_state<H, DK, NV, OUT>(lds, d, S);
+            }
+            __syncthreads();
+        }
+        if constexpr (OUT)
+            break;
+        float odd = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    odd = fmaf(S[i][n][r], 0.0f, odd);
+        if (threadIdx.x == 0 && tile == 0) {
+            a.ws_decay[(long long)place * a.heads + head] = sum;
+            if (p.part == 0)
+                a.ws_serial[(long long)p.seq * a.heads + head] = 0x7FFFFFFF;
+        }
+        if (!__syncthreads_or(odd != 0.0f))
+            break;
+    }
+    if constexpr (OUT) {
+        if (last && a.state_out && slot >= 0)
+            store_state<DK, NV>(a, a.state_out + slot * a.so_slot + head * a.so_head, col0, S);
+    } else {
+        store_state<DK, NV>(a, a.ws_state + ws_off, col0, S);
+    }
+}
+
+// State at the start of every part of the sequences that have several:
+// S_0 = the old state, S_{j+1} = exp(G of part j) S_j + what part j adds.
+// That is the recurrence only while the factor is finite, and not 0 on a state
+// that is not: exp(g) (S + a) is neither inf S + inf a nor, where exp(G) has
+// underflowed, 0 * inf.  Such a part takes the rest of its sequence in one go instead (ws_serial).
+__global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
+{
+    const int head = blockIdx.y, seq = blockIdx.z;
+    Place p;
+    const int place0 = first_place(a.starts[seq], a.tokens, a.part, seq);
+    place_of(a.starts[seq], a.starts[seq + 1], a.tokens, a.part, place0, seq, p);
+    const int parts = parts_of(p.len, a.part);
+    const int at = (blockIdx.x * kThreads + threadIdx.x) * 4, size = a.dk * a.dv;
+    if (parts < 2 || at >= size)
+        return;
+    const int slot = slot_of(a, seq);
+    f32x4 S = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.state_in && slot >= 0)
+        S = *reinterpret_cast<const f32x4 *>(a.state_in + slot * a.in_slot + head * a.in_head + at);
+    for (int j = 0; j < parts; ++j) {
+        const long long ph = (long long)(place0 + j) * a.heads + head;
+        float *w = a.ws_state + ph * size + at;
+        f32x4 add = S;
+        float f = 0.0f;
+        if (j + 1 < parts) {
+            add = *reinterpret_cast<const f32x4 *>(w);
+            f = __builtin_amdgcn_exp2f((float)a.ws_decay[ph]);
+            const float odd = fmaf(S[0], 0.0f, 0.0f) + fmaf(S[1], 0.0f, 0.0f) + fmaf(S[2], 0.0f, 0.0f) +
+                              fmaf(S[3], 0.0f, 0.0f);
+            if (!(f < INFINITY) || (f == 0.0f && odd != 0.0f))
+                atomicMin(&a.ws_serial[(long long)seq * a.heads + head], j);
+        }
+        *reinterpret_cast<f32x4 *>(w) = S;
+        S = S * f + add;
+    }
+}
+
+// One new token of each sequence.  A workgroup takes 32 value columns of one
+// (sequence, head): 8 threads of four columns by 32 rows of the state, so that
+// every load of the state is under way at once and a single sequence still
+// gives several workgroups a head.  Bound by the state's bytes, 8 dk dv a head.
+template <bool H>
+__global__ __launch_bounds__(kThreads, 4) void linear_step(LArgs a)
+{
+    __shared__ f32x4 part[4][8];
+    const int head = blockIdx.y, seq = blockIdx.z;
+    const int cq = threadIdx.x & 7, row0 = threadIdx.x >> 3, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned col = blockIdx.x * 32 + 4 * cq, dv = (unsigned)a.dv;
+    const int khead = head / a.share, slot = slot_of(a, seq);
+    const bool live = col < dv;
+    const unsigned short *q = static_cast<const unsigned short *>(a.q) + seq * a.q_token + khead * a.q_head;
+    const unsigned short *k = static_cast<const unsigned short *>(a.k) + seq * a.k_token + khead * a.k_head;
+    const unsigned short *v = static_cast<const unsigned short *>(a.v) + seq * a.v_token + head * a.v_head;
+    const float *in = slot >= 0 && a.state_in ? a.state_in + slot * a.in_slot + head * a.in_head : nullptr;
+    float *so = slot >= 0 && a.state_out ? a.state_out + slot * a.so_slot + head * a.so_head : nullptr;
+    constexpr int kRows = 8;                    // dk <= 256: at most 8 rows a thread
+    f32x4 S[kRows];
+    float kk[kRows], qq[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const unsigned row = row0 + 32 * i;
+        S[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        kk[i] = qq[i] = 0.0f;
+        if (row < (unsigned)a.dk && live) {
+            if (in)
+                S[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(in + (row * dv + col)));
+            kk[i] = to_float<H>(k[row]);
+            qq[i] = to_float<H>(q[row]);
+        }
+    }
+    const float e = expf(a.g[seq * a.g_token + head * a.g_head]);
+    f32x4 vv = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, o = vv;
+    if (live) {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(v + col);
+        const unsigned int w0 = w.x, w1 = w.y;
+        float x0, x1, x2, x3;
+        unpack2<H>(w0, x0, x1);
+        unpack2<H>(w1, x2, x3);
+        vv = f32x4{x0, x1, x2, x3};
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const unsigned row = row0 + 32 * i;
+        if (row < (unsigned)a.dk && live) {
+            S[i] = S[i] * e + kk[i] * vv;
+            o += qq[i] * S[i];
+            if (so)
+                __builtin_nontemporal_store(S[i], reinterpret_cast<f32x4 *>(so + (row * dv + col)));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float x = o[r];
+        x += __shfl_xor(x, 8, 64);
+        x += __shfl_xor(x, 16, 64);
+        x += __shfl_xor(x, 32, 64);
+        o[r] = x;
+    }
+    if (lane < 8)
+        part[wave][lane] = o;
+    __syncthreads();
+    if (threadIdx.x < 8 && live) {
+        const f32x4 s = ((part[0][cq] + part[1][cq]) + (part[2][cq] + part[3][cq])) * a.scale;
+        u32x2 w;
+        w.x = to_bits<H>(s[0]) | (unsigned)to_bits<H>(s[1]) << 16;
+        w.y = to_bits<H>(s[2]) | (unsigned)to_bits<H>(s[3]) << 16;
+        *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + seq * a.out_token + head * a.out_head +
+                                   col) = w;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Launch shape of a prompt, from its sizes alone.
+struct Shape {
+    int nv, col_tiles, part, places, multi;
+};
+
+constexpr int kMinPart = 256;
+
+Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
+{
+    Shape s;
+    s.nv = dk > 128 || dv <= 64 || (dv > 128 && dv <= 192) ? 1 : 2;
+    s.col_tiles = (dv + 64 * s.nv - 1) / (64 * s.nv);
+    const long long units = (long long)heads * s.col_tiles;
+    long long part = ((long long)tokens * units + 511) / 512;
+    part = (part + kChunk - 1) / kChunk * kChunk;
+    if (part < kMinPart)
+        part = kMinPart;
+    s.multi = part < tokens;
+    if (!s.multi)                               // past every start: sequence i is place i
+        part = ((long long)tokens / kChunk + 1) * kChunk;
+    s.part = (int)part;
+    s.places = tokens / s.part + sequences;
+    return s;
+}
+
+size_t state_bytes(const Shape &s, int heads, int dk, int dv)
+{
+    return s.multi ? (size_t)s.places * heads * dk * dv * sizeof(float) : 0;
+}
+
+size_t decay_bytes(const Shape &s, int heads) { return (size_t)s.places * heads * sizeof(double); }
+
+size_t workspace_of(const Shape &s, int sequences, int heads, int dk, int dv)
+{
+    return s.multi ? state_bytes(s, heads, dk, dv) + decay_bytes(s, heads) + (size_t)sequences * heads * sizeof(int)
+                   : 0;
+}
+
+hipError_t launch_one(void (*fn)(LArgs), dim3 grid, size_t lds, const LArgs &a, hipStream_t stream)
+{
+    LArgs copy = a;
+    void *params[] = {&copy};
+    return hipLaunchKernel(reinterpret_cast<const void *>(fn), grid, dim3(kThreads), params, lds, stream);
+}
+
+template <bool H, int DK, int NV>
+hipError_t launch_prompt(const LArgs &a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((long long)a.places * a.heads * a.col_tiles));
+    hipError_t e = hipSuccess;
+    if (a.multi) {
+        e = launch_one(linear_chunks<H, DK, NV, false>, grid, Layout<DK, NV, false>::kBytes, a, stream);
+        const dim3 jg((unsigned)((a.dk * a.dv / 4 + kThreads - 1) / kThreads), (unsigned)a.heads,
+                      (unsigned)a.sequences);
+        if (e == hipSuccess)
+            e = launch_one(linear_join, jg, 0, a, stream);
+    }
+    if (e == hipSuccess)
+        e = launch_one(linear_chunks<H, DK, NV, true>, grid, Layout<DK, NV, true>::kBytes, a, stream);
+    return e;
+}
+
+template <bool H>
+hipError_t launch_prompt_type(const LArgs &a, int nv, hipStream_t stream)
+{
+    if (a.dk > 128)
+        return launch_prompt<H, 256, 1>(a, stream);
+    if (a.dk > 64)
+        return nv == 2 ? launch_prompt<H, 128, 2>(a, stream) : launch_prompt<H, 128, 1>(a, stream);
+    if (a.dk > 32)
+        return nv == 2 ? launch_prompt<H, 64, 2>(a, stream) : launch_prompt<H, 64, 1>(a, stream);
+    return nv == 2 ? launch_prompt<H, 32, 2>(a, stream) : launch_prompt<H, 32, 1>(a, stream);
+}
+
+// Kernels that need more than the default 64 KiB of dynamic LDS.
+template <bool H>
+void raise_limits()
+{
+    const auto set = [](const void *fn, int bytes) {
+        (void)hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    set(reinterpret_cast<const void *>(linear_chunks<H, 128, 2, true>), Layout<128, 2, true>::kBytes);
+    set(reinterpret_cast<const void *>(linear_chunks<H, 256, 1, true>), Layout<256, 1, true>::kBytes);
+}
+
+constexpr long long kMaxTokenStride = 1 << 24;
+
+skinny_status bad(skinny_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+skinny_status bad(skinny_status s, const char *fmt, ...)
+{
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_error("%s", buf);
+    return s;
+}
+
+skinny_status check_linear(const skinny_linear_args *p, bool prompt)
+{
+    if (!p)
+        return bad(SKINNY_ERR_INVALID_ARG, "args is NULL");
+    if (p->type != SKINNY_IN_BF16 && p->type != SKINNY_IN_F16)
+        return bad(SKINNY_ERR_INVALID_ARG, "type %d is neither BF16 nor FP16", p->type);
+    if (p->tokens < 0 || p->sequences < 0 || p->pool < 0)
+        return bad(SKINNY_ERR_INVALID_ARG, "tokens=%d, sequences=%d and pool=%d must not be negative", p->tokens,
+                   p->sequences, p->pool);
+    if (p->heads < 1 || p->heads > 65535 || p->key_heads < 1 || p->heads % p->key_heads)
+        return bad(SKINNY_ERR_SHAPE, "heads=%d must be 1..65535 and a multiple of key_heads=%d", p->heads,
+                   p->key_heads);
+    if (p->sequences > 65535)
+        return bad(SKINNY_ERR_SHAPE, "sequences=%d: at most 65535", p->sequences);
+    if (p->dk < 8 || p->dk > 256 || p->dk % 8 || p->dv < 8 || p->dv > 1024 || p->dv % 8)
+        return bad(SKINNY_ERR_SHAPE, "dk=%d and dv=%d must be multiples of 8, dk <= 256, dv <= 1024", p->dk, p->dv);
+    if (!prompt && p->tokens != p->sequences)
+        return bad(SKINNY_ERR_SHAPE, "a step has one token a sequence: tokens=%d, sequences=%d", p->tokens,
+                   p->sequences);
+    if (p->tokens > 0 && (!p->q || !p->k || !p->v || !p->log_decay || !p->out))
+        return bad(SKINNY_ERR_INVALID_ARG, "q, k, v, log_decay or out is NULL");
+    if (prompt && p->sequences > 0 && !p->starts)
+        return bad(SKINNY_ERR_INVALID_ARG, "starts is NULL");
+    if (prompt && p->sequences == 0 && p->tokens > 0)
+        return bad(SKINNY_ERR_SHAPE, "%d tokens but no sequence", p->tokens);
+    if (!p->slots && (p->state_in || p->state_out) && p->pool < p->sequences)
+        return bad(SKINNY_ERR_SHAPE, "pool=%d holds fewer states than sequences=%d", p->pool, p->sequences);
+    const long long token[] = {p->q_token, p->k_token, p->v_token, p->out_token};
+    const long long per_head[] = {p->q_head, p->k_head, p->v_head, p->out_head};
+    static const char *const names[] = {"q", "k", "v", "out"};
+    const void *const ptr[] = {p->q, p->k, p->v, p->out};
+    for (int i = 0; i < 4; ++i) {
+        if (token[i] % 8 || per_head[i] % 8 || token[i] < 0 || per_head[i] < 0 || token[i] >= kMaxTokenStride)
+            return bad(SKINNY_ERR_SHAPE, "%s strides (%lld, %lld) must be multiples of 8 in [0, 2^24)", names[i],
+                       token[i], per_head[i]);
+        if ((uintptr_t)ptr[i] & 15)
+            return bad(SKINNY_ERR_ALIGN, "%s must be 16-byte aligned", names[i]);
+    }
+    if (p->decay_token < 0 || p->decay_head < 0)
+        return bad(SKINNY_ERR_SHAPE, "log_decay strides must not be negative");
+    if (((uintptr_t)p->log_decay & 3) || ((uintptr_t)p->starts & 3) || ((uintptr_t)p->slots & 3))
+        return bad(SKINNY_ERR_ALIGN, "log_decay, starts and slots must be 4-byte aligned");
+    if (((uintptr_t)p->state_in & 15) || ((uintptr_t)p->state_out & 15))
+        return bad(SKINNY_ERR_ALIGN, "state_in and state_out must be 16-byte aligned");
+    if (p->in_state_slot % 4 || p->in_state_head % 4 || p->out_state_slot % 4 || p->out_state_head % 4 || p->in_state_slot < 0 ||
+        p->in_state_head < 0 || p->out_state_slot < 0 || p->out_state_head < 0)
+        return bad(SKINNY_ERR_SHAPE, "state strides must be multiples of 4 and not negative");
+    return SKINNY_OK;
+}
+
+LArgs kernel_args(const skinny_linear_args *p)
+{
+    LArgs a{};
+    a.q = p->q;
+    a.k = p->k;
+    a.v = p->v;
+    a.out = p->out;
+    a.g = p->log_decay;
+    a.state_in = p->state_in;
+    a.state_out = p->state_out;
+    a.starts = p->starts;
+    a.slots = p->slots;
+    a.q_token = p->q_token;
+    a.q_head = p->q_head;
+    a.k_token = p->k_token;
+    a.k_head = p->k_head;
+    a.v_token = p->v_token;
+    a.v_head = p->v_head;
+    a.out_token = p->out_token;
+    a.out_head = p->out_head;
+    a.g_token = p->decay_token;
+    a.g_head = p->decay_head;
+    a.in_slot = p->in_state_slot;
+    a.in_head = p->in_state_head;
+    a.so_slot = p->out_state_slot;
+    a.so_head = p->out_state_head;
+    a.tokens = p->tokens;
+    a.sequences = p->sequences;
+    a.heads = p->heads;
+    a.share = p->heads / p->key_heads;
+    a.dk = p->dk;
+    a.dv = p->dv;
+    a.pool = p->pool;
+    a.scale = p->scale;
+    return a;
+}
+
+skinny_status launched(hipError_t e)
+{
+    return e == hipSuccess ? SKINNY_OK : bad(SKINNY_ERR_HIP, "linear attention launch: %s", hipGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace skinny
+
+using namespace skinny;
+
+extern "C" {
+
+size_t skinny_linear_workspace(int tokens, int sequences, int heads, int dk, int dv)
+{
+    if (tokens < 0 || sequences < 0 || heads < 1 || dk < 8 || dk > 256 || dv < 8 || dv > 1024)
+        return 0;
+    return workspace_of(shape_of(tokens, sequences, heads, dk, dv), sequences, heads, dk, dv);
+}
+
+skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
+{
+    skinny_status st = check_linear(p, true);
+    if (st != SKINNY_OK)
+        return st;
+    if (p->sequences == 0)
+        return SKINNY_OK;
+    const Shape s = shape_of(p->tokens, p->sequences, p->heads, p->dk, p->dv);
+    if ((long long)s.places * p->heads * s.col_tiles > 0x7FFFFFFFLL)
+        return bad(SKINNY_ERR_SHAPE, "tokens=%d, sequences=%d and heads=%d are too many for one call", p->tokens,
+                   p->sequences, p->heads);
+    const size_t need = workspace_of(s, p->sequences, p->heads, p->dk, p->dv);
+    if (need && (!p->workspace || p->workspace_bytes < need))
+        return bad(SKINNY_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu are needed",
+                   p->workspace ? p->workspace_bytes : (size_t)0, need);
+    if (need && ((uintptr_t)p->workspace & 15))
+        return bad(SKINNY_ERR_ALIGN, "workspace must be 16-byte aligned");
+    LArgs a = kernel_args(p);
+    a.part = s.part;
+    a.places = s.places;
+    a.col_tiles = s.col_tiles;
+    a.multi = s.multi;
+    if (s.multi) {
+        char *ws = static_cast<char *>(p->workspace);
+        a.ws_state = reinterpret_cast<float *>(ws);
+        a.ws_decay = reinterpret_cast<double *>(ws += state_bytes(s, p->heads, p->dk, p->dv));
+        a.ws_serial = reinterpret_cast<int *>(ws + decay_bytes(s, p->heads));
+    }
+    static const bool raised = (raise_limits<false>(), raise_limits<true>(), true);
+    (void)raised;
+    return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s.nv, (hipStream_t)stream)
+                                             : launch_prompt_type<false>(a, s.nv, (hipStream_t)stream));
+}
+
+skinny_status skinny_linear_step(const skinny_linear_args *p, void *stream)
+{
+    skinny_status st = check_linear(p, false);
+    if (st != SKINNY_OK)
+        return st;
+    if (p->sequences == 0)
+        return SKINNY_OK;
+    const LArgs a = kernel_args(p);
+    const dim3 grid((unsigned)((a.dv + 31) / 32), (unsigned)a.heads, (unsigned)a.sequences);
+    return launched(launch_one(p->type == SKINNY_IN_F16 ? linear_step<true> : linear_step<false>, grid, 0, a,
+                               (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -327,7 +327,9 @@ void set_call_args(KArgs &a, const void *x, int ldx, const void *residual, int l
     a.ldr = residual ? ldr : ldo;
 }
 
-skinny_status current_gfx950(int *dev, int *cus)
+}  // namespace
+
+skinny_status skinny::current_gfx950(int *dev, int *cus)
 {
     int count = 0;
     if (hipGetDeviceCount(&count) != hipSuccess || count == 0) {
@@ -344,6 +346,8 @@ skinny_status current_gfx950(int *dev, int *cus)
     *cus = prop.multiProcessorCount;
     return SKINNY_OK;
 }
+
+namespace {
 
 struct DevBuf {
     void *p = nullptr;

@@ -103,6 +103,9 @@ size_t tactic_lds_bytes(const skinny_tactic &t, int K8);
 // Thread-local error text.
 void set_error(const char *fmt, ...);
 
+// The current device and its CU count, or an error if it is not a gfx950.
+skinny_status current_gfx950(int *dev, int *cus);
+
 // Stored tuned tables (tables.cpp): one text line per (chip, N, K, input and
 // output type, residual or not: res = 1 for the table of runs that add a
 // residual).  parse_table_line fills `table` and returns true only for a

@@ -1,0 +1,145 @@
+"""Linear attention with a decay for each head and token.
+
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T,    o_t = scale q_t^T S_t
+
+for every head, over packed sequences of prompts (``prompt``: chunks on the
+matrix units, long sequences split over the chip) or for one new token of each
+sequence (``step``).  The states stay in a pool of fp32 [dk, dv] matrices, one
+[heads, dk, dv] slot a sequence.  q, k, v and out are views with a contiguous
+last dimension, so the column ranges of a packed projection's output can be
+passed in place.  Argument marshalling only: the kernels are in
+csrc/linear_attention.hip.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import IN_BF16, IN_F16, _raise, load_library, stream_handle
+
+_TYPES = {torch.bfloat16: IN_BF16, torch.float16: IN_F16}
+_P, _LL, _I = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int
+
+
+class _Args(ctypes.Structure):
+    _fields_ = ([(n, _P) for n in ("q", "k", "v", "out", "log_decay", "state_in", "state_out", "starts", "slots",
+                                   "workspace")] + [("workspace_bytes", ctypes.c_size_t)] +
+                [(n, _LL) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head", "out_token",
+                                    "out_head", "decay_token", "decay_head", "in_state_slot", "in_state_head",
+                                    "out_state_slot", "out_state_head")] +
+                [(n, _I) for n in ("type", "tokens", "sequences", "heads", "key_heads", "dk", "dv", "pool")] +
+                [("scale", ctypes.c_float)])
+
+
+def workspace_bytes(tokens: int, sequences: int, heads: int, dk: int, dv: int) -> int:
+    """Bytes of workspace a prompt call of these sizes needs (may be 0)."""
+    return load_library().skinny_linear_workspace(tokens, sequences, heads, dk, dv)
+
+
+def _state(name, t, heads, dk, dv, device):
+    if t.dtype != torch.float32 or t.dim() != 4 or tuple(t.shape[1:]) != (heads, dk, dv):
+        raise ValueError(f"{name} must be torch.float32 [pool, {heads}, {dk}, {dv}], got {tuple(t.shape)} {t.dtype}")
+    slot, head, row, unit = t.stride()
+    if unit != 1 or row != dv:
+        raise ValueError(f"{name}'s [dk, dv] matrices must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    return slot, head
+
+
+def _ints(name, t, count, device):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != count or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous torch.int32 [{count}], got {tuple(t.shape)} {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    return t.data_ptr()
+
+
+def _call(entry, q, k, v, log_decay, out, sequences, starts, state_in, state_out, slots, scale, workspace, stream):
+    kind = _TYPES.get(v.dtype)
+    device = v.device
+    if kind is None or v.dim() != 3 or device.type != "cuda":
+        raise ValueError("v must be a BF16 or FP16 [tokens, heads, dv] tensor on a GPU")
+    tokens, heads, dv = v.shape
+    if q.dim() != 3 or q.shape[0] != tokens or k.shape != q.shape:
+        raise ValueError(f"q and k must be [{tokens}, key_heads, dk] alike, got {tuple(q.shape)} and {tuple(k.shape)}")
+    key_heads, dk = q.shape[1:]
+    if out.shape != v.shape:
+        raise ValueError(f"out must have v's shape {tuple(v.shape)}, got {tuple(out.shape)}")
+    if log_decay.dtype != torch.float32 or log_decay.shape != (tokens, heads):
+        raise ValueError(f"log_decay must be torch.float32 [{tokens}, {heads}], got {tuple(log_decay.shape)} "
+                         f"{log_decay.dtype}")
+    qt, qh, qu = q.stride()
+    kt, kh, ku = k.stride()
+    vt, vh, vu = v.stride()
+    ot, oh, ou = out.stride()
+    if qu != 1 or ku != 1 or vu != 1 or ou != 1:
+        raise ValueError("q, k, v and out must have a contiguous last dimension")
+    if q.dtype != v.dtype or k.dtype != v.dtype or out.dtype != v.dtype:
+        raise ValueError(f"q, k, v and out must have one type, got {q.dtype}, {k.dtype}, {v.dtype} and {out.dtype}")
+    if q.device != device or k.device != device or out.device != device or log_decay.device != device:
+        raise ValueError("q, k, v, out and log_decay must be on the same device")
+    pool = 0
+    ip = op = slot_ptr = start_ptr = None
+    i_slot = i_head = o_slot = o_head = 0
+    if state_in is not None:
+        i_slot, i_head = _state("state_in", state_in, heads, dk, dv, device)
+        ip, pool = state_in.data_ptr(), state_in.shape[0]
+    if state_out is not None:
+        o_slot, o_head = _state("state_out", state_out, heads, dk, dv, device)
+        if ip is not None and state_out.shape[0] != pool:
+            raise ValueError(f"state_in and state_out hold {pool} and {state_out.shape[0]} states")
+        op, pool = state_out.data_ptr(), state_out.shape[0]
+    if slots is not None:
+        slot_ptr = _ints("slots", slots, sequences, device)
+    if starts is not None:
+        start_ptr = _ints("starts", starts, sequences + 1, device)
+    wp, wb = None, 0
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the same device")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if scale is None:
+        scale = dk ** -0.5
+    if tokens <= 1:                     # the strides of a single token say nothing
+        qt = kt = vt = ot = 0
+    args = _Args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(), ip, op, start_ptr,
+                 slot_ptr, wp, wb, qt, qh, kt, kh, vt, vh, ot, oh, *log_decay.stride(), i_slot, i_head, o_slot,
+                 o_head, kind, tokens, sequences, heads, key_heads, dk, dv, pool, scale)
+    _raise(entry(ctypes.byref(args), stream_handle(stream, device)))
+
+
+def prompt(q, k, v, log_decay, out, starts, state_in=None, state_out=None, slots=None, scale=None, workspace=None,
+           stream=None):
+    """out[t] = scale q_t^T S_t over packed sequences, on the current (or given) stream; returns out.
+
+    q, k [tokens, key_heads, dk]; v, out [tokens, heads, dv]; BF16 or FP16,
+    dk <= 256 and dv <= 1024 multiples of 8, any strides that are multiples of 8
+    elements on 16-byte aligned tensors.  log_decay fp32 [tokens, heads], at
+    most 0.  starts int32 [sequences + 1] on the GPU: sequence i has the
+    tokens starts[i] .. starts[i + 1] (none is allowed).  state_in (None: zero)
+    and state_out (None: not kept; may be state_in) are fp32 [pool, heads, dk,
+    dv]; slots int32 [sequences] names each sequence's state, all different
+    (None: 0, 1, ...); a slot outside the pool is no state.  scale: dk ** -0.5
+    if None.  workspace: a tensor of at least workspace_bytes(...) bytes, which
+    must not serve two calls at once; None allocates one for the call."""
+    if starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must be int32 [sequences + 1]")
+    sequences = starts.shape[0] - 1
+    if workspace is None and v.dim() == 3 and q.dim() == 3:
+        need = workspace_bytes(v.shape[0], sequences, v.shape[1], q.shape[2], v.shape[2])
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+            if stream is not None and hasattr(stream, "cuda_stream"):
+                workspace.record_stream(stream)
+    _call(load_library().skinny_linear_prompt, q, k, v, log_decay, out, sequences, starts, state_in, state_out,
+          slots, scale, workspace, stream)
+    return out
+
+
+def step(q, k, v, log_decay, out, state_in=None, state_out=None, slots=None, scale=None, stream=None):
+    """One new token of each sequence: prompt's arguments with tokens == sequences and no starts; returns out."""
+    _call(load_library().skinny_linear_step, q, k, v, log_decay, out, v.shape[0], None, state_in, state_out, slots,
+          scale, None, stream)
+    return out
