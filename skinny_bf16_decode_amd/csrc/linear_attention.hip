@@ -91,17 +91,28 @@ __device__ __forceinline__ unsigned short to_bits(float v)
 }
 
 template <bool H>
+__device__ __forceinline__ unsigned int pack2(float a, float b)
+{
+    if constexpr (H) {
+        typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+        return __builtin_bit_cast(unsigned int, f16x2{(_Float16)a, (_Float16)b});
+    } else {
+        typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+        return __builtin_bit_cast(unsigned int, bf16x2{(__bf16)a, (__bf16)b});
+    }
+}
+
+template <bool H>
 __device__ __forceinline__ void unpack2(unsigned int w, float &lo, float &hi)
 {
     lo = to_float<H>((unsigned short)(w & 0xFFFFu));
     hi = to_float<H>((unsigned short)(w >> 16));
 }
 
-__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
-
-// Two fp32 values as the sum of TERMS pairs of 16-bit values.  BF16 (8 bits a
-// term, cut off, so that what is left is exact): 16 bits for two terms, all 24
-// for three.  FP16 (11 bits a term, the caller scales into its range): 22 bits.
+// Two fp32 values as the sum of TERMS pairs of 16-bit values, each term the
+// rounded rest, which is exact.  BF16 (8 bits and a sign a term): 17 bits for
+// two terms, all 24 for three.  FP16 (the caller scales into its range; terms
+// cut off, the form that takes two values at once): 22 bits.
 template <bool H, int TERMS>
 __device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[TERMS])
 {
@@ -110,12 +121,18 @@ __device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[TERMS
         if constexpr (H) {
             const auto p = __builtin_amdgcn_cvt_pkrtz(a, b);
             w[i] = __builtin_bit_cast(unsigned int, p);
-            a -= (float)p[0];
-            b -= (float)p[1];
+            if (i + 1 < TERMS) {
+                a -= (float)p[0];
+                b -= (float)p[1];
+            }
         } else {
-            w[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-            a -= cut(a);
-            b -= cut(b);
+            typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+            const bf16x2 p = {(__bf16)a, (__bf16)b};
+            w[i] = __builtin_bit_cast(unsigned int, p);
+            if (i + 1 < TERMS) {
+                a -= __uint_as_float(w[i] << 16);
+                b -= __uint_as_float(w[i] & 0xFFFF0000u);
+            }
         }
     }
 }
@@ -191,6 +208,17 @@ __device__ __forceinline__ int slot_of(const LArgs &a, int seq)
     return s >= 0 && s < a.pool ? s : -1;
 }
 
+// A buffer load whose offset is past its resource reads zero and touches no
+// memory, a store writes none: rows and columns to be left out take kSkip as
+// their offset, so that loads and stores need no branches.  Offsets inside a
+// chunk stay below it: 63 rows at strides below 2^24 elements of 2 bytes.
+constexpr unsigned kSkip = 0x7FF00000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)kSkip, 0x00020000);
+}
+
 // A tile of 64 token rows of COLS 16-bit columns on its way from global memory
 // through registers to LDS.  Rows from `rows` on and columns from `cols` on
 // are zero.
@@ -200,17 +228,22 @@ struct Tile {
     static constexpr int kVecs = kChunk * kPerRow / kThreads;
     static constexpr int kRowStep = kThreads / kPerRow;
     u32x4 r[kVecs];
+    unsigned off, step;         // byte offset of the first vector, bytes between vectors
 
-    __device__ __forceinline__ void load(const unsigned short *base, long long stride, int rows, int cols)
+    __device__ __forceinline__ void init(long long stride, int cols)
     {
         const int row = threadIdx.x / kPerRow, col = (threadIdx.x % kPerRow) * 8;
-        const unsigned off = (unsigned)(row * (int)stride + col);     // strides are below 2^24
+        off = col < cols ? (unsigned)row * (unsigned)(2 * stride) + 2 * col : kSkip;
+        step = kRowStep * (unsigned)(2 * stride);
+    }
+
+    __device__ __forceinline__ void load(const unsigned short *base, int rows)
+    {
+        const __amdgpu_buffer_rsrc_t src = make_rsrc(base);
+        const int row = threadIdx.x / kPerRow;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const unsigned short *p = base + (long long)i * kRowStep * stride;
-            r[i] = u32x4{0u, 0u, 0u, 0u};
-            if (row + i * kRowStep < rows && col < cols)
-                r[i] = *reinterpret_cast<const u32x4 *>(p + off);
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(src, row + i * kRowStep < rows ? off : kSkip, i * step, 0);
         }
     }
 
@@ -303,27 +336,33 @@ struct Layout {
 // The recurrence token by token, as it is defined, for one wave's columns of a
 // chunk in LDS: used where a value is not finite, since 0 * inf in a product
 // over masked tokens, or in a split into terms, would spread NaN to outputs
-// that the definition leaves alone.
+// that the definition leaves alone.  The state is indexed at run time and so
+// goes through memory: the path is rare, and as registers it made the common
+// one spill (32768 tokens of 12 heads of 128: 532 us, 310 without it).
 template <bool H, int DK, int NV, bool OUT>
 __device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds, const Decays &d, int rows,
-                                   f32x4 (&S)[DK / 16][NV], unsigned short *out, int col0)
+                                      f32x4 (&S)[DK / 16][NV], unsigned short *out, int col0)
 {
     using L = Layout<DK, NV, OUT>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
+    f32x4 T[DK / 16][NV];
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+            T[i][n] = S[i][n];
+#pragma unroll 1
     for (int t = 0; t < rows; ++t) {
         const float e = d.own[t];
-        int dk = a.dk;
-        asm volatile("" : "+s"(dk));                // compared anew: 4 DK / 16 lane masks are not kept over the loop
         float v[NV], o[NV];
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             v[n] = to_float<H>(vs[t * L::kVPitch + 16 * (NV * wave + n) + (lane & 15)]);
             o[n] = 0.0f;
         }
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < DK / 16; ++i) {
-            __builtin_amdgcn_sched_barrier(0);      // few loads in flight: the path is rare, registers are not
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int c = 16 * i + 4 * g + r;
@@ -334,10 +373,10 @@ __device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds,
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     // columns past dk hold no state: 0 * a non-finite v is not theirs to add
-                    const float s = c < dk ? S[i][n][r] * e + k * v[n] : 0.0f;
-                    S[i][n][r] = s;
+                    const float s = c < a.dk ? T[i][n][r] * e + k * v[n] : 0.0f;
+                    T[i][n][r] = s;
                     if constexpr (OUT)
-                        o[n] += c < dk ? q * s : 0.0f;
+                        o[n] += c < a.dk ? q * s : 0.0f;
                 }
             }
         }
@@ -353,44 +392,63 @@ __device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds,
             }
         }
     }
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+            S[i][n] = T[i][n];
 }
 
-// Natural [dk][dv] state <-> result registers of the wave's columns.
+// Natural [dk][dv] state <-> result registers of the wave's columns.  Lane
+// group g holds rows 4 g .. 4 g + 3 of each 16; dk is a multiple of 8, so the
+// four are all in or all out.
 template <int DK, int NV>
 __device__ __forceinline__ void load_state(const LArgs &a, const float *p, int col0, f32x4 (&S)[DK / 16][NV])
 {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const unsigned dk = (unsigned)a.dk, dv = (unsigned)a.dv;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const __amdgpu_buffer_rsrc_t src = make_rsrc(p);
+    const unsigned pitch = 4u * (unsigned)a.dv;
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
+    for (int n = 0; n < NV; ++n) {
+        const int c = col0 + 16 * (NV * wave + n) + (lane & 15);
+        const unsigned off = p && c < a.dv ? 4u * g * pitch + 4u * c : kSkip;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+        for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const unsigned row = 16 * i + 4 * (lane >> 4) + r, c = col0 + 16 * (NV * wave + n) + (lane & 15);
-                S[i][n][r] = p && row < dk && c < dv ? p[row * dv + c] : 0.0f;
-            }
+            for (int r = 0; r < 4; ++r)
+                S[i][n][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                    src, 16 * i + 4 * g < a.dk ? off : kSkip, (unsigned)(16 * i + r) * pitch, 0));
     }
 }
 
 template <int DK, int NV>
 __device__ __forceinline__ void store_state(const LArgs &a, float *p, int col0, const f32x4 (&S)[DK / 16][NV])
 {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const unsigned dk = (unsigned)a.dk, dv = (unsigned)a.dv;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const __amdgpu_buffer_rsrc_t dst = make_rsrc(p);
+    const unsigned pitch = 4u * (unsigned)a.dv;
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
+    for (int n = 0; n < NV; ++n) {
+        const int c = col0 + 16 * (NV * wave + n) + (lane & 15);
+        const unsigned off = c < a.dv ? 4u * g * pitch + 4u * c : kSkip;
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][n][r]), dst,
+                                                      16 * i + 4 * g < a.dk ? off : kSkip,
+                                                      (unsigned)(16 * i + r) * pitch, 0);
+    }
+}
+
+template <int DK, int NV>
+__device__ __forceinline__ void zero_state(f32x4 (&S)[DK / 16][NV])
+{
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const unsigned row = 16 * i + 4 * (lane >> 4) + r, c = col0 + 16 * (NV * wave + n) + (lane & 15);
-                if (row < dk && c < dv)
-                    p[row * dv + c] = S[i][n][r];
-            }
-    }
+            S[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
 // S = exp(G_63) S + sum_s k_s (exp(G_63 - G_s) v_s)^T over the chunk in LDS.
@@ -439,8 +497,6 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
             }
 #pragma unroll
         for (int i = 0; i < DK / 16; ++i) {
-            if (i % 2 == 0)
-                __builtin_amdgcn_sched_barrier(0);
             f32x4 add[NV];
 #pragma unroll
             for (int n = 0; n < NV; ++n)
@@ -489,8 +545,6 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
             }
 #pragma unroll
             for (int i = 0; i < DK / 16; ++i) {
-                if (i % 4 == 0)
-                    __builtin_amdgcn_sched_barrier(0);
                 const u32x4 k = column_operand(ks, L::kKPitch, 16 * i, j);
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
@@ -554,6 +608,13 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
     const unsigned short *vp = static_cast<const unsigned short *>(a.v) + tok * a.v_token + head * a.v_head + col0;
     const float *gp = a.g + tok * a.g_token + head * a.g_head;
     unsigned short *op = static_cast<unsigned short *>(a.out) + tok * a.out_token + head * a.out_head;
+    const unsigned out_step = (unsigned)(2 * a.out_token);
+    unsigned out_off[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c = col0 + 16 * NV * wave + 4 * g;
+        out_off[n] = c + 16 * n < a.dv ? (lane & 15) * out_step + 2 * c : kSkip;
+    }
     const long long ws_off = ((long long)place * a.heads + head) * a.dk * a.dv;
 
     f32x4 S[DK / 16][NV];
@@ -569,16 +630,19 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
     // the parts-only kernel takes a second, token by token, pass if its state is not finite
     for (int attempt = 0; attempt < 2; ++attempt) {
         if constexpr (!OUT)
-            load_state<DK, NV>(a, nullptr, col0, S);
+            zero_state<DK, NV>(S);
         Tile<DK> tq, tk;
         Tile<64 * NV> tv;
+        tq.init(a.q_token, a.dk);
+        tk.init(a.k_token, a.dk);
+        tv.init(a.v_token, cols);
         double sum = 0.0;
         float gate = 0.0f;
         if (chunks > 0) {
             if constexpr (OUT)
-                tq.load(qp, a.q_token, n_tok, a.dk);
-            tk.load(kp, a.k_token, n_tok, a.dk);
-            tv.load(vp, a.v_token, n_tok, cols);
+                tq.load(qp, n_tok);
+            tk.load(kp, n_tok);
+            tv.load(vp, n_tok);
             if (wave == 0) {
                 gate = lane < n_tok ? gp[lane * a.g_token] : 0.0f;
                 sum = chunk_decays(gate, decays[0]);
@@ -597,45 +661,43 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
                 const long long at = (long long)(c + 1) * kChunk;
                 const int left = n_tok - (c + 1) * kChunk;
                 if constexpr (OUT)
-                    tq.load(qp + at * a.q_token, a.q_token, left, a.dk);
-                tk.load(kp + at * a.k_token, a.k_token, left, a.dk);
-                tv.load(vp + at * a.v_token, a.v_token, left, cols);
+                    tq.load(qp + at * a.q_token, left);
+                tk.load(kp + at * a.k_token, left);
+                tv.load(vp + at * a.v_token, left);
                 if (wave == 0) {
                     sum += chunk_decays(gate, decays[(c + 1) & 1]);
                     gate = kChunk + lane < left ? gp[(at + kChunk + lane) * a.g_token] : 0.0f;
                 }
             }
             if constexpr (OUT) {
-                // masked, decayed scores of the 16 tokens 16 wave + l % 16 with the tokens up to them
+                // masked, decayed, scaled scores of the 16 tokens 16 wave + l % 16 with the tokens up to them
                 {
-                    f32x4 sc[4];
+                    u32x4 qf[DK / 32];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int j = 0; j < DK / 32; ++j) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        const u32x4 qf = row_operand(qs, L::kQPitch, 16 * wave, j);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i <= wave)
-                                sc[i] = mma16<H>(row_operand(ks, L::kKPitch, 16 * i, j), qf, sc[i]);
-                    }
+                    for (int j = 0; j < DK / 32; ++j)
+                        qf[j] = row_operand(qs, L::kQPitch, 16 * wave, j);
                     const int t = 16 * wave + (lane & 15);
                     const float th = d.hi[t], tl = d.lo[t];
+                    f32x4 sc[4];
                     float top = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        sc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                         if (i > wave)
                             continue;
+#pragma unroll
+                        for (int j = 0; j < DK / 32; ++j)
+                            sc[i] = mma16<H>(row_operand(ks, L::kKPitch, 16 * i, j), qf[j], sc[i]);
                         const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * i + 4 * g]);
                         const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * i + 4 * g]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const bool seen = 16 * i + 4 * g + r <= t;
-                            const float e = __builtin_amdgcn_exp2f((th - sh[r]) + (tl - sl[r]));
-                            sc[i][r] = seen ? sc[i][r] * e : 0.0f;
-                            top = fmaxf(top, fabsf(sc[i][r]));
+                            // a later token: exp2(-inf) = 0 (times a score that is not finite: NaN, see recur)
+                            const bool seen = i < wave || 4 * g + r <= (lane & 15);
+                            const float x = seen ? (th - sh[r]) + (tl - sl[r]) : -INFINITY;
+                            sc[i][r] *= __builtin_amdgcn_exp2f(x) * a.scale;
+                            if constexpr (H)
+                                top = fmaxf(top, fabsf(sc[i][r]));
                         }
                     }
                     if constexpr (H) {
@@ -682,7 +744,6 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
                 }
 #pragma unroll
                 for (int j = 0; j < DK / 32; ++j) {
-                    __builtin_amdgcn_sched_barrier(0);
                     u32x4 f[NV][2];
 #pragma unroll
                     for (int n = 0; n < NV; ++n) {
@@ -715,7 +776,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     back[i] = 1.0f;
-                    float f = d.grown[16 * i + (lane & 15)];
+                    float f = d.grown[16 * i + (lane & 15)] * a.scale;
                     if constexpr (H) {
                         back[i] = score_back[i];
                         f *= s_back / back[i];          // powers of two: exact
@@ -743,31 +804,29 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
                         }
                     }
                 }
-                float odd = 0.0f;
+                // a sum is finite only if all of it is
+                float sums[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    sums[i] = 0.0f;
 #pragma unroll
                     for (int n = 0; n < NV; ++n)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            odd = fmaf(acc[i][n][r], 0.0f, odd);
+                        sums[i] += (acc[i][n][0] + acc[i][n][1]) + (acc[i][n][2] + acc[i][n][3]);
+                }
                 unsigned short *o = op + (long long)c * kChunk * a.out_token;
-                if (wave_any_nan(odd)) {
+                if (wave_any_nan(((sums[0] + sums[1]) + (sums[2] + sums[3])) * 0.0f)) {
                     recur<H, DK, NV, OUT>(a, lds, d, rows, S, o, col0);
                 } else {
+                    const __amdgpu_buffer_rsrc_t dst = make_rsrc(o);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int t = 16 * i + (lane & 15);
-                        const float f = a.scale * back[i];
 #pragma unroll
                         for (int n = 0; n < NV; ++n) {
-                            const int col = col0 + 16 * (NV * wave + n) + 4 * g;
-                            if (t < rows && col < a.dv) {
-                                u32x2 w;
-                                w.x = to_bits<H>(acc[i][n][0] * f) | (unsigned)to_bits<H>(acc[i][n][1] * f) << 16;
-                                w.y = to_bits<H>(acc[i][n][2] * f) | (unsigned)to_bits<H>(acc[i][n][3] * f) << 16;
-                                *reinterpret_cast<u32x2 *>(o + t * a.out_token + col) = w;
-                            }
+                            u32x2 w;
+                            w.x = pack2<H>(acc[i][n][0] * back[i], acc[i][n][1] * back[i]);
+                            w.y = pack2<H>(acc[i][n][2] * back[i], acc[i][n][3] * back[i]);
+                            __builtin_amdgcn_raw_buffer_store_b64(
+                                w, dst, 16 * i + (lane & 15) < rows ? out_off[n] : kSkip, 16 * i * out_step + 32 * n, 0);
                         }
                     }
                     update_state<H, DK, NV, OUT>(lds, d, S);
@@ -927,6 +986,7 @@ struct Shape {
 };
 
 constexpr int kMinPart = 256;
+constexpr int kSlots = 512;     // workgroups the chip runs at once: two on each of 256 CUs
 
 Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
 {
@@ -934,8 +994,8 @@ Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
     s.nv = dk > 128 || dv <= 64 || (dv > 128 && dv <= 192) ? 1 : 2;
     s.col_tiles = (dv + 64 * s.nv - 1) / (64 * s.nv);
     const long long units = (long long)heads * s.col_tiles;
-    long long part = ((long long)tokens * units + 511) / 512;
-    part = (part + kChunk - 1) / kChunk * kChunk;
+    const long long most = units < kSlots ? kSlots / units : 1;
+    long long part = ((tokens + most - 1) / most + kChunk - 1) / kChunk * kChunk;
     if (part < kMinPart)
         part = kMinPart;
     s.multi = part < tokens;
