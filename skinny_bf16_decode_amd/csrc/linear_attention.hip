@@ -13,10 +13,10 @@
 //   o_t   = scale (exp(G_t) q_t^T S + sum_{s <= t} exp(G_t - G_s) (q_t . k_s) v_s)
 //   S_new = exp(G_63) S + sum_s k_s (exp(G_63 - G_s) v_s)^T
 //
-// which are four matrix products a chunk.  A workgroup of four waves walks the
-// chunks of one (sequence part, head, 64 NV value columns); each wave keeps the
-// state of its own 16 NV columns in registers, in the result layout of the
-// 16x16x32 MFMA, from one chunk to the next.
+// which are four matrix products a chunk.  A workgroup of four or eight waves
+// walks the chunks of one (sequence part, head, 64 or 128 value columns); each
+// wave keeps the state of its own 16 columns in registers, in the result layout
+// of the 16x16x32 MFMA, from one chunk to the next.
 #include <hip/hip_runtime.h>
 
 #include <stdarg.h>
@@ -130,6 +130,7 @@ __device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[TERMS
             const bf16x2 p = {(__bf16)a, (__bf16)b};
             w[i] = __builtin_bit_cast(unsigned int, p);
             if (i + 1 < TERMS) {
+                asm("" : "+v"(w[i]));       // else the low half is rounded a second time, alone
                 a -= __uint_as_float(w[i] << 16);
                 b -= __uint_as_float(w[i] & 0xFFFF0000u);
             }
@@ -180,6 +181,9 @@ __device__ __forceinline__ void half_range(float top, float &mul, float &back)
     back = __uint_as_float((e - 14u) << 23);
 }
 
+// 1 / p of a power of two between 2^-126 and 2^126
+__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+
 // Whether any lane of the wave saw a value that is not finite: acc gathers x * 0.
 __device__ __forceinline__ bool wave_any_nan(float acc) { return __ballot(acc != 0.0f) != 0ull; }
 
@@ -222,11 +226,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base)
 // A tile of 64 token rows of COLS 16-bit columns on its way from global memory
 // through registers to LDS.  Rows from `rows` on and columns from `cols` on
 // are zero.
-template <int COLS>
+template <int COLS, int THREADS>
 struct Tile {
     static constexpr int kPerRow = COLS / 8;
-    static constexpr int kVecs = kChunk * kPerRow / kThreads;
-    static constexpr int kRowStep = kThreads / kPerRow;
+    static constexpr int kVecs = (kChunk * kPerRow + THREADS - 1) / THREADS;
+    static constexpr int kRowStep = THREADS / kPerRow;
     u32x4 r[kVecs];
     unsigned off, step;         // byte offset of the first vector, bytes between vectors
 
@@ -252,9 +256,38 @@ struct Tile {
         const int row = threadIdx.x / kPerRow, col = (threadIdx.x % kPerRow) * 8;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
-            *reinterpret_cast<u32x4 *>(lds + (row + i * kRowStep) * pitch + col) = r[i];
+            if (kRowStep <= kChunk || row < kChunk)     // more threads than vectors
+                *reinterpret_cast<u32x4 *>(lds + (row + i * kRowStep) * pitch + col) = r[i];
+    }
+
+    // Columns in the order of operand_position.
+    __device__ __forceinline__ void store_operands(unsigned short *lds, int pitch) const
+    {
+        const int row = threadIdx.x / kPerRow, col = (threadIdx.x % kPerRow) * 8;
+        unsigned short *at = lds + row * pitch + (col & ~31) + 2 * (col & 8) + ((col >> 2) & 4);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            if (kRowStep <= kChunk || row < kChunk) {
+                *reinterpret_cast<u32x2 *>(at + i * kRowStep * pitch) = u32x2{r[i].x, r[i].y};
+                *reinterpret_cast<u32x2 *>(at + i * kRowStep * pitch + 8) = u32x2{r[i].z, r[i].w};
+            }
     }
 };
+
+// Position in an LDS row of q of column c: within 32 columns, the four
+// 16 h + 4 g + 0..3 lie at 8 g + 4 h, the order of the MFMA operand below, so
+// that it is one 16-byte read.
+__device__ __forceinline__ int operand_position(int c)
+{
+    return (c & ~31) + 8 * ((c >> 2) & 3) + 4 * ((c >> 4) & 1) + (c & 3);
+}
+
+// MFMA operand from 16 token rows of q as stored by store_operands.
+__device__ __forceinline__ u32x4 query_operand(const unsigned short *lds, int pitch, int row0, int j)
+{
+    const int lane = threadIdx.x & 63;
+    return *reinterpret_cast<const u32x4 *>(lds + (row0 + (lane & 15)) * pitch + 32 * j + 8 * (lane >> 4));
+}
 
 // MFMA operand from 16 token rows: lane (row l % 16) holds columns
 // 32 j + 4 (l / 16) + 0..3 and the 4 columns 16 further on, the order in
@@ -290,7 +323,7 @@ struct alignas(16) Decays {
     float total;                    // exp(G_63)
 };
 
-// Wave 0: lane t has g_t (0 past the end).  Sums are in 64 bits, so that the
+// One wave: lane t has g_t (0 past the end).  Sums are in 64 bits, so that the
 // differences of far-decayed chunks keep their bits.  Finite sums are wanted
 // of -inf too: -200 gives 0 as well.  NaN stays.
 __device__ __forceinline__ double chunk_decays(float g, Decays &d)
@@ -321,11 +354,12 @@ __device__ __forceinline__ double chunk_decays(float g, Decays &d)
 __device__ __host__ constexpr int score_slot(int tile, int j) { return (tile < 2 ? tile : 2 * tile - 2) + j; }
 constexpr int kScoreSlots = 6;
 
-template <int DK, int NV, bool OUT>
+template <int DK, int WAVES, bool OUT>
 struct Layout {
+    static constexpr int kCols = 16 * WAVES;    // value columns of a workgroup
     static constexpr int kQPitch = DK + 8;      // row reads: 16 rows x 16 bytes on all banks
     static constexpr int kKPitch = DK + 16;     // transposing reads: 8 rows x 32 bytes on all banks
-    static constexpr int kVPitch = 64 * NV + 16;
+    static constexpr int kVPitch = kCols + 16;
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + (OUT ? kChunk * kQPitch * 2 : 0);
     static constexpr int kV = kK + kChunk * kKPitch * 2;
@@ -333,240 +367,185 @@ struct Layout {
     static constexpr int kBytes = kScores + (OUT ? kScoreSlots * 2 * 64 * 16 : 0);
 };
 
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // The recurrence token by token, as it is defined, for one wave's columns of a
-// chunk in LDS: used where a value is not finite, since 0 * inf in a product
-// over masked tokens, or in a split into terms, would spread NaN to outputs
-// that the definition leaves alone.  The state is indexed at run time and so
-// goes through memory: the path is rare, and as registers it made the common
-// one spill (32768 tokens of 12 heads of 128: 532 us, 310 without it).
-template <bool H, int DK, int NV, bool OUT>
-__device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds, const Decays &d, int rows,
-                                      f32x4 (&S)[DK / 16][NV], unsigned short *out, int col0)
+// chunk in LDS, its state in memory (T, laid out like the registers): used
+// where a value is not finite, since 0 * inf in a product over masked tokens, or in a split into
+// terms, would spread NaN to outputs that the definition leaves alone.  A wave
+// that has come here stays here for the rest of its part, and carries the
+// state in registers along unused: merging the two would cost every wave a
+// second copy of it.
+template <bool H, int DK, int WAVES, bool OUT>
+__device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds, const Decays &d, int rows, f32x4 *T,
+                                      unsigned short *out, int col0)
 {
-    using L = Layout<DK, NV, OUT>;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    using L = Layout<DK, WAVES, OUT>;
+    const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4;
     const unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
-    f32x4 T[DK / 16][NV];
-#pragma unroll
-    for (int i = 0; i < DK / 16; ++i)
-#pragma unroll
-        for (int n = 0; n < NV; ++n)
-            T[i][n] = S[i][n];
 #pragma unroll 1
     for (int t = 0; t < rows; ++t) {
-        const float e = d.own[t];
-        float v[NV], o[NV];
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            v[n] = to_float<H>(vs[t * L::kVPitch + 16 * (NV * wave + n) + (lane & 15)]);
-            o[n] = 0.0f;
-        }
+        const float e = d.own[t], v = to_float<H>(vs[t * L::kVPitch + 16 * wave + (lane & 15)]);
+        float o = 0.0f;
 #pragma unroll 1
         for (int i = 0; i < DK / 16; ++i) {
+            f32x4 S = T[i];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int c = 16 * i + 4 * g + r;
                 const float k = to_float<H>(ks[t * L::kKPitch + c]);
-                float q = 0.0f;
+                // rows past dk hold no state: 0 * a v that is not finite is not theirs to add
+                const float s = c < a.dk ? S[r] * e + k * v : 0.0f;
+                S[r] = s;
                 if constexpr (OUT)
-                    q = to_float<H>(qs[t * L::kQPitch + c]);
-#pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    // columns past dk hold no state: 0 * a non-finite v is not theirs to add
-                    const float s = c < a.dk ? T[i][n][r] * e + k * v[n] : 0.0f;
-                    T[i][n][r] = s;
-                    if constexpr (OUT)
-                        o[n] += c < a.dk ? q * s : 0.0f;
-                }
+                    o += c < a.dk ? to_float<H>(qs[t * L::kQPitch + operand_position(c)]) * s : 0.0f;
             }
+            T[i] = S;
         }
         if constexpr (OUT) {
-#pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                float x = o[n];
-                x += __shfl_xor(x, 16, 64);
-                x += __shfl_xor(x, 32, 64);
-                const int c = col0 + 16 * (NV * wave + n) + (lane & 15);
-                if (g == 0 && c < a.dv)
-                    out[t * a.out_token + c] = to_bits<H>(x * a.scale);
-            }
+            o += __shfl_xor(o, 16, 64);
+            o += __shfl_xor(o, 32, 64);
+            const int c = col0 + 16 * wave + (lane & 15);
+            if (g == 0 && c < a.dv)
+                out[t * a.out_token + c] = to_bits<H>(o * a.scale);
         }
     }
-#pragma unroll
-    for (int i = 0; i < DK / 16; ++i)
-#pragma unroll
-        for (int n = 0; n < NV; ++n)
-            S[i][n] = T[i][n];
 }
 
 // Natural [dk][dv] state <-> result registers of the wave's columns.  Lane
 // group g holds rows 4 g .. 4 g + 3 of each 16; dk is a multiple of 8, so the
 // four are all in or all out.
-template <int DK, int NV>
-__device__ __forceinline__ void load_state(const LArgs &a, const float *p, int col0, f32x4 (&S)[DK / 16][NV])
+template <int DK>
+__device__ __forceinline__ unsigned state_offset(const LArgs &a, int col0)
 {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const int lane = threadIdx.x & 63, c = col0 + 16 * wave_id() + (lane & 15);
+    return c < a.dv ? 4u * (lane >> 4) * 4u * (unsigned)a.dv + 4u * c : kSkip;
+}
+
+template <int DK>
+__device__ __forceinline__ void load_state(const LArgs &a, const float *p, int col0, f32x4 (&S)[DK / 16])
+{
     const __amdgpu_buffer_rsrc_t src = make_rsrc(p);
-    const unsigned pitch = 4u * (unsigned)a.dv;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int c = col0 + 16 * (NV * wave + n) + (lane & 15);
-        const unsigned off = p && c < a.dv ? 4u * g * pitch + 4u * c : kSkip;
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                S[i][n][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                    src, 16 * i + 4 * g < a.dk ? off : kSkip, (unsigned)(16 * i + r) * pitch, 0));
-    }
-}
-
-template <int DK, int NV>
-__device__ __forceinline__ void store_state(const LArgs &a, float *p, int col0, const f32x4 (&S)[DK / 16][NV])
-{
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
-    const __amdgpu_buffer_rsrc_t dst = make_rsrc(p);
-    const unsigned pitch = 4u * (unsigned)a.dv;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int c = col0 + 16 * (NV * wave + n) + (lane & 15);
-        const unsigned off = c < a.dv ? 4u * g * pitch + 4u * c : kSkip;
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][n][r]), dst,
-                                                      16 * i + 4 * g < a.dk ? off : kSkip,
-                                                      (unsigned)(16 * i + r) * pitch, 0);
-    }
-}
-
-template <int DK, int NV>
-__device__ __forceinline__ void zero_state(f32x4 (&S)[DK / 16][NV])
-{
+    const unsigned off = p ? state_offset<DK>(a, col0) : kSkip;
+    const int row = 4 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-            S[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < 4; ++r)
+            S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                src, 16 * i + row < a.dk ? off : kSkip, (unsigned)(16 * i + r) * 4u * (unsigned)a.dv, 0));
+}
+
+template <int DK>
+__device__ __forceinline__ void store_state(const LArgs &a, float *p, int col0, const f32x4 (&S)[DK / 16])
+{
+    const __amdgpu_buffer_rsrc_t dst = make_rsrc(p);
+    const unsigned off = state_offset<DK>(a, col0);
+    const int row = 4 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), dst, 16 * i + row < a.dk ? off : kSkip,
+                                                  (unsigned)(16 * i + r) * 4u * (unsigned)a.dv, 0);
+}
+
+// The wave's columns of v over the tokens of step j, each times exp(G_63 - G_s).
+template <bool H>
+__device__ __forceinline__ void decayed_values(u32x4 v, const Decays &d, int j, float (&x)[8])
+{
+    const int g = (threadIdx.x & 63) >> 4;
+    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 4 * g]);
+    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 16 + 4 * g]);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float lo, hi;
+        const unsigned int w = v[p];
+        unpack2<H>(w, lo, hi);
+        x[2 * p] = lo * (p < 2 ? w0[2 * p] : w1[2 * p - 4]);
+        x[2 * p + 1] = hi * (p < 2 ? w0[2 * p + 1] : w1[2 * p - 3]);
+    }
 }
 
 // S = exp(G_63) S + sum_s k_s (exp(G_63 - G_s) v_s)^T over the chunk in LDS.
 // k is exact in 16 bits; the decayed v is fp32 and goes in as three BF16 terms
 // (24 bits), or two FP16 terms after a power of two (22 bits), so the state
 // keeps fp32's accuracy on the matrix units.
-template <bool H, int DK, int NV, bool OUT>
-__device__ __forceinline__ void update_state(const unsigned short *lds, const Decays &d, f32x4 (&S)[DK / 16][NV])
+template <bool H, int DK, int WAVES, bool OUT>
+__device__ __forceinline__ void update_state(const unsigned short *lds, const Decays &d, f32x4 (&S)[DK / 16])
 {
-    using L = Layout<DK, NV, OUT>;
+    using L = Layout<DK, WAVES, OUT>;
     constexpr int kTerms = H ? 2 : 3;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
-    const unsigned short *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
+    const unsigned short *ks = lds + L::kK / 2, *vs = lds + L::kV / 2 + 16 * wave_id();
     const float total = d.total;
     if constexpr (H) {
-        float x[2][NV][8], top = 0.0f;
+        float x[2][8], top = 0.0f, mul, back;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 4 * g]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 16 + 4 * g]);
+            decayed_values<H>(column_operand(vs, L::kVPitch, 0, j), d, j, x[j]);
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const u32x4 v = column_operand(vs, L::kVPitch, 16 * (NV * wave + n), j);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    float lo, hi;
-                    const unsigned int w = v[p];
-                    unpack2<H>(w, lo, hi);
-                    x[j][n][2 * p] = lo * (p < 2 ? w0[2 * p] : w1[2 * p - 4]);
-                    x[j][n][2 * p + 1] = hi * (p < 2 ? w0[2 * p + 1] : w1[2 * p - 3]);
-                    top = fmaxf(top, fmaxf(fabsf(x[j][n][2 * p]), fabsf(x[j][n][2 * p + 1])));
-                }
-            }
+            for (int p = 0; p < 8; ++p)
+                top = fmaxf(top, fabsf(x[j][p]));
         }
-        float mul, back;
         half_range(wave_max(top), mul, back);
-        u32x4 f[2][NV][kTerms];
+        u32x4 f[2][kTerms];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-#pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    x[j][n][p] *= mul;
-                split8<H, kTerms>(x[j][n], f[j][n]);
-            }
+            for (int p = 0; p < 8; ++p)
+                x[j][p] *= mul;
+            split8<H, kTerms>(x[j], f[j]);
+        }
 #pragma unroll
         for (int i = 0; i < DK / 16; ++i) {
-            f32x4 add[NV];
-#pragma unroll
-            for (int n = 0; n < NV; ++n)
-                add[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 add = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const u32x4 k = column_operand(ks, L::kKPitch, 16 * i, j);
 #pragma unroll
-                for (int n = 0; n < NV; ++n)
-#pragma unroll
-                    for (int m = 0; m < kTerms; ++m)
-                        add[n] = mma16<H>(k, f[j][n][m], add[n]);
+                for (int m = 0; m < kTerms; ++m)
+                    add = mma16<H>(k, f[j][m], add);
             }
 #pragma unroll
-            for (int n = 0; n < NV; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    S[i][n][r] = S[i][n][r] * total + add[n][r] * back;
+            for (int r = 0; r < 4; ++r)
+                S[i][r] = S[i][r] * total + add[r] * back;
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i)
-#pragma unroll
-            for (int n = 0; n < NV; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    S[i][n][r] *= total;
+        u32x4 f[2][kTerms];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 4 * g]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.rest[32 * j + 16 + 4 * g]);
-            u32x4 f[NV][kTerms];
+            float x[8];
+            decayed_values<H>(column_operand(vs, L::kVPitch, 0, j), d, j, x);
+            split8<H, kTerms>(x, f[j]);
+        }
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const u32x4 v = column_operand(vs, L::kVPitch, 16 * (NV * wave + n), j);
-                float x[8];
+        for (int i = 0; i < DK / 16; ++i) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    float lo, hi;
-                    const unsigned int w = v[p];
-                    unpack2<H>(w, lo, hi);
-                    x[2 * p] = lo * (p < 2 ? w0[2 * p] : w1[2 * p - 4]);
-                    x[2 * p + 1] = hi * (p < 2 ? w0[2 * p + 1] : w1[2 * p - 3]);
-                }
-                split8<H, kTerms>(x, f[n]);
-            }
+            for (int r = 0; r < 4; ++r)
+                S[i][r] *= total;
 #pragma unroll
-            for (int i = 0; i < DK / 16; ++i) {
+            for (int j = 0; j < 2; ++j) {
                 const u32x4 k = column_operand(ks, L::kKPitch, 16 * i, j);
 #pragma unroll
-                for (int n = 0; n < NV; ++n)
-#pragma unroll
-                    for (int m = 0; m < kTerms; ++m)
-                        S[i][n] = mma16<H>(k, f[n][m], S[i][n]);
+                for (int m = 0; m < kTerms; ++m)
+                    S[i] = mma16<H>(k, f[j][m], S[i]);
             }
         }
     }
 }
 
-// One part of a sequence for one head and 64 NV value columns.  OUT: outputs,
-// and the sequence's new state after its last part.  Otherwise: what the part
-// alone adds to the state, for the parts after it.
-template <bool H, int DK, int NV, bool OUT>
-__global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
+// One part of a sequence for one head and 16 WAVES value columns, 16 a wave.
+// OUT: outputs, and the sequence's new state after its last part.  Otherwise:
+// what the part alone adds to the state, for the parts after it.
+template <bool H, int DK, int WAVES, bool OUT>
+__global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void linear_chunks(LArgs a)
 {
-    using L = Layout<DK, NV, OUT>;
+    using L = Layout<DK, WAVES, OUT>;
+    constexpr int kGateWave = WAVES == 8 ? 4 : 0;   // it has the least of the scores to do
     extern __shared__ __align__(16) unsigned short lds[];
     __shared__ Decays decays[2];
-    __shared__ float score_back[4];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    __shared__ float score_back[4][2];
+    const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4;
     unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
     u32x4 *scores = reinterpret_cast<u32x4 *>(lds + L::kScores / 2);
 
@@ -598,7 +577,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
         }
     }
     const int chunks = (n_tok + kChunk - 1) / kChunk;
-    const int col0 = tile * 64 * NV, cols = min(a.dv - col0, 64 * NV);
+    const int col0 = tile * L::kCols, cols = min(a.dv - col0, L::kCols);
     const int khead = head / a.share;
     const int slot = slot_of(a, p.seq);
 
@@ -609,30 +588,34 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
     const float *gp = a.g + tok * a.g_token + head * a.g_head;
     unsigned short *op = static_cast<unsigned short *>(a.out) + tok * a.out_token + head * a.out_head;
     const unsigned out_step = (unsigned)(2 * a.out_token);
-    unsigned out_off[NV];
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int c = col0 + 16 * NV * wave + 4 * g;
-        out_off[n] = c + 16 * n < a.dv ? (lane & 15) * out_step + 2 * c : kSkip;
-    }
+    const int out_col = col0 + 16 * wave + 4 * g;
+    const unsigned out_off = out_col < a.dv ? (lane & 15) * out_step + 2 * out_col : kSkip;
     const long long ws_off = ((long long)place * a.heads + head) * a.dk * a.dv;
 
-    f32x4 S[DK / 16][NV];
+    f32x4 S[DK / 16];
+    f32x4 memory[DK / 16], *T = memory;         // the state of a wave that goes token by token
+    asm volatile("" : "+v"(T) : : "memory");    // an address of its own: not turned back into registers
+    bool slow = false;
     if constexpr (OUT) {
         const float *from = nullptr;
         if (a.multi && parts > 1)
             from = a.ws_state + ws_off;
         else if (a.state_in && slot >= 0)
             from = a.state_in + slot * a.in_slot + head * a.in_head;
-        load_state<DK, NV>(a, from, col0, S);
+        load_state<DK>(a, from, col0, S);
     }
 
     // the parts-only kernel takes a second, token by token, pass if its state is not finite
     for (int attempt = 0; attempt < 2; ++attempt) {
-        if constexpr (!OUT)
-            zero_state<DK, NV>(S);
-        Tile<DK> tq, tk;
-        Tile<64 * NV> tv;
+        if constexpr (!OUT) {
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i) {
+                T[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                S[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+        }
+        Tile<DK, 64 * WAVES> tq, tk;
+        Tile<L::kCols, 64 * WAVES> tv;
         tq.init(a.q_token, a.dk);
         tk.init(a.k_token, a.dk);
         tv.init(a.v_token, cols);
@@ -643,7 +626,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
                 tq.load(qp, n_tok);
             tk.load(kp, n_tok);
             tv.load(vp, n_tok);
-            if (wave == 0) {
+            if (wave == kGateWave) {
                 gate = lane < n_tok ? gp[lane * a.g_token] : 0.0f;
                 sum = chunk_decays(gate, decays[0]);
                 gate = kChunk + lane < n_tok ? gp[(kChunk + lane) * a.g_token] : 0.0f;
@@ -653,7 +636,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
             const int rows = min(n_tok - c * kChunk, kChunk);
             const Decays &d = decays[c & 1];
             if constexpr (OUT)
-                tq.store(qs, L::kQPitch);
+                tq.store_operands(qs, L::kQPitch);
             tk.store(ks, L::kKPitch);
             tv.store(vs, L::kVPitch);
             __syncthreads();
@@ -664,179 +647,164 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
                     tq.load(qp + at * a.q_token, left);
                 tk.load(kp + at * a.k_token, left);
                 tv.load(vp + at * a.v_token, left);
-                if (wave == 0) {
+                if (wave == kGateWave) {
                     sum += chunk_decays(gate, decays[(c + 1) & 1]);
                     gate = kChunk + lane < left ? gp[(at + kChunk + lane) * a.g_token] : 0.0f;
                 }
             }
             if constexpr (OUT) {
-                // masked, decayed, scaled scores of the 16 tokens 16 wave + l % 16 with the tokens up to them
-                {
+                // masked, decayed, scaled scores of 16 tokens t with the 32 tokens of step j, over the waves
+#pragma unroll
+                for (int jj = 0; jj < 8 / WAVES; ++jj) {
+                    const int tt = wave & 3, j = WAVES == 8 ? wave >> 2 : jj;
+                    if (2 * j > tt)
+                        continue;               // all later
                     u32x4 qf[DK / 32];
 #pragma unroll
-                    for (int j = 0; j < DK / 32; ++j)
-                        qf[j] = row_operand(qs, L::kQPitch, 16 * wave, j);
-                    const int t = 16 * wave + (lane & 15);
+                    for (int i = 0; i < DK / 32; ++i)
+                        qf[i] = query_operand(qs, L::kQPitch, 16 * tt, i);
+                    const int t = 16 * tt + (lane & 15);
                     const float th = d.hi[t], tl = d.lo[t];
-                    f32x4 sc[4];
-                    float top = 0.0f;
+                    float x[8], top = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        sc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                        if (i > wave)
-                            continue;
+                    for (int h = 0; h < 2; ++h) {
+                        const int st = 2 * j + h;   // tokens 16 st ..; past tile tt all later
+                        f32x4 sc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        if (h == 0 || st <= tt) {
 #pragma unroll
-                        for (int j = 0; j < DK / 32; ++j)
-                            sc[i] = mma16<H>(row_operand(ks, L::kKPitch, 16 * i, j), qf[j], sc[i]);
-                        const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * i + 4 * g]);
-                        const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * i + 4 * g]);
+                            for (int i = 0; i < DK / 32; ++i)
+                                sc = mma16<H>(row_operand(ks, L::kKPitch, 16 * st, i), qf[i], sc);
+                        }
+                        const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * st + 4 * g]);
+                        const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * st + 4 * g]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             // a later token: exp2(-inf) = 0 (times a score that is not finite: NaN, see recur)
-                            const bool seen = i < wave || 4 * g + r <= (lane & 15);
-                            const float x = seen ? (th - sh[r]) + (tl - sl[r]) : -INFINITY;
-                            sc[i][r] *= __builtin_amdgcn_exp2f(x) * a.scale;
+                            const bool seen = st < tt || (st == tt && 4 * g + r <= (lane & 15));
+                            const float e = seen ? (th - sh[r]) + (tl - sl[r]) : -INFINITY;
+                            x[4 * h + r] = sc[r] * (__builtin_amdgcn_exp2f(e) * a.scale);
                             if constexpr (H)
-                                top = fmaxf(top, fabsf(sc[i][r]));
+                                top = fmaxf(top, fabsf(x[4 * h + r]));
                         }
                     }
                     if constexpr (H) {
                         float mul, back;
                         half_range(wave_max(top), mul, back);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                sc[i][r] *= mul;
+                        for (int r = 0; r < 8; ++r)
+                            x[r] *= mul;
                         if (lane == 0)
-                            score_back[wave] = back;
+                            score_back[tt][j] = back;
                     }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (2 * j > wave)
-                            continue;
-                        const float x[8] = {sc[2 * j][0], sc[2 * j][1], sc[2 * j][2], sc[2 * j][3],
-                                            sc[2 * j + 1][0], sc[2 * j + 1][1], sc[2 * j + 1][2], sc[2 * j + 1][3]};
-                        u32x4 f[2];
-                        split8<H, 2>(x, f);
-                        scores[(score_slot(wave, j) * 2 + 0) * 64 + lane] = f[0];
-                        scores[(score_slot(wave, j) * 2 + 1) * 64 + lane] = f[1];
-                    }
+                    u32x4 f[2];
+                    split8<H, 2>(x, f);
+                    scores[(score_slot(tt, j) * 2 + 0) * 64 + lane] = f[0];
+                    scores[(score_slot(tt, j) * 2 + 1) * 64 + lane] = f[1];
                 }
                 // S^T q of all 64 tokens, the state in two terms
-                f32x4 acc[4][NV];
+                f32x4 acc[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int n = 0; n < NV; ++n)
-                        acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 float s_mul = 1.0f, s_back = 1.0f;
                 if constexpr (H) {
                     float top = 0.0f;
 #pragma unroll
                     for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
-                        for (int n = 0; n < NV; ++n)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                top = fmaxf(top, fabsf(S[i][n][r]));
+                        for (int r = 0; r < 4; ++r)
+                            top = fmaxf(top, fabsf(S[i][r]));
                     half_range(wave_max(top), s_mul, s_back);
                 }
 #pragma unroll
                 for (int j = 0; j < DK / 32; ++j) {
-                    u32x4 f[NV][2];
+                    u32x4 qf[4], f[2];
 #pragma unroll
-                    for (int n = 0; n < NV; ++n) {
-                        float x[8];
+                    for (int i = 0; i < 4; ++i)
+                        qf[i] = query_operand(qs, L::kQPitch, 16 * i, j);
+                    __builtin_amdgcn_sched_barrier(0);      // on their way while the state is split
+                    float x[8];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            x[r] = S[2 * j][n][r];
-                            x[4 + r] = S[2 * j + 1][n][r];
-                        }
-                        if constexpr (H) {
-#pragma unroll
-                            for (int r = 0; r < 8; ++r)
-                                x[r] *= s_mul;
-                        }
-                        split8<H, 2>(x, f[n]);
+                    for (int r = 0; r < 4; ++r) {
+                        x[r] = S[2 * j][r];
+                        x[4 + r] = S[2 * j + 1][r];
                     }
+                    if constexpr (H) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const u32x4 qf = row_operand(qs, L::kQPitch, 16 * i, j);
-#pragma unroll
-                        for (int n = 0; n < NV; ++n) {
-                            acc[i][n] = mma16<H>(f[n][0], qf, acc[i][n]);
-                            acc[i][n] = mma16<H>(f[n][1], qf, acc[i][n]);
-                        }
+                        for (int r = 0; r < 8; ++r)
+                            x[r] *= s_mul;
                     }
+                    split8<H, 2>(x, f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[i] = mma16<H>(f[0], qf[i], acc[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[i] = mma16<H>(f[1], qf[i], acc[i]);
                 }
                 __syncthreads();
-                // + scores V
+                // + scores V; FP16 scores carry powers of two (all steps below are exact in them)
                 float back[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     back[i] = 1.0f;
                     float f = d.grown[16 * i + (lane & 15)] * a.scale;
                     if constexpr (H) {
-                        back[i] = score_back[i];
-                        f *= s_back / back[i];          // powers of two: exact
+                        back[i] = score_back[i][0];
+                        f *= s_back * inverse_power(back[i]);
                     }
 #pragma unroll
-                    for (int n = 0; n < NV; ++n)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[i][n][r] *= f;
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][r] *= f;
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    u32x4 vf[NV];
-#pragma unroll
-                    for (int n = 0; n < NV; ++n)
-                        vf[n] = column_operand(vs, L::kVPitch, 16 * (NV * wave + n), j);
+                    const u32x4 vf = column_operand(vs, L::kVPitch, 16 * wave, j);
 #pragma unroll
                     for (int i = 2 * j; i < 4; ++i) {
-                        const u32x4 p0 = scores[(score_slot(i, j) * 2 + 0) * 64 + lane];
-                        const u32x4 p1 = scores[(score_slot(i, j) * 2 + 1) * 64 + lane];
+                        if constexpr (H) {
+                            if (j) {
+                                const float f = back[i] * inverse_power(score_back[i][1]);
 #pragma unroll
-                        for (int n = 0; n < NV; ++n) {
-                            acc[i][n] = mma16<H>(vf[n], p0, acc[i][n]);
-                            acc[i][n] = mma16<H>(vf[n], p1, acc[i][n]);
+                                for (int r = 0; r < 4; ++r)
+                                    acc[i][r] *= f;
+                                back[i] = score_back[i][1];
+                            }
                         }
+                        acc[i] = mma16<H>(vf, scores[(score_slot(i, j) * 2 + 0) * 64 + lane], acc[i]);
+                        acc[i] = mma16<H>(vf, scores[(score_slot(i, j) * 2 + 1) * 64 + lane], acc[i]);
                     }
                 }
                 // a sum is finite only if all of it is
                 float sums[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sums[i] = 0.0f;
-#pragma unroll
-                    for (int n = 0; n < NV; ++n)
-                        sums[i] += (acc[i][n][0] + acc[i][n][1]) + (acc[i][n][2] + acc[i][n][3]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    sums[i] = (acc[i][0] + acc[i][1]) + (acc[i][2] + acc[i][3]);
                 unsigned short *o = op + (long long)c * kChunk * a.out_token;
-                if (wave_any_nan(((sums[0] + sums[1]) + (sums[2] + sums[3])) * 0.0f)) {
-                    recur<H, DK, NV, OUT>(a, lds, d, rows, S, o, col0);
+                if (!slow && wave_any_nan(((sums[0] + sums[1]) + (sums[2] + sums[3])) * 0.0f)) {
+                    slow = true;
+#pragma unroll
+                    for (int i = 0; i < DK / 16; ++i)
+                        T[i] = S[i];
+                }
+                if (slow) {
+                    recur<H, DK, WAVES, OUT>(a, lds, d, rows, T, o, col0);
                 } else {
                     const __amdgpu_buffer_rsrc_t dst = make_rsrc(o);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                        for (int n = 0; n < NV; ++n) {
-                            u32x2 w;
-                            w.x = pack2<H>(acc[i][n][0] * back[i], acc[i][n][1] * back[i]);
-                            w.y = pack2<H>(acc[i][n][2] * back[i], acc[i][n][3] * back[i]);
-                            __builtin_amdgcn_raw_buffer_store_b64(
-                                w, dst, 16 * i + (lane & 15) < rows ? out_off[n] : kSkip, 16 * i * out_step + 32 * n, 0);
-                        }
+                        u32x2 w;
+                        w.x = pack2<H>(acc[i][0] * back[i], acc[i][1] * back[i]);
+                        w.y = pack2<H>(acc[i][2] * back[i], acc[i][3] * back[i]);
+                        __builtin_amdgcn_raw_buffer_store_b64(w, dst, 16 * i + (lane & 15) < rows ? out_off : kSkip,
+                                                              16 * i * out_step, 0);
                     }
-                    update_state<H, DK, NV, OUT>(lds, d, S);
                 }
             } else {
                 if (attempt)
-                    recur<H, DK, NV, OUT>(a, lds, d, rows, S, nullptr, col0);
-                else
-                    update_state<H, DK, NV, OUT>(lds, d, S);
+                    recur<H, DK, WAVES, OUT>(a, lds, d, rows, T, nullptr, col0);
             }
+            update_state<H, DK, WAVES, OUT>(lds, d, S);
             __syncthreads();
         }
         if constexpr (OUT)
@@ -845,24 +813,29 @@ __global__ __launch_bounds__(kThreads, 2) void linear_chunks(LArgs a)
 #pragma unroll
         for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
-            for (int n = 0; n < NV; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    odd = fmaf(S[i][n][r], 0.0f, odd);
-        if (threadIdx.x == 0 && tile == 0) {
+            for (int r = 0; r < 4; ++r)
+                odd += S[i][r] * 0.0f;
+        slow = attempt == 1;
+        if (wave == kGateWave && lane == 0 && tile == 0) {
             a.ws_decay[(long long)place * a.heads + head] = sum;
             if (p.part == 0)
                 a.ws_serial[(long long)p.seq * a.heads + head] = 0x7FFFFFFF;
         }
-        if (!__syncthreads_or(odd != 0.0f))
+        if (slow || !__syncthreads_or(odd != 0.0f))
             break;
     }
+    float *to = a.ws_state + ws_off;
     if constexpr (OUT) {
-        if (last && a.state_out && slot >= 0)
-            store_state<DK, NV>(a, a.state_out + slot * a.so_slot + head * a.so_head, col0, S);
-    } else {
-        store_state<DK, NV>(a, a.ws_state + ws_off, col0, S);
+        if (!last || !a.state_out || slot < 0)
+            return;
+        to = a.state_out + slot * a.so_slot + head * a.so_head;
     }
+    if (slow) {
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i)
+            S[i] = T[i];
+    }
+    store_state<DK>(a, to, col0, S);
 }
 
 // State at the start of every part of the sequences that have several:
@@ -884,21 +857,36 @@ __global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
     f32x4 S = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (a.state_in && slot >= 0)
         S = *reinterpret_cast<const f32x4 *>(a.state_in + slot * a.in_slot + head * a.in_head + at);
-    for (int j = 0; j < parts; ++j) {
-        const long long ph = (long long)(place0 + j) * a.heads + head;
-        float *w = a.ws_state + ph * size + at;
-        f32x4 add = S;
-        float f = 0.0f;
-        if (j + 1 < parts) {
-            add = *reinterpret_cast<const f32x4 *>(w);
-            f = __builtin_amdgcn_exp2f((float)a.ws_decay[ph]);
-            const float odd = fmaf(S[0], 0.0f, 0.0f) + fmaf(S[1], 0.0f, 0.0f) + fmaf(S[2], 0.0f, 0.0f) +
-                              fmaf(S[3], 0.0f, 0.0f);
-            if (!(f < INFINITY) || (f == 0.0f && odd != 0.0f))
-                atomicMin(&a.ws_serial[(long long)seq * a.heads + head], j);
+    float *w = a.ws_state + ((long long)place0 * a.heads + head) * size + at;
+    const double *decay = a.ws_decay + (long long)place0 * a.heads + head;
+    const long long step = (long long)a.heads * size;
+    constexpr int kAhead = 8;                   // parts whose loads are under way at once
+    for (int j0 = 0; j0 < parts; j0 += kAhead) {
+        f32x4 add[kAhead];
+        double log2[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = j0 + u;
+            add[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            log2[u] = 0.0;
+            if (j + 1 < parts) {
+                add[u] = *reinterpret_cast<const f32x4 *>(w + j * step);
+                log2[u] = decay[(long long)j * a.heads];
+            }
         }
-        *reinterpret_cast<f32x4 *>(w) = S;
-        S = S * f + add;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = j0 + u;
+            if (j < parts)
+                *reinterpret_cast<f32x4 *>(w + j * step) = S;
+            if (j + 1 < parts) {
+                const float f = __builtin_amdgcn_exp2f((float)log2[u]);
+                const float odd = ((S[0] + S[1]) + (S[2] + S[3])) * 0.0f;
+                if (!(f < INFINITY) || (f == 0.0f && odd != 0.0f))
+                    atomicMin(&a.ws_serial[(long long)seq * a.heads + head], j);
+                S = S * f + add[u];
+            }
+        }
     }
 }
 
@@ -982,7 +970,7 @@ __global__ __launch_bounds__(kThreads, 4) void linear_step(LArgs a)
 
 // Launch shape of a prompt, from its sizes alone.
 struct Shape {
-    int nv, col_tiles, part, places, multi;
+    int waves, col_tiles, part, places, multi;
 };
 
 constexpr int kMinPart = 256;
@@ -991,11 +979,14 @@ constexpr int kSlots = 512;     // workgroups the chip runs at once: two on each
 Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
 {
     Shape s;
-    s.nv = dk > 128 || dv <= 64 || (dv > 128 && dv <= 192) ? 1 : 2;
-    s.col_tiles = (dv + 64 * s.nv - 1) / (64 * s.nv);
-    const long long units = (long long)heads * s.col_tiles;
-    const long long most = units < kSlots ? kSlots / units : 1;
-    long long part = ((tokens + most - 1) / most + kChunk - 1) / kChunk * kChunk;
+    s.waves = dv <= 64 || (dv > 128 && dv <= 192) ? 4 : 8;
+    s.col_tiles = (dv + 16 * s.waves - 1) / (16 * s.waves);
+    // as many parts as run at once, the same number for every sequence of the
+    // average length (the lengths are on the device), none shorter than kMinPart
+    const long long units = (long long)heads * s.col_tiles * (sequences > 0 ? sequences : 1);
+    const long long per_sequence = units < kSlots ? kSlots / units : 1;
+    const long long average = sequences > 0 ? ((long long)tokens + sequences - 1) / sequences : 0;
+    long long part = ((average + per_sequence - 1) / per_sequence + kChunk - 1) / kChunk * kChunk;
     if (part < kMinPart)
         part = kMinPart;
     s.multi = part < tokens;
@@ -1019,51 +1010,46 @@ size_t workspace_of(const Shape &s, int sequences, int heads, int dk, int dv)
                    : 0;
 }
 
-hipError_t launch_one(void (*fn)(LArgs), dim3 grid, size_t lds, const LArgs &a, hipStream_t stream)
+hipError_t launch_one(void (*fn)(LArgs), dim3 grid, int threads, size_t lds, const LArgs &a, hipStream_t stream)
 {
     LArgs copy = a;
     void *params[] = {&copy};
-    return hipLaunchKernel(reinterpret_cast<const void *>(fn), grid, dim3(kThreads), params, lds, stream);
+    return hipLaunchKernel(reinterpret_cast<const void *>(fn), grid, dim3(threads), params, lds, stream);
 }
 
-template <bool H, int DK, int NV>
+template <bool H, int DK, int WAVES>
 hipError_t launch_prompt(const LArgs &a, hipStream_t stream)
 {
+    // dynamic LDS past 64 KiB has to be asked for, once
+    static const hipError_t raised = hipFuncSetAttribute(
+        reinterpret_cast<const void *>(linear_chunks<H, DK, WAVES, true>), hipFuncAttributeMaxDynamicSharedMemorySize,
+        Layout<DK, WAVES, true>::kBytes);
+    (void)raised;
     const dim3 grid((unsigned)((long long)a.places * a.heads * a.col_tiles));
     hipError_t e = hipSuccess;
     if (a.multi) {
-        e = launch_one(linear_chunks<H, DK, NV, false>, grid, Layout<DK, NV, false>::kBytes, a, stream);
+        e = launch_one(linear_chunks<H, DK, WAVES, false>, grid, 64 * WAVES, Layout<DK, WAVES, false>::kBytes, a,
+                       stream);
         const dim3 jg((unsigned)((a.dk * a.dv / 4 + kThreads - 1) / kThreads), (unsigned)a.heads,
                       (unsigned)a.sequences);
         if (e == hipSuccess)
-            e = launch_one(linear_join, jg, 0, a, stream);
+            e = launch_one(linear_join, jg, kThreads, 0, a, stream);
     }
     if (e == hipSuccess)
-        e = launch_one(linear_chunks<H, DK, NV, true>, grid, Layout<DK, NV, true>::kBytes, a, stream);
+        e = launch_one(linear_chunks<H, DK, WAVES, true>, grid, 64 * WAVES, Layout<DK, WAVES, true>::kBytes, a, stream);
     return e;
 }
 
 template <bool H>
-hipError_t launch_prompt_type(const LArgs &a, int nv, hipStream_t stream)
+hipError_t launch_prompt_type(const LArgs &a, int waves, hipStream_t stream)
 {
     if (a.dk > 128)
-        return launch_prompt<H, 256, 1>(a, stream);
+        return waves == 8 ? launch_prompt<H, 256, 8>(a, stream) : launch_prompt<H, 256, 4>(a, stream);
     if (a.dk > 64)
-        return nv == 2 ? launch_prompt<H, 128, 2>(a, stream) : launch_prompt<H, 128, 1>(a, stream);
+        return waves == 8 ? launch_prompt<H, 128, 8>(a, stream) : launch_prompt<H, 128, 4>(a, stream);
     if (a.dk > 32)
-        return nv == 2 ? launch_prompt<H, 64, 2>(a, stream) : launch_prompt<H, 64, 1>(a, stream);
-    return nv == 2 ? launch_prompt<H, 32, 2>(a, stream) : launch_prompt<H, 32, 1>(a, stream);
-}
-
-// Kernels that need more than the default 64 KiB of dynamic LDS.
-template <bool H>
-void raise_limits()
-{
-    const auto set = [](const void *fn, int bytes) {
-        (void)hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    };
-    set(reinterpret_cast<const void *>(linear_chunks<H, 128, 2, true>), Layout<128, 2, true>::kBytes);
-    set(reinterpret_cast<const void *>(linear_chunks<H, 256, 1, true>), Layout<256, 1, true>::kBytes);
+        return waves == 8 ? launch_prompt<H, 64, 8>(a, stream) : launch_prompt<H, 64, 4>(a, stream);
+    return waves == 8 ? launch_prompt<H, 32, 8>(a, stream) : launch_prompt<H, 32, 4>(a, stream);
 }
 
 constexpr long long kMaxTokenStride = 1 << 24;
@@ -1214,10 +1200,8 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
         a.ws_decay = reinterpret_cast<double *>(ws += state_bytes(s, p->heads, p->dk, p->dv));
         a.ws_serial = reinterpret_cast<int *>(ws + decay_bytes(s, p->heads));
     }
-    static const bool raised = (raise_limits<false>(), raise_limits<true>(), true);
-    (void)raised;
-    return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s.nv, (hipStream_t)stream)
-                                             : launch_prompt_type<false>(a, s.nv, (hipStream_t)stream));
+    return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s.waves, (hipStream_t)stream)
+                                             : launch_prompt_type<false>(a, s.waves, (hipStream_t)stream));
 }
 
 skinny_status skinny_linear_step(const skinny_linear_args *p, void *stream)
@@ -1229,7 +1213,7 @@ skinny_status skinny_linear_step(const skinny_linear_args *p, void *stream)
         return SKINNY_OK;
     const LArgs a = kernel_args(p);
     const dim3 grid((unsigned)((a.dv + 31) / 32), (unsigned)a.heads, (unsigned)a.sequences);
-    return launched(launch_one(p->type == SKINNY_IN_F16 ? linear_step<true> : linear_step<false>, grid, 0, a,
+    return launched(launch_one(p->type == SKINNY_IN_F16 ? linear_step<true> : linear_step<false>, grid, kThreads, 0, a,
                                (hipStream_t)stream));
 }
 
