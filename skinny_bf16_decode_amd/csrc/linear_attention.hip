@@ -223,6 +223,17 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)kSkip, 0x00020000);
 }
 
+// k is read by rows (scores) and, transposed, by columns (states), both without
+// bank conflicts: in row r, 16-byte unit u lies at u ^ h(r), so that sixteen
+// rows of one unit, and eight rows of two, fall on all 64 banks (a row of 128
+// bytes, pitch 64, covers half of them).  Byte offset of column c of row r; the
+// row pitch is a multiple of 128 bytes, so that columns can be XORed in.
+__device__ __forceinline__ unsigned key_address(int pitch, int r, int c)
+{
+    const unsigned h = (pitch >= 128 ? 2 * (r & 7) : 2 * ((r >> 1) & 3)) + ((r >> 3) & 1);
+    return (unsigned)(r * pitch) * 2 + ((((unsigned)c >> 3) ^ h) << 4) + ((unsigned)c & 7) * 2;
+}
+
 // A tile of 64 token rows of COLS 16-bit columns on its way from global memory
 // through registers to LDS.  Rows from `rows` on and columns from `cols` on
 // are zero.
@@ -260,6 +271,19 @@ struct Tile {
                 *reinterpret_cast<u32x4 *>(lds + (row + i * kRowStep) * pitch + col) = r[i];
     }
 
+    // Columns where key_address has them.
+    __device__ __forceinline__ void store_keys(unsigned short *lds, int pitch) const
+    {
+        const int row = threadIdx.x / kPerRow, col = (threadIdx.x % kPerRow) * 8;
+        char *base = reinterpret_cast<char *>(lds);
+        const unsigned at = key_address(pitch, row, col);   // kRowStep is a multiple of 8: h differs by its last bit
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            if (kRowStep <= kChunk || row < kChunk)
+                *reinterpret_cast<u32x4 *>(base + (at ^ (((i * kRowStep >> 3) & 1) << 4)) + i * kRowStep * pitch * 2) =
+                    r[i];
+    }
+
     // Columns in the order of operand_position.
     __device__ __forceinline__ void store_operands(unsigned short *lds, int pitch) const
     {
@@ -289,24 +313,57 @@ __device__ __forceinline__ u32x4 query_operand(const unsigned short *lds, int pi
     return *reinterpret_cast<const u32x4 *>(lds + (row0 + (lane & 15)) * pitch + 32 * j + 8 * (lane >> 4));
 }
 
-// MFMA operand from 16 token rows: lane (row l % 16) holds columns
+template <typename T>
+__device__ __forceinline__ const T *at_byte(const unsigned short *lds, unsigned off)
+{
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(lds) + off);
+}
+
+// MFMA operand from 16 rows of k: lane (row l % 16) holds columns
 // 32 j + 4 (l / 16) + 0..3 and the 4 columns 16 further on, the order in
 // which the state's result registers hold dk.
-__device__ __forceinline__ u32x4 row_operand(const unsigned short *lds, int pitch, int row0, int j)
+__device__ __forceinline__ u32x4 key_row_operand(const unsigned short *lds, int pitch, int row0, int j)
 {
     const int lane = threadIdx.x & 63;
-    const unsigned short *p = lds + (row0 + (lane & 15)) * pitch + 32 * j + 4 * (lane >> 4);
-    const u32x2 a = *reinterpret_cast<const u32x2 *>(p), b = *reinterpret_cast<const u32x2 *>(p + 16);
+    unsigned off = key_address(pitch, lane & 15, 4 * (lane >> 4));      // row0: a multiple of 16
+    asm volatile("" : "+v"(off));               // one address kept over the chunks, not one for every j
+    off ^= 64 * j;
+    const u32x2 a = *at_byte<u32x2>(lds + row0 * pitch, off), b = *at_byte<u32x2>(lds + row0 * pitch, off ^ 32);
     return u32x4{a.x, a.y, b.x, b.y};
 }
 
-// MFMA operand from 16 columns over the 32 tokens 32 j..: lane (column l % 16)
-// holds tokens 32 j + 4 (l / 16) + 0..3 and the 4 tokens 16 further on.  The
-// transposing LDS read gives each lane of 16 four rows of its own column.
-__device__ __forceinline__ u32x4 column_operand(const unsigned short *lds, int pitch, int col0, int j)
+// The same of 16 columns over the 32 tokens 32 j.., see column_operand.
+__device__ __forceinline__ u32x4 key_column_operand(const unsigned short *lds, int pitch, int col0, int j)
 {
     const int lane = threadIdx.x & 63, in = lane & 15;
-    const unsigned short *p = lds + (32 * j + 4 * (lane >> 4) + (in >> 2)) * pitch + col0 + 4 * (in & 3);
+    unsigned off = key_address(pitch, 4 * (lane >> 4) + (in >> 2), 4 * (in & 3));
+    asm volatile("" : "+v"(off));
+    off ^= 2 * col0;
+    const unsigned short *p = at_byte<unsigned short>(lds + 32 * j * pitch, off);
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * pitch));
+    const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+    return u32x4{x.x, x.y, y.x, y.y};
+}
+
+// Column, among the wave's 16 NV, of MFMA column m of its group n.  Two groups
+// are interleaved by fours, so that a lane's results of both, rows 4 g .. 4 g + 3
+// of the transposed output, are eight columns in a row: one 16-byte store.
+template <int NV>
+__device__ __forceinline__ int value_column(int n, int m)
+{
+    return NV == 2 ? 8 * (m >> 2) + 4 * n + (m & 3) : m;
+}
+
+// MFMA operand from column group n of v over the 32 tokens 32 j..: lane (column l % 16)
+// holds tokens 32 j + 4 (l / 16) + 0..3 and the 4 tokens 16 further on.  The
+// transposing LDS read gives each lane of 16 four rows of its own column.
+template <int NV>
+__device__ __forceinline__ u32x4 column_operand(const unsigned short *lds, int pitch, int n, int j)
+{
+    const int lane = threadIdx.x & 63, in = lane & 15;
+    const unsigned short *p = lds + (32 * j + 4 * (lane >> 4) + (in >> 2)) * pitch + value_column<NV>(n, 4 * (in & 3));
     typedef __attribute__((address_space(3))) s16x4 *lds4;
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * pitch));
@@ -354,11 +411,11 @@ __device__ __forceinline__ double chunk_decays(float g, Decays &d)
 __device__ __host__ constexpr int score_slot(int tile, int j) { return (tile < 2 ? tile : 2 * tile - 2) + j; }
 constexpr int kScoreSlots = 6;
 
-template <int DK, int WAVES, bool OUT>
+template <int DK, int WAVES, int NV, bool OUT>
 struct Layout {
-    static constexpr int kCols = 16 * WAVES;    // value columns of a workgroup
+    static constexpr int kCols = 16 * WAVES * NV;    // value columns of a workgroup
     static constexpr int kQPitch = DK + 8;      // row reads: 16 rows x 16 bytes on all banks
-    static constexpr int kKPitch = DK + 16;     // transposing reads: 8 rows x 32 bytes on all banks
+    static constexpr int kKPitch = DK < 64 ? 64 : DK;   // swizzled, see key_address
     static constexpr int kVPitch = kCols + 16;
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + (OUT ? kChunk * kQPitch * 2 : 0);
@@ -376,36 +433,37 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 // that has come here stays here for the rest of its part, and carries the
 // state in registers along unused: merging the two would cost every wave a
 // second copy of it.
-template <bool H, int DK, int WAVES, bool OUT>
+template <bool H, int DK, int WAVES, int NV, bool OUT>
 __device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds, const Decays &d, int rows, f32x4 *T,
                                       unsigned short *out, int col0)
 {
-    using L = Layout<DK, WAVES, OUT>;
+    using L = Layout<DK, WAVES, NV, OUT>;
     const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4;
     const unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
 #pragma unroll 1
-    for (int t = 0; t < rows; ++t) {
-        const float e = d.own[t], v = to_float<H>(vs[t * L::kVPitch + 16 * wave + (lane & 15)]);
+    for (int nt = 0; nt < rows * NV; ++nt) {
+        const int n = nt / rows, t = nt - n * rows;     // one column group after the other
+        const float e = d.own[t], v = to_float<H>(vs[t * L::kVPitch + 16 * NV * wave + value_column<NV>(n, lane & 15)]);
         float o = 0.0f;
 #pragma unroll 1
         for (int i = 0; i < DK / 16; ++i) {
-            f32x4 S = T[i];
+            f32x4 S = T[n * (DK / 16) + i];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int c = 16 * i + 4 * g + r;
-                const float k = to_float<H>(ks[t * L::kKPitch + c]);
+                const float k = to_float<H>(ks[key_address(L::kKPitch, t, c) / 2]);
                 // rows past dk hold no state: 0 * a v that is not finite is not theirs to add
                 const float s = c < a.dk ? S[r] * e + k * v : 0.0f;
                 S[r] = s;
                 if constexpr (OUT)
                     o += c < a.dk ? to_float<H>(qs[t * L::kQPitch + operand_position(c)]) * s : 0.0f;
             }
-            T[i] = S;
+            T[n * (DK / 16) + i] = S;
         }
         if constexpr (OUT) {
             o += __shfl_xor(o, 16, 64);
             o += __shfl_xor(o, 32, 64);
-            const int c = col0 + 16 * wave + (lane & 15);
+            const int c = col0 + 16 * NV * wave + value_column<NV>(n, lane & 15);
             if (g == 0 && c < a.dv)
                 out[t * a.out_token + c] = to_bits<H>(o * a.scale);
         }
@@ -415,18 +473,18 @@ __device__ __forceinline__ void recur(const LArgs &a, const unsigned short *lds,
 // Natural [dk][dv] state <-> result registers of the wave's columns.  Lane
 // group g holds rows 4 g .. 4 g + 3 of each 16; dk is a multiple of 8, so the
 // four are all in or all out.
-template <int DK>
-__device__ __forceinline__ unsigned state_offset(const LArgs &a, int col0)
+__device__ __forceinline__ unsigned state_offset(const LArgs &a, int c)
 {
-    const int lane = threadIdx.x & 63, c = col0 + 16 * wave_id() + (lane & 15);
+    const int lane = threadIdx.x & 63;
     return c < a.dv ? 4u * (lane >> 4) * 4u * (unsigned)a.dv + 4u * c : kSkip;
 }
 
+// c: the lane's column, of one of the wave's groups.
 template <int DK>
-__device__ __forceinline__ void load_state(const LArgs &a, const float *p, int col0, f32x4 (&S)[DK / 16])
+__device__ __forceinline__ void load_state(const LArgs &a, const float *p, int c, f32x4 (&S)[DK / 16])
 {
     const __amdgpu_buffer_rsrc_t src = make_rsrc(p);
-    const unsigned off = p ? state_offset<DK>(a, col0) : kSkip;
+    const unsigned off = p ? state_offset(a, c) : kSkip;
     const int row = 4 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int i = 0; i < DK / 16; ++i)
@@ -437,10 +495,10 @@ __device__ __forceinline__ void load_state(const LArgs &a, const float *p, int c
 }
 
 template <int DK>
-__device__ __forceinline__ void store_state(const LArgs &a, float *p, int col0, const f32x4 (&S)[DK / 16])
+__device__ __forceinline__ void store_state(const LArgs &a, float *p, int c, const f32x4 (&S)[DK / 16])
 {
     const __amdgpu_buffer_rsrc_t dst = make_rsrc(p);
-    const unsigned off = state_offset<DK>(a, col0);
+    const unsigned off = state_offset(a, c);
     const int row = 4 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int i = 0; i < DK / 16; ++i)
@@ -471,77 +529,91 @@ __device__ __forceinline__ void decayed_values(u32x4 v, const Decays &d, int j, 
 // k is exact in 16 bits; the decayed v is fp32 and goes in as three BF16 terms
 // (24 bits), or two FP16 terms after a power of two (22 bits), so the state
 // keeps fp32's accuracy on the matrix units.
-template <bool H, int DK, int WAVES, bool OUT>
-__device__ __forceinline__ void update_state(const unsigned short *lds, const Decays &d, f32x4 (&S)[DK / 16])
+template <bool H, int DK, int WAVES, int NV, bool OUT>
+__device__ __forceinline__ void update_state(const unsigned short *lds, const Decays &d, f32x4 (&S)[NV][DK / 16])
 {
-    using L = Layout<DK, WAVES, OUT>;
+    using L = Layout<DK, WAVES, NV, OUT>;
     constexpr int kTerms = H ? 2 : 3;
-    const unsigned short *ks = lds + L::kK / 2, *vs = lds + L::kV / 2 + 16 * wave_id();
+    const unsigned short *ks = lds + L::kK / 2, *vs = lds + L::kV / 2 + 16 * NV * wave_id();
     const float total = d.total;
-    if constexpr (H) {
-        float x[2][8], top = 0.0f, mul, back;
+    u32x4 f[NV][2][kTerms];
+    float back[NV];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            decayed_values<H>(column_operand(vs, L::kVPitch, 0, j), d, j, x[j]);
+    for (int n = 0; n < NV; ++n) {
+        float x[2][8];
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-                top = fmaxf(top, fabsf(x[j][p]));
+        for (int j = 0; j < 2; ++j)
+            decayed_values<H>(column_operand<NV>(vs, L::kVPitch, n, j), d, j, x[j]);
+        if constexpr (H) {
+            float top = 0.0f, mul;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    top = fmaxf(top, fabsf(x[j][p]));
+            half_range(wave_max(top), mul, back[n]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    x[j][p] *= mul;
         }
-        half_range(wave_max(top), mul, back);
-        u32x4 f[2][kTerms];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j)
+            split8<H, kTerms>(x[j], f[n][j]);
+    }
+    u32x4 k[2][2];                              // of this row tile and the next
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-                x[j][p] *= mul;
-            split8<H, kTerms>(x[j], f[j]);
+    for (int j = 0; j < 2; ++j)
+        k[0][j] = key_column_operand(ks, L::kKPitch, 0, j);
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) {
+        if (i + 1 < DK / 16) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                k[(i + 1) & 1][j] = key_column_operand(ks, L::kKPitch, 16 * (i + 1), j);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 add[NV];
 #pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-            f32x4 add = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < NV; ++n) {
+            if constexpr (H) {
+                add[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const u32x4 k = column_operand(ks, L::kKPitch, 16 * i, j);
-#pragma unroll
-                for (int m = 0; m < kTerms; ++m)
-                    add = mma16<H>(k, f[j][m], add);
+                for (int r = 0; r < 4; ++r)
+                    S[n][i][r] *= total;
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                S[i][r] = S[i][r] * total + add[r] * back;
-        }
-    } else {
-        u32x4 f[2][kTerms];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float x[8];
-            decayed_values<H>(column_operand(vs, L::kVPitch, 0, j), d, j, x);
-            split8<H, kTerms>(x, f[j]);
         }
 #pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                S[i][r] *= total;
+            for (int m = 0; m < kTerms; ++m)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const u32x4 k = column_operand(ks, L::kKPitch, 16 * i, j);
+                for (int n = 0; n < NV; ++n) {
+                    if constexpr (H)
+                        add[n] = mma16<H>(k[i & 1][j], f[n][j][m], add[n]);
+                    else
+                        S[n][i] = mma16<H>(k[i & 1][j], f[n][j][m], S[n][i]);
+                }
+        if constexpr (H) {
 #pragma unroll
-                for (int m = 0; m < kTerms; ++m)
-                    S[i] = mma16<H>(k, f[j][m], S[i]);
-            }
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[n][i][r] = S[n][i][r] * total + add[n][r] * back[n];
         }
     }
 }
 
-// One part of a sequence for one head and 16 WAVES value columns, 16 a wave.
+// One part of a sequence for one head and 16 WAVES NV value columns, 16 NV a wave.
 // OUT: outputs, and the sequence's new state after its last part.  Otherwise:
 // what the part alone adds to the state, for the parts after it.
-template <bool H, int DK, int WAVES, bool OUT>
-__global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void linear_chunks(LArgs a)
+template <bool H, int DK, int WAVES, int NV, bool OUT>
+__global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
 {
-    using L = Layout<DK, WAVES, OUT>;
-    constexpr int kGateWave = WAVES == 8 ? 4 : 0;   // it has the least of the scores to do
+    using L = Layout<DK, WAVES, NV, OUT>;
+    constexpr int kGateWave = WAVES == 8 ? 7 : 2;   // it has the least of the scores to do
     extern __shared__ __align__(16) unsigned short lds[];
     __shared__ Decays decays[2];
     __shared__ float score_back[4][2];
@@ -588,12 +660,13 @@ __global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void li
     const float *gp = a.g + tok * a.g_token + head * a.g_head;
     unsigned short *op = static_cast<unsigned short *>(a.out) + tok * a.out_token + head * a.out_head;
     const unsigned out_step = (unsigned)(2 * a.out_token);
-    const int out_col = col0 + 16 * wave + 4 * g;
+    const int wave_col = col0 + 16 * NV * wave;
+    const int out_col = wave_col + 4 * NV * g;  // dv is a multiple of 8: 4 NV columns are all in or all out
     const unsigned out_off = out_col < a.dv ? (lane & 15) * out_step + 2 * out_col : kSkip;
     const long long ws_off = ((long long)place * a.heads + head) * a.dk * a.dv;
 
-    f32x4 S[DK / 16];
-    f32x4 memory[DK / 16], *T = memory;         // the state of a wave that goes token by token
+    f32x4 S[NV][DK / 16];
+    f32x4 memory[NV * (DK / 16)], *T = memory;         // the state of a wave that goes token by token
     asm volatile("" : "+v"(T) : : "memory");    // an address of its own: not turned back into registers
     bool slow = false;
     if constexpr (OUT) {
@@ -602,16 +675,18 @@ __global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void li
             from = a.ws_state + ws_off;
         else if (a.state_in && slot >= 0)
             from = a.state_in + slot * a.in_slot + head * a.in_head;
-        load_state<DK>(a, from, col0, S);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+            load_state<DK>(a, from, wave_col + value_column<NV>(n, lane & 15), S[n]);
     }
 
     // the parts-only kernel takes a second, token by token, pass if its state is not finite
     for (int attempt = 0; attempt < 2; ++attempt) {
         if constexpr (!OUT) {
 #pragma unroll
-            for (int i = 0; i < DK / 16; ++i) {
+            for (int i = 0; i < NV * (DK / 16); ++i) {
                 T[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                S[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                S[i / (DK / 16)][i % (DK / 16)] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
         }
         Tile<DK, 64 * WAVES> tq, tk;
@@ -637,28 +712,31 @@ __global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void li
             const Decays &d = decays[c & 1];
             if constexpr (OUT)
                 tq.store_operands(qs, L::kQPitch);
-            tk.store(ks, L::kKPitch);
+            tk.store_keys(ks, L::kKPitch);
             tv.store(vs, L::kVPitch);
             __syncthreads();
-            if (c + 1 < chunks) {
-                const long long at = (long long)(c + 1) * kChunk;
-                const int left = n_tok - (c + 1) * kChunk;
-                if constexpr (OUT)
-                    tq.load(qp + at * a.q_token, left);
+            // the next chunk, a tile at a time between the products: all at once they fill the CU's queue, and
+            // the wave waits to issue them (2200 of 16700 cycles a chunk)
+            const bool more = c + 1 < chunks;
+            const long long at = (long long)(c + 1) * kChunk;
+            const int left = n_tok - (c + 1) * kChunk;
+            if (more) {
                 tk.load(kp + at * a.k_token, left);
-                tv.load(vp + at * a.v_token, left);
                 if (wave == kGateWave) {
                     sum += chunk_decays(gate, decays[(c + 1) & 1]);
                     gate = kChunk + lane < left ? gp[(at + kChunk + lane) * a.g_token] : 0.0f;
                 }
             }
             if constexpr (OUT) {
-                // masked, decayed, scaled scores of 16 tokens t with the 32 tokens of step j, over the waves
+                // masked, decayed, scaled scores of 16 tokens t with the 32 tokens of step j: the six that the
+                // causal mask leaves, (tile, step) 00 10 20 21 30 31, over the waves; of four, 0 and 1 have
+                // three tiles of 16 tokens, 2 and 3 two
 #pragma unroll
-                for (int jj = 0; jj < 8 / WAVES; ++jj) {
-                    const int tt = wave & 3, j = WAVES == 8 ? wave >> 2 : jj;
-                    if (2 * j > tt)
-                        continue;               // all later
+                for (int jj = 0; jj < (WAVES == 8 ? 1 : 2); ++jj) {
+                    const int job = WAVES == 8 ? wave : (wave < 2 ? 2 * wave + jj : (jj ? 6 : 2 + wave));
+                    if (job >= kScoreSlots)
+                        continue;
+                    const int tt = job < 2 ? job : (job + 2) >> 1, j = job < 2 ? 0 : job & 1;
                     u32x4 qf[DK / 32];
 #pragma unroll
                     for (int i = 0; i < DK / 32; ++i)
@@ -673,7 +751,7 @@ __global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void li
                         if (h == 0 || st <= tt) {
 #pragma unroll
                             for (int i = 0; i < DK / 32; ++i)
-                                sc = mma16<H>(row_operand(ks, L::kKPitch, 16 * st, i), qf[i], sc);
+                                sc = mma16<H>(key_row_operand(ks, L::kKPitch, 16 * st, i), qf[i], sc);
                         }
                         const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[16 * st + 4 * g]);
                         const f32x4 sl = *reinterpret_cast<const f32x4 *>(&d.lo[16 * st + 4 * g]);
@@ -698,49 +776,59 @@ __global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void li
                     }
                     u32x4 f[2];
                     split8<H, 2>(x, f);
-                    scores[(score_slot(tt, j) * 2 + 0) * 64 + lane] = f[0];
-                    scores[(score_slot(tt, j) * 2 + 1) * 64 + lane] = f[1];
+                    scores[(job * 2 + 0) * 64 + lane] = f[0];
+                    scores[(job * 2 + 1) * 64 + lane] = f[1];
                 }
+                if (more)
+                    tq.load(qp + at * a.q_token, left);
                 // S^T q of all 64 tokens, the state in two terms
-                f32x4 acc[4];
+                f32x4 acc[4][NV];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+                        acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 float s_mul = 1.0f, s_back = 1.0f;
                 if constexpr (H) {
                     float top = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < DK / 16; ++i)
+                    for (int n = 0; n < NV; ++n)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            top = fmaxf(top, fabsf(S[i][r]));
+                        for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                top = fmaxf(top, fabsf(S[n][i][r]));
                     half_range(wave_max(top), s_mul, s_back);
                 }
 #pragma unroll
                 for (int j = 0; j < DK / 32; ++j) {
-                    u32x4 qf[4], f[2];
+                    u32x4 qf[4], f[NV][2];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         qf[i] = query_operand(qs, L::kQPitch, 16 * i, j);
                     __builtin_amdgcn_sched_barrier(0);      // on their way while the state is split
-                    float x[8];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        x[r] = S[2 * j][r];
-                        x[4 + r] = S[2 * j + 1][r];
+                    for (int n = 0; n < NV; ++n) {
+                        float x[8];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            x[r] = S[n][2 * j][r];
+                            x[4 + r] = S[n][2 * j + 1][r];
+                        }
+                        if constexpr (H) {
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                x[r] *= s_mul;
+                        }
+                        split8<H, 2>(x, f[n]);
                     }
-                    if constexpr (H) {
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            x[r] *= s_mul;
-                    }
-                    split8<H, 2>(x, f);
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[i] = mma16<H>(f[0], qf[i], acc[i]);
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[i] = mma16<H>(f[1], qf[i], acc[i]);
+                            for (int n = 0; n < NV; ++n)
+                                acc[i][n] = mma16<H>(f[n][m], qf[i], acc[i][n]);
                 }
                 __syncthreads();
                 // + scores V; FP16 scores carry powers of two (all steps below are exact in them)
@@ -754,67 +842,94 @@ __global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void li
                         f *= s_back * inverse_power(back[i]);
                     }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][r] *= f;
+                    for (int n = 0; n < NV; ++n)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[i][n][r] *= f;
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const u32x4 vf = column_operand(vs, L::kVPitch, 16 * wave, j);
+                    u32x4 vf[NV];
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+                        vf[n] = column_operand<NV>(vs + 16 * NV * wave, L::kVPitch, n, j);
 #pragma unroll
                     for (int i = 2 * j; i < 4; ++i) {
                         if constexpr (H) {
                             if (j) {
                                 const float f = back[i] * inverse_power(score_back[i][1]);
 #pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    acc[i][r] *= f;
+                                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                                    for (int r = 0; r < 4; ++r)
+                                        acc[i][n][r] *= f;
                                 back[i] = score_back[i][1];
                             }
                         }
-                        acc[i] = mma16<H>(vf, scores[(score_slot(i, j) * 2 + 0) * 64 + lane], acc[i]);
-                        acc[i] = mma16<H>(vf, scores[(score_slot(i, j) * 2 + 1) * 64 + lane], acc[i]);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const u32x4 pf = scores[(score_slot(i, j) * 2 + m) * 64 + lane];
+#pragma unroll
+                            for (int n = 0; n < NV; ++n)
+                                acc[i][n] = mma16<H>(vf[n], pf, acc[i][n]);
+                        }
                     }
                 }
+                if (more)
+                    tv.load(vp + at * a.v_token, left);
                 // a sum is finite only if all of it is
                 float sums[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sums[i] = (acc[i][0] + acc[i][1]) + (acc[i][2] + acc[i][3]);
+                for (int i = 0; i < 4; ++i) {
+                    sums[i] = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+                        sums[i] += (acc[i][n][0] + acc[i][n][1]) + (acc[i][n][2] + acc[i][n][3]);
+                }
                 unsigned short *o = op + (long long)c * kChunk * a.out_token;
                 if (!slow && wave_any_nan(((sums[0] + sums[1]) + (sums[2] + sums[3])) * 0.0f)) {
                     slow = true;
 #pragma unroll
-                    for (int i = 0; i < DK / 16; ++i)
-                        T[i] = S[i];
+                    for (int i = 0; i < NV * (DK / 16); ++i)
+                        T[i] = S[i / (DK / 16)][i % (DK / 16)];
                 }
                 if (slow) {
-                    recur<H, DK, WAVES, OUT>(a, lds, d, rows, T, o, col0);
+                    recur<H, DK, WAVES, NV, OUT>(a, lds, d, rows, T, o, col0);
                 } else {
                     const __amdgpu_buffer_rsrc_t dst = make_rsrc(o);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        u32x2 w;
-                        w.x = pack2<H>(acc[i][0] * back[i], acc[i][1] * back[i]);
-                        w.y = pack2<H>(acc[i][2] * back[i], acc[i][3] * back[i]);
-                        __builtin_amdgcn_raw_buffer_store_b64(w, dst, 16 * i + (lane & 15) < rows ? out_off : kSkip,
-                                                              16 * i * out_step, 0);
+                        unsigned int w[2 * NV];
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            w[2 * n] = pack2<H>(acc[i][n][0] * back[i], acc[i][n][1] * back[i]);
+                            w[2 * n + 1] = pack2<H>(acc[i][n][2] * back[i], acc[i][n][3] * back[i]);
+                        }
+                        const unsigned to = 16 * i + (lane & 15) < rows ? out_off : kSkip;
+                        if constexpr (NV == 2)
+                            __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, dst, to,
+                                                                   16 * i * out_step, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b64(u32x2{w[0], w[1]}, dst, to, 16 * i * out_step, 0);
                     }
                 }
             } else {
+                if (more)
+                    tv.load(vp + at * a.v_token, left);
                 if (attempt)
-                    recur<H, DK, WAVES, OUT>(a, lds, d, rows, T, nullptr, col0);
+                    recur<H, DK, WAVES, NV, OUT>(a, lds, d, rows, T, nullptr, col0);
             }
-            update_state<H, DK, WAVES, OUT>(lds, d, S);
+            update_state<H, DK, WAVES, NV, OUT>(lds, d, S);
             __syncthreads();
         }
         if constexpr (OUT)
             break;
         float odd = 0.0f;
 #pragma unroll
-        for (int i = 0; i < DK / 16; ++i)
+        for (int i = 0; i < NV * (DK / 16); ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                odd += S[i][r] * 0.0f;
+                odd += S[i / (DK / 16)][i % (DK / 16)][r] * 0.0f;
         slow = attempt == 1;
         if (wave == kGateWave && lane == 0 && tile == 0) {
             a.ws_decay[(long long)place * a.heads + head] = sum;
@@ -832,10 +947,12 @@ __global__ __launch_bounds__(64 * WAVES, DK > 128 || WAVES == 4 ? 2 : 4) void li
     }
     if (slow) {
 #pragma unroll
-        for (int i = 0; i < DK / 16; ++i)
-            S[i] = T[i];
+        for (int i = 0; i < NV * (DK / 16); ++i)
+            S[i / (DK / 16)][i % (DK / 16)] = T[i];
     }
-    store_state<DK>(a, to, col0, S);
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+        store_state<DK>(a, to, wave_col + value_column<NV>(n, lane & 15), S[n]);
 }
 
 // State at the start of every part of the sequences that have several:
@@ -866,13 +983,9 @@ __global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
         double log2[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int j = j0 + u;
-            add[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            log2[u] = 0.0;
-            if (j + 1 < parts) {
-                add[u] = *reinterpret_cast<const f32x4 *>(w + j * step);
-                log2[u] = decay[(long long)j * a.heads];
-            }
+            const int j = min(j0 + u, parts - 1);   // the last part's place is there, and not used
+            add[u] = *reinterpret_cast<const f32x4 *>(w + j * step);
+            log2[u] = decay[(long long)j * a.heads];
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -970,7 +1083,7 @@ __global__ __launch_bounds__(kThreads, 4) void linear_step(LArgs a)
 
 // Launch shape of a prompt, from its sizes alone.
 struct Shape {
-    int waves, col_tiles, part, places, multi;
+    int cols, col_tiles, part, places, multi;
 };
 
 constexpr int kMinPart = 256;
@@ -979,8 +1092,15 @@ constexpr int kSlots = 512;     // workgroups the chip runs at once: two on each
 Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
 {
     Shape s;
-    s.waves = dv <= 64 || (dv > 128 && dv <= 192) ? 4 : 8;
-    s.col_tiles = (dv + 16 * s.waves - 1) / (16 * s.waves);
+    // 128 columns a workgroup, or 64: where there are no more, or a last tile would be half empty; and for
+    // the four-wave kernels of 64 < dk <= 128, where that makes enough workgroups of whole sequences (16
+    // prompts of 2048 tokens, 12 heads of 128: 208 against 226 us, no part is done twice), or where there are
+    // few of either (1500 tokens: 42 against 50 us)
+    const long long wide = (dv + 127) / 128, narrow = (dv + 63) / 64;
+    const bool whole = heads * narrow * sequences >= 3 * kSlots / 4 && (long long)tokens <= 4096LL * sequences;
+    const bool few = heads * wide * (tokens / kMinPart + sequences) <= 128;
+    s.cols = dv <= 64 || (dv > 128 && dv <= 192) || (dk > 64 && dk <= 128 && (whole || few)) ? 64 : 128;
+    s.col_tiles = (dv + s.cols - 1) / s.cols;
     // as many parts as run at once, the same number for every sequence of the
     // average length (the lengths are on the device), none shorter than kMinPart
     const long long units = (long long)heads * s.col_tiles * (sequences > 0 ? sequences : 1);
@@ -1017,18 +1137,18 @@ hipError_t launch_one(void (*fn)(LArgs), dim3 grid, int threads, size_t lds, con
     return hipLaunchKernel(reinterpret_cast<const void *>(fn), grid, dim3(threads), params, lds, stream);
 }
 
-template <bool H, int DK, int WAVES>
+template <bool H, int DK, int WAVES, int NV>
 hipError_t launch_prompt(const LArgs &a, hipStream_t stream)
 {
     // dynamic LDS past 64 KiB has to be asked for, once
     static const hipError_t raised = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(linear_chunks<H, DK, WAVES, true>), hipFuncAttributeMaxDynamicSharedMemorySize,
-        Layout<DK, WAVES, true>::kBytes);
+        reinterpret_cast<const void *>(linear_chunks<H, DK, WAVES, NV, true>), hipFuncAttributeMaxDynamicSharedMemorySize,
+        Layout<DK, WAVES, NV, true>::kBytes);
     (void)raised;
     const dim3 grid((unsigned)((long long)a.places * a.heads * a.col_tiles));
     hipError_t e = hipSuccess;
     if (a.multi) {
-        e = launch_one(linear_chunks<H, DK, WAVES, false>, grid, 64 * WAVES, Layout<DK, WAVES, false>::kBytes, a,
+        e = launch_one(linear_chunks<H, DK, WAVES, NV, false>, grid, 64 * WAVES, Layout<DK, WAVES, NV, false>::kBytes, a,
                        stream);
         const dim3 jg((unsigned)((a.dk * a.dv / 4 + kThreads - 1) / kThreads), (unsigned)a.heads,
                       (unsigned)a.sequences);
@@ -1036,20 +1156,20 @@ hipError_t launch_prompt(const LArgs &a, hipStream_t stream)
             e = launch_one(linear_join, jg, kThreads, 0, a, stream);
     }
     if (e == hipSuccess)
-        e = launch_one(linear_chunks<H, DK, WAVES, true>, grid, 64 * WAVES, Layout<DK, WAVES, true>::kBytes, a, stream);
+        e = launch_one(linear_chunks<H, DK, WAVES, NV, true>, grid, 64 * WAVES, Layout<DK, WAVES, NV, true>::kBytes, a, stream);
     return e;
 }
 
 template <bool H>
-hipError_t launch_prompt_type(const LArgs &a, int waves, hipStream_t stream)
+hipError_t launch_prompt_type(const LArgs &a, int cols, hipStream_t stream)
 {
     if (a.dk > 128)
-        return waves == 8 ? launch_prompt<H, 256, 8>(a, stream) : launch_prompt<H, 256, 4>(a, stream);
+        return cols == 128 ? launch_prompt<H, 256, 8, 1>(a, stream) : launch_prompt<H, 256, 4, 1>(a, stream);
     if (a.dk > 64)
-        return waves == 8 ? launch_prompt<H, 128, 8>(a, stream) : launch_prompt<H, 128, 4>(a, stream);
+        return cols == 128 ? launch_prompt<H, 128, 4, 2>(a, stream) : launch_prompt<H, 128, 4, 1>(a, stream);
     if (a.dk > 32)
-        return waves == 8 ? launch_prompt<H, 64, 8>(a, stream) : launch_prompt<H, 64, 4>(a, stream);
-    return waves == 8 ? launch_prompt<H, 32, 8>(a, stream) : launch_prompt<H, 32, 4>(a, stream);
+        return cols == 128 ? launch_prompt<H, 64, 8, 1>(a, stream) : launch_prompt<H, 64, 4, 1>(a, stream);
+    return cols == 128 ? launch_prompt<H, 32, 8, 1>(a, stream) : launch_prompt<H, 32, 4, 1>(a, stream);
 }
 
 constexpr long long kMaxTokenStride = 1 << 24;
@@ -1200,8 +1320,8 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
         a.ws_decay = reinterpret_cast<double *>(ws += state_bytes(s, p->heads, p->dk, p->dv));
         a.ws_serial = reinterpret_cast<int *>(ws + decay_bytes(s, p->heads));
     }
-    return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s.waves, (hipStream_t)stream)
-                                             : launch_prompt_type<false>(a, s.waves, (hipStream_t)stream));
+    return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s.cols, (hipStream_t)stream)
+                                             : launch_prompt_type<false>(a, s.cols, (hipStream_t)stream));
 }
 
 skinny_status skinny_linear_step(const skinny_linear_args *p, void *stream)
