@@ -436,8 +436,8 @@ skinny_status skinny_int8_prepare(const void *Wq, int N, int K, long long ldw, c
  * x_scale [M]; residual (NULL for none) and out have the plan's out type,
  * elements m * ldr + n and m * ldo + n; residual may be out itself (ldr == ldo)
  * but must not otherwise overlap out.  No allocation or synchronisation: may
- * be captured in a graph.  A plan holds the workspace of its K splits: one plan must
- * not run on two streams at once.  Different plans may.
+ * be captured in a graph.  Runs change nothing in a plan, so one plan may run on
+ * several streams at once.
  */
 skinny_status skinny_int8_run(const skinny_int8_plan *plan, const void *xq, long long ldx, const float *x_scale,
                               const void *residual, long long ldr, void *out, long long ldo, int M,

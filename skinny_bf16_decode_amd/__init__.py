@@ -181,11 +181,11 @@ def _stream_handle(stream):
     return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def stream_handle(stream, device):
-    """hipStream_t of the given stream (an object or a handle), or of the device's current one."""
+def stream_handle(stream, index):
+    """hipStream_t of the given stream (an object or a handle), or of the current one of GPU `index`."""
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 

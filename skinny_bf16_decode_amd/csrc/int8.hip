@@ -15,8 +15,8 @@
 
 // A prepared 8-bit weight.
 struct skinny_int8_plan {
-    int N, K, steps;            // steps = K / 64, rounded up
-    int pitch;                  // steps of a row tile in w: steps, made even
+    int N, K;
+    int pitch;                  // steps of a row tile in w: K / 64, rounded up to an even number
     skinny_type out;
     int device;
     void *w;                    // [N / 16][pitch][64 lanes][16 bytes], zero past N and K
@@ -249,8 +249,7 @@ struct PArgs {
     void *out;
     long long ldx, ldr, ldo;
     int M, N, K;
-    int steps;                  // K / 64, rounded up
-    int pitch;                  // steps a row tile holds in w: even, zeros past K
+    int pitch;                  // steps of 64 a row tile holds in w: even, zeros past K
     int type;                   // skinny_type of out and res
     int vec;                    // out and res take four columns at once
     int m_tiles;                // token tiles of the launch
@@ -371,14 +370,21 @@ __device__ __forceinline__ unsigned logical_id()
 }
 
 // 16 RT weight rows by 16 MT tokens a workgroup, its eight waves taking every
-// eighth K step: each holds all sums of the tile, which are added at the end
-// through LDS.  Operands go straight into registers, D steps ahead.  NT: the
+// eighth unit of two K steps: each holds all sums of the tile, which are added
+// at the end through LDS.  Loads go into registers, D units ahead.  x is read
+// in whole lines, eight rows of 128 bytes a load, and passes through the wave's
+// own LDS on its way into operands: gathered by the operands' lanes, 64 bytes
+// of 16 rows a load, it held the CU's one load path longest (64 x 7168 x 18432:
+// 53 against 36 us; x alone takes 17 us, w alone 22).  What bounds it is that
+// path: 16 K (RT + MT) bytes a workgroup, most of them w's and late (132 MB at
+// 3.6 TB/s there, 45 MB at 4.8 TB/s for one token of 6288 x 7168).  NT: the
 // weight passes by once (a single token tile) and need not stay in the caches.
 template <int RT, int MT, int D, bool NT>
 __global__ __launch_bounds__(512) void product_rows(PArgs a)
 {
     constexpr int kWaves = 8, kV = RT * MT;
-    __shared__ i32x4 part[kWaves / 2][kV][64];
+    constexpr int kUnit = 128 * MT;             // 16-byte vectors of a wave's x in LDS
+    __shared__ u32x4 shared[kWaves * kUnit > 256 * kV ? kWaves * kUnit : 256 * kV];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const unsigned id = logical_id();
     const int mt = (int)(id % (unsigned)a.m_tiles), block = (int)(id / (unsigned)a.m_tiles);
@@ -387,14 +393,15 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (long long)block * RT * a.pitch * 64,
                                                 (unsigned)(row_tiles * a.pitch) * 1024u);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + m0 * a.ldx, (unsigned)((rows - 1) * a.ldx) + (unsigned)a.K);
-    unsigned w_off[RT], x_off[MT];
+    const int units = a.pitch / 2;
+    unsigned w_off[RT], x_off[2 * MT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
         w_off[r] = (unsigned)(r * a.pitch) * 1024u + 16u * lane;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int row = 16 * t + (lane & 15);
-        x_off[t] = row < rows ? (unsigned)(row * a.ldx) + 16u * g : kSkip;
+    for (int t = 0; t < 2 * MT; ++t) {
+        const int row = 8 * t + (lane >> 3);
+        x_off[t] = row < rows ? (unsigned)(row * a.ldx) + 16u * (lane & 7) : kSkip;
     }
     i32x4 acc[RT][MT];
 #pragma unroll
@@ -402,31 +409,53 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
             acc[r][t] = i32x4{0, 0, 0, 0};
-    u32x4 wf[D][RT], xf[D][MT];
-    const auto load = [&](int d, int s) {
-        const unsigned wo = s < a.steps ? (unsigned)s * 1024u : kSkip, xo = s < a.steps ? (unsigned)s * kStep : kSkip;
+    u32x4 wf[D][2][RT], xf[D][2 * MT];
+    // past K: w is zero up to the end of its last unit, so that x may be anything there (the next row)
+    const auto load = [&](int d, int u) {
+        const unsigned wo = u < units ? (unsigned)u * 2048u : kSkip, xo = u < units ? (unsigned)u * (2 * kStep) : kSkip;
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-            wf[d][r] = __builtin_amdgcn_raw_buffer_load_b128(wr, w_off[r] + wo, 0, NT ? 2 : 0);
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+            for (int r = 0; r < RT; ++r)
+                wf[d][k][r] = __builtin_amdgcn_raw_buffer_load_b128(wr, w_off[r] + wo + 1024u * k, 0, NT ? 2 : 0);
+#pragma unroll
+        for (int t = 0; t < 2 * MT; ++t)
             xf[d][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_off[t] + xo, 0, 0);
     };
+    // 16-byte chunk c of row r lies at c ^ (r % 8): written a row at a time and
+    // read a column at a time without bank conflicts
+    u32x4 *put = shared + wave * kUnit + (lane & ~7) + ((lane & 7) ^ (lane >> 3));
+    const u32x4 *take = shared + wave * kUnit + 8 * (lane & 15);
 #pragma unroll
     for (int d = 0; d < D; ++d)
         load(d, wave + kWaves * d);
-    for (int s = wave; s < a.steps; s += kWaves * D) {
+    for (int u = wave; u < units; u += kWaves * D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int t = 0; t < 2 * MT; ++t)
+                put[64 * t] = xf[d][t];
+            __builtin_amdgcn_wave_barrier();
+            u32x4 x[2][MT];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
-                    acc[r][t] = mma64(wf[d][r], xf[d][t], acc[r][t]);
-            load(d, s + kWaves * (d + D));
+                    x[k][t] = take[128 * t + ((4 * k + g) ^ (lane & 7))];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        acc[r][t] = mma64(wf[d][k][r], x[k][t], acc[r][t]);
+            load(d, u + kWaves * (d + D));
         }
     }
     // waves 4..7 to LDS, 0..3 add theirs, all add the four
+    i32x4(*part)[kV][64] = reinterpret_cast<i32x4(*)[kV][64]>(shared);
+    __syncthreads();
     if (wave >= 4) {
 #pragma unroll
         for (int v = 0; v < kV; ++v)
@@ -598,22 +627,26 @@ hipError_t launch_quantize(const QArgs &a, int M, hipStream_t stream)
     return hipLaunchKernel(fn, dim3(M), dim3(threads), params, 0, stream);
 }
 
-template <int RT, int MT, int D, bool NT>
+// Two units ahead where there are few registers to fill (one row tile, one
+// token tile) and where the long tile's products hide them (4 x 4); one
+// elsewhere, which measured faster (3584 x 7168, 48 tokens: 11.8 against 12.9 us).
+template <int RT, int MT, bool NT>
 const void *rows_fn()
 {
-    return reinterpret_cast<const void *>(product_rows<RT, MT, D, NT>);
+    return reinterpret_cast<const void *>(product_rows<RT, MT, RT == MT && RT != 2 ? 2 : 1, NT>);
+}
+
+template <int RT, bool NT>
+const void *rows_kernel_of(int mt)
+{
+    return mt == 1 ? rows_fn<RT, 1, NT>() : mt == 2 ? rows_fn<RT, 2, NT>() : mt == 3 ? rows_fn<RT, 3, NT>()
+                                                                           : rows_fn<RT, 4, NT>();
 }
 
 template <bool NT>
 const void *rows_kernel(int rt, int mt)
 {
-    if (rt == 4)
-        return rows_fn<4, 4, 2, NT>();
-    if (rt == 2)
-        return mt == 1 ? rows_fn<2, 1, 4, NT>() : mt == 2 ? rows_fn<2, 2, 4, NT>()
-             : mt == 3 ? rows_fn<2, 3, 4, NT>() : rows_fn<2, 4, 4, NT>();
-    return mt == 1 ? rows_fn<1, 1, 8, NT>() : mt == 2 ? rows_fn<1, 2, 4, NT>()
-         : mt == 3 ? rows_fn<1, 3, 4, NT>() : rows_fn<1, 4, 4, NT>();
+    return rt == 1 ? rows_kernel_of<1, NT>(mt) : rt == 2 ? rows_kernel_of<2, NT>(mt) : rows_kernel_of<4, NT>(mt);
 }
 
 template <int T0>
@@ -653,11 +686,21 @@ hipError_t launch_product(PArgs a, hipStream_t stream)
         return hipLaunchKernel(tiles_kernel(t0),
                                dim3((unsigned)(nt * a.m_tiles)), dim3(512), params, tiles_lds(t0), stream);
     }
-    int rt = 1, mt = a.M >= 49 ? 4 : (a.M + 15) / 16;
-    if (a.M > 64)
-        rt = 4;
-    else if (a.M > 16)
-        rt = 2;
+    // the tile with the shortest way: rounds over 256 CUs, each as long as the
+    // bytes a workgroup loads.  Of equal ones the most tokens, which read the weight
+    // least often (3584 x 7168, 128 tokens: 2 x 4 14.8, 4 x 2 15.7, 4 x 4 and 2 x 2 17 us or more)
+    int rt = 0, mt = 0;
+    long long way = 0;
+    for (int t = min(4, (a.M + 15) / 16); t >= 1; --t)
+        for (int r = 1; r <= 4; r *= 2) {
+            const long long count = (long long)((a.N + 16 * r - 1) / (16 * r)) * ((a.M + 16 * t - 1) / (16 * t));
+            const long long w = (count + 255) / 256 * (r + t);
+            if (!rt || w < way) {
+                way = w;
+                rt = r;
+                mt = t;
+            }
+        }
     a.m_tiles = (a.M + 16 * mt - 1) / (16 * mt);
     a.n_tiles = (a.N + 16 * rt - 1) / (16 * rt);
     const void *fn = a.m_tiles == 1 ? rows_kernel<true>(rt, mt) : rows_kernel<false>(rt, mt);
@@ -722,7 +765,7 @@ skinny_status skinny_int8_prepare(const void *Wq, int N, int K, long long ldw, c
     const long long tiles = ((long long)N + 15) / 16, count = tiles * pitch * 64;
     if (count >= 1LL << 36 || (count + 255) / 256 > 0x7FFFFFFFLL)
         return bad(SKINNY_ERR_SHAPE, "N=%d by K=%d is too large", N, K);
-    skinny_int8_plan *p = new (std::nothrow) skinny_int8_plan{N, K, steps, pitch, out_type, 0, nullptr, nullptr};
+    skinny_int8_plan *p = new (std::nothrow) skinny_int8_plan{N, K, pitch, out_type, 0, nullptr, nullptr};
     if (!p)
         return bad(SKINNY_ERR_NOMEM, "host allocation failed");
     int cus = 0;
@@ -788,7 +831,6 @@ skinny_status skinny_int8_run(const skinny_int8_plan *p, const void *xq, long lo
     a.M = M;
     a.N = p->N;
     a.K = p->K;
-    a.steps = p->steps;
     a.pitch = p->pitch;
     a.type = p->out;
     a.vec = (uintptr_t)out % (4 * eb) == 0 && ldo % 4 == 0 && (uintptr_t)residual % (4 * eb) == 0 && ldr % 4 == 0;

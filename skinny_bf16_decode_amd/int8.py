@@ -24,23 +24,25 @@ from . import _raise, load_library, stream_handle
 TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
-def _rows(name, t, dtype, rows, cols, device):
+def _rows(name, t, dtype, rows, cols, index):
     """Checks a [>= rows, cols] matrix with contiguous rows; returns its pitch."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != cols or t.shape[0] < rows:
-        raise ValueError(f"{name} must be {dtype} [>= {rows}, {cols}], got {tuple(t.shape)} {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 2 or shape[1] != cols or shape[0] < rows:
+        raise ValueError(f"{name} must be {dtype} [>= {rows}, {cols}], got {tuple(shape)} {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} rows must have unit stride")
-    return ld if t.shape[0] > 1 else cols
+    return ld if shape[0] > 1 else cols
 
 
-def _scales(name, t, count, device):
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] < count or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous torch.float32 [>= {count}], got {tuple(t.shape)} {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+def _scales(name, t, count, index):
+    shape = t.shape
+    if t.dtype != torch.float32 or len(shape) != 1 or shape[0] < count or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous torch.float32 [>= {count}], got {tuple(shape)} {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
 
 
 def quantize_rows(x, q, scale, stream=None):
@@ -50,17 +52,19 @@ def quantize_rows(x, q, scale, stream=None):
     scale NaN, both q = 0.  Rows may be pitched; whole 16-byte vectors (8-byte
     in q) are fastest.  Capturable in a graph."""
     kind = TYPES.get(x.dtype)
-    device = x.device
-    if kind is None or x.dim() != 2 or device.type != "cuda":
+    index = x.get_device()                      # -1: not on a GPU
+    if kind is None or x.dim() != 2 or index < 0:
         raise ValueError("x must be a 2-D BF16, FP16 or fp32 tensor on a GPU")
     m, k = x.shape
     ldx, unit = x.stride()
     if unit != 1 and k > 1:
         raise ValueError("x rows must have unit stride")
-    ldq = _rows("q", q, torch.int8, m, k, device)
-    _scales("scale", scale, m, device)
-    _raise(load_library().skinny_quantize_rows(x.data_ptr(), kind, m, k, ldx if m > 1 else k, q.data_ptr(), ldq,
-                                               scale.data_ptr(), stream_handle(stream, device)))
+    ldq = _rows("q", q, torch.int8, m, k, index)
+    _scales("scale", scale, m, index)
+    status = load_library().skinny_quantize_rows(x.data_ptr(), kind, m, k, ldx if m > 1 else k, q.data_ptr(), ldq,
+                                                 scale.data_ptr(), stream_handle(stream, index))
+    if status:
+        _raise(status)
     return q, scale
 
 
@@ -68,8 +72,8 @@ class PreparedInt8:
     """A prepared 8-bit weight: a copy in the matrix units' order, with its
     channel scales.  ``weight`` is torch.int8 [N, K] with contiguous rows (a
     pitch is allowed), K a multiple of 16 below 131072; ``w_scale`` fp32 [N];
-    ``out_dtype`` BF16, FP16 or fp32.  A plan holds one workspace, so it must
-    not run on two streams at once."""
+    ``out_dtype`` BF16, FP16 or fp32.  Runs change nothing in a plan: it may
+    run on several streams at once."""
 
     def __init__(self, weight, w_scale, out_dtype=None, stream=None):
         self._plan = ctypes.c_void_p()
@@ -79,13 +83,15 @@ class PreparedInt8:
         if out_dtype not in TYPES:
             raise ValueError(f"unsupported output dtype {out_dtype}")
         self.n, self.k = weight.shape
-        ldw = _rows("weight", weight, torch.int8, self.n, self.k, weight.device)
-        _scales("w_scale", w_scale, self.n, weight.device)
+        index = weight.get_device()
+        ldw = _rows("weight", weight, torch.int8, self.n, self.k, index)
+        _scales("w_scale", w_scale, self.n, index)
         self.out_dtype = out_dtype
         self.device = weight.device
+        self._index = index
         with torch.cuda.device(self.device):
             _raise(load_library().skinny_int8_prepare(weight.data_ptr(), self.n, self.k, ldw, w_scale.data_ptr(),
-                                                      TYPES[out_dtype], stream_handle(stream, self.device),
+                                                      TYPES[out_dtype], stream_handle(stream, index),
                                                       ctypes.byref(self._plan)))
 
     def run(self, xq, x_scale, out, stream=None, residual=None):
@@ -97,16 +103,18 @@ class PreparedInt8:
         if not self._plan:
             raise ValueError("the plan is closed")
         m = xq.shape[0]
-        device = self.device
-        ldx = _rows("xq", xq, torch.int8, m, self.k, device)
-        _scales("x_scale", x_scale, m, device)
-        ldo = _rows("out", out, self.out_dtype, m, self.n, device)
+        index = self._index
+        ldx = _rows("xq", xq, torch.int8, m, self.k, index)
+        _scales("x_scale", x_scale, m, index)
+        ldo = _rows("out", out, self.out_dtype, m, self.n, index)
         res, ldr = None, 0
         if residual is not None:
-            ldr = _rows("residual", residual, self.out_dtype, m, self.n, device)
+            ldr = _rows("residual", residual, self.out_dtype, m, self.n, index)
             res = residual.data_ptr()
-        _raise(load_library().skinny_int8_run(self._plan, xq.data_ptr(), ldx, x_scale.data_ptr(), res, ldr,
-                                              out.data_ptr(), ldo, m, stream_handle(stream, device)))
+        status = load_library().skinny_int8_run(self._plan, xq.data_ptr(), ldx, x_scale.data_ptr(), res, ldr,
+                                                out.data_ptr(), ldo, m, stream_handle(stream, index))
+        if status:
+            _raise(status)
         return out
 
     def close(self):

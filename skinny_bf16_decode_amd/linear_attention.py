@@ -13,6 +13,7 @@ csrc/linear_attention.hip.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -32,41 +33,49 @@ class _Args(ctypes.Structure):
                 [("scale", ctypes.c_float)])
 
 
+# the same as bytes, which take a fifth of the time to make: decode steps of few sequences wait for this
+_ARGS = struct.Struct("@10PQ14q8if0P")
+assert _ARGS.size == ctypes.sizeof(_Args)
+
+
 def workspace_bytes(tokens: int, sequences: int, heads: int, dk: int, dv: int) -> int:
     """Bytes of workspace a prompt call of these sizes needs (may be 0)."""
     return load_library().skinny_linear_workspace(tokens, sequences, heads, dk, dv)
 
 
-def _state(name, t, heads, dk, dv, device):
-    if t.dtype != torch.float32 or t.dim() != 4 or tuple(t.shape[1:]) != (heads, dk, dv):
-        raise ValueError(f"{name} must be torch.float32 [pool, {heads}, {dk}, {dv}], got {tuple(t.shape)} {t.dtype}")
+def _state(name, t, heads, dk, dv, index):
+    shape = t.shape
+    if t.dtype != torch.float32 or len(shape) != 4 or tuple(shape[1:]) != (heads, dk, dv):
+        raise ValueError(f"{name} must be torch.float32 [pool, {heads}, {dk}, {dv}], got {tuple(shape)} {t.dtype}")
     slot, head, row, unit = t.stride()
     if unit != 1 or row != dv:
         raise ValueError(f"{name}'s [dk, dv] matrices must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
-    return slot, head
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
+    return t.data_ptr(), shape[0], slot, head
 
 
-def _ints(name, t, count, device):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != count or not t.is_contiguous():
+def _ints(name, t, count, index):
+    if t.dtype != torch.int32 or t.shape != (count,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous torch.int32 [{count}], got {tuple(t.shape)} {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
     return t.data_ptr()
 
 
 def _call(entry, q, k, v, log_decay, out, sequences, starts, state_in, state_out, slots, scale, workspace, stream):
-    kind = _TYPES.get(v.dtype)
-    device = v.device
-    if kind is None or v.dim() != 3 or device.type != "cuda":
+    dtype, shape = v.dtype, v.shape
+    kind = _TYPES.get(dtype)
+    index = v.get_device()                      # -1: not on a GPU
+    if kind is None or len(shape) != 3 or index < 0:
         raise ValueError("v must be a BF16 or FP16 [tokens, heads, dv] tensor on a GPU")
-    tokens, heads, dv = v.shape
-    if q.dim() != 3 or q.shape[0] != tokens or k.shape != q.shape:
+    tokens, heads, dv = shape
+    q_shape = q.shape
+    if len(q_shape) != 3 or q_shape[0] != tokens or k.shape != q_shape:
         raise ValueError(f"q and k must be [{tokens}, key_heads, dk] alike, got {tuple(q.shape)} and {tuple(k.shape)}")
-    key_heads, dk = q.shape[1:]
-    if out.shape != v.shape:
-        raise ValueError(f"out must have v's shape {tuple(v.shape)}, got {tuple(out.shape)}")
+    key_heads, dk = q_shape[1:]
+    if out.shape != shape:
+        raise ValueError(f"out must have v's shape {tuple(shape)}, got {tuple(out.shape)}")
     if log_decay.dtype != torch.float32 or log_decay.shape != (tokens, heads):
         raise ValueError(f"log_decay must be torch.float32 [{tokens}, {heads}], got {tuple(log_decay.shape)} "
                          f"{log_decay.dtype}")
@@ -76,38 +85,39 @@ def _call(entry, q, k, v, log_decay, out, sequences, starts, state_in, state_out
     ot, oh, ou = out.stride()
     if qu != 1 or ku != 1 or vu != 1 or ou != 1:
         raise ValueError("q, k, v and out must have a contiguous last dimension")
-    if q.dtype != v.dtype or k.dtype != v.dtype or out.dtype != v.dtype:
+    if q.dtype != dtype or k.dtype != dtype or out.dtype != dtype:
         raise ValueError(f"q, k, v and out must have one type, got {q.dtype}, {k.dtype}, {v.dtype} and {out.dtype}")
-    if q.device != device or k.device != device or out.device != device or log_decay.device != device:
+    if (q.get_device() != index or k.get_device() != index or out.get_device() != index or
+            log_decay.get_device() != index):
         raise ValueError("q, k, v, out and log_decay must be on the same device")
-    pool = 0
-    ip = op = slot_ptr = start_ptr = None
+    pool = ip = op = slot_ptr = start_ptr = wp = wb = 0
     i_slot = i_head = o_slot = o_head = 0
     if state_in is not None:
-        i_slot, i_head = _state("state_in", state_in, heads, dk, dv, device)
-        ip, pool = state_in.data_ptr(), state_in.shape[0]
+        ip, pool, i_slot, i_head = _state("state_in", state_in, heads, dk, dv, index)
     if state_out is not None:
-        o_slot, o_head = _state("state_out", state_out, heads, dk, dv, device)
-        if ip is not None and state_out.shape[0] != pool:
-            raise ValueError(f"state_in and state_out hold {pool} and {state_out.shape[0]} states")
-        op, pool = state_out.data_ptr(), state_out.shape[0]
+        op, count, o_slot, o_head = _state("state_out", state_out, heads, dk, dv, index)
+        if state_in is not None and count != pool:
+            raise ValueError(f"state_in and state_out hold {pool} and {count} states")
+        pool = count
     if slots is not None:
-        slot_ptr = _ints("slots", slots, sequences, device)
+        slot_ptr = _ints("slots", slots, sequences, index)
     if starts is not None:
-        start_ptr = _ints("starts", starts, sequences + 1, device)
-    wp, wb = None, 0
+        start_ptr = _ints("starts", starts, sequences + 1, index)
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
+        if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous and on the same device")
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        wp, wb = workspace.data_ptr(), workspace.nbytes
     if scale is None:
         scale = dk ** -0.5
     if tokens <= 1:                     # the strides of a single token say nothing
         qt = kt = vt = ot = 0
-    args = _Args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(), ip, op, start_ptr,
-                 slot_ptr, wp, wb, qt, qh, kt, kh, vt, vh, ot, oh, *log_decay.stride(), i_slot, i_head, o_slot,
-                 o_head, kind, tokens, sequences, heads, key_heads, dk, dv, pool, scale)
-    _raise(entry(ctypes.byref(args), stream_handle(stream, device)))
+    gt, gh = log_decay.stride()
+    status = entry(_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(), ip, op,
+                              start_ptr, slot_ptr, wp, wb, qt, qh, kt, kh, vt, vh, ot, oh, gt, gh, i_slot, i_head,
+                              o_slot, o_head, kind, tokens, sequences, heads, key_heads, dk, dv, pool, scale),
+                   stream_handle(stream, index))
+    if status:
+        _raise(status)
 
 
 def prompt(q, k, v, log_decay, out, starts, state_in=None, state_out=None, slots=None, scale=None, workspace=None,
