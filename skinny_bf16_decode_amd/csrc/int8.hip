@@ -254,7 +254,6 @@ struct PArgs {
     int vec;                    // out and res take four columns at once
     int m_tiles;                // token tiles of the launch
     int n_tiles;                // tiles of weight rows
-    int frags;                  // product_tiles: 16-token operands of a token tile
 };
 
 // Weight rows into MFMA operands: lane l of step s of row tile t takes row
@@ -348,6 +347,7 @@ __device__ __forceinline__ i32x4 mma64(u32x4 w, u32x4 x, i32x4 c)
 // per-lane part, the one that is checked whatever its value.
 constexpr unsigned kSkip = 0x7FF00000u;
 constexpr long long kMaxPitch = 1 << 22;
+constexpr int kMaxRows = 0x7FFFF000;     // of x and w: tiles are counted in 32 bits
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, unsigned bytes)
 {
@@ -476,16 +476,31 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
     }
 }
 
-// Many tokens: 256 weight rows by 16 `frags` tokens a workgroup of eight waves,
-// each a quarter of the rows by one half of the token operands (T0 = half of
-// them, rounded up).  Both operands are copied to LDS in MFMA order -- w lies
-// that way, x is gathered so by the lanes' addresses -- two K steps a stage,
-// one stage ahead, and read back without bank conflicts.
+// Many tokens: 256 weight rows by 32 T0 tokens a workgroup of eight waves, each
+// a quarter of the rows by half of the tokens, 4 x T0 products a K step.  Both operands are copied to LDS, two K steps a stage, as
+// many stages ahead as LDS has room for (1000 tokens: up to 3) -- w lies in MFMA order, x goes by lines, its 16-byte chunks in an
+// order without bank conflicts -- and read into registers one step ahead of the
+// products.  Bound by the matrix units and LDS side by side: 28 products of 16
+// cycles against 11 reads of 1 KiB a wave and step (T0 = 7).  Reads ahead, and
+// spread over the products, made 1000 x 7168 x 18432 228 -> 186 us at
+// T0 = 8, 4000 x 6288 x 7168 193 -> 174 us (2070 TOP/s).
+// s_waitcnt for at most `vm` vector memory and `lgkm` LDS operations under way.
+constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (vm >> 4) << 14 | 0x70 | lgkm << 8; }
+
+template <int T0>
+struct TilesLayout {
+    static constexpr int kXCopies = (T0 + 1) / 2;       // a wave's copies of x a stage
+    static constexpr int kVecs = (32 + 8 * kXCopies) * 64;
+    static constexpr int kStages = T0 == 1 ? 4 : T0 <= 4 ? 3 : 2;
+    static constexpr int kBytes = kStages * kVecs * 16;
+};
+
 template <int T0>
 __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 {
-    constexpr int kStageFrags = 2 * (16 + 2 * T0);
-    extern __shared__ u32x4 stage[];            // [2][2 steps][16 + 2 T0][64]
+    using L = TilesLayout<T0>;
+    constexpr int kStages = L::kStages, kCopies = 4 + L::kXCopies;
+    extern __shared__ u32x4 ring[];             // [kStages]: w [2 steps][16][64], x [8 kXCopies times 8 rows][64]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const int half = wave >> 2, quarter = wave & 3;
     // four token tiles by all row tiles at a time: the 32 workgroups of an XCD
@@ -494,36 +509,34 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
     const unsigned per = 4u * (unsigned)a.n_tiles, grp = id / per, in = id - grp * per;
     const unsigned width = min(4u, (unsigned)a.m_tiles - 4u * grp);
     const int mt = (int)(4u * grp + in % width), nt = (int)(in / width);
-    const int n0 = nt * 256, m0 = mt * 16 * a.frags;
-    const int row_tiles = min(16, (a.N - n0 + 15) / 16), rows = min(16 * a.frags, a.M - m0);
+    const int n0 = nt * 256, m0 = mt * 32 * T0;
+    const int row_tiles = min(16, (a.N - n0 + 15) / 16), rows = min(32 * T0, a.M - m0);
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (long long)nt * 16 * a.pitch * 64,
                                                 (unsigned)(row_tiles * a.pitch) * 1024u);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + m0 * a.ldx, (unsigned)((rows - 1) * a.ldx) + (unsigned)a.K);
     // this wave's copies of a stage: row tiles 2 wave, 2 wave + 1 of w at both
-    // steps, and token operand (wave + 8 j) / 2 at step (wave + 8 j) % 2
-    constexpr int kXCopies = (4 * T0 + 7) / 8;
-    unsigned w_off[2], x_off[kXCopies];
+    // steps, and every eighth 8 rows of x, 16-byte chunk c of row r at c ^ (r % 8)
+    unsigned w_off[2], x_off[L::kXCopies];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
         w_off[j] = (unsigned)((2 * wave + j) * a.pitch) * 1024u + 16u * lane;
 #pragma unroll
-    for (int j = 0; j < kXCopies; ++j) {
-        const int f = wave + 8 * j, row = 16 * (f >> 1) + (lane & 15);
-        x_off[j] = row < rows ? (unsigned)(row * a.ldx) + 16u * g + (f & 1) * kStep : kSkip;
+    for (int j = 0; j < L::kXCopies; ++j) {
+        const int row = 8 * (wave + 8 * j) + (lane >> 3);
+        x_off[j] = row < rows ? (unsigned)(row * a.ldx) + 16u * ((lane & 7) ^ (lane >> 3)) : kSkip;
     }
-    const auto copy = [&](int st, int buf) {
-        u32x4 *base = stage + buf * kStageFrags * 64;
+    const int stages = a.pitch / 2;
+    // the same count of copies for every stage, past the last one too: the waits below count them
+    const auto copy = [&](int st, int buf) __attribute__((always_inline)) {
+        u32x4 *base = ring + buf * L::kVecs;
+        const unsigned wo = st < stages ? (unsigned)st * 2048u : kSkip;
+        const unsigned xo = st < stages ? (unsigned)st * (2 * kStep) : kSkip;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            copy_to_lds(wr, base + ((j & 1) * (16 + 2 * T0) + 2 * wave + (j >> 1)) * 64,
-                        w_off[j >> 1] + (unsigned)(2 * st + (j & 1)) * 1024u);
+            copy_to_lds(wr, base + ((j & 1) * 16 + 2 * wave + (j >> 1)) * 64, w_off[j >> 1] + wo + (j & 1) * 1024u);
 #pragma unroll
-        for (int j = 0; j < kXCopies; ++j) {
-            const int f = wave + 8 * j;
-            if (f < 4 * T0)
-                copy_to_lds(xr, base + ((f & 1) * (16 + 2 * T0) + 16 + (f >> 1)) * 64,
-                            x_off[j] + (unsigned)st * (2 * kStep));
-        }
+        for (int j = 0; j < L::kXCopies; ++j)
+            copy_to_lds(xr, base + (32 + wave + 8 * j) * 64, x_off[j] + xo);
     };
     i32x4 acc[4][T0];
 #pragma unroll
@@ -531,34 +544,54 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 #pragma unroll
         for (int t = 0; t < T0; ++t)
             acc[i][t] = i32x4{0, 0, 0, 0};
-    const int mine = half ? a.frags - T0 : T0;  // T0 or T0 - 1
-    const int stages = a.pitch / 2;
-    copy(0, 0);
-    for (int st = 0; st < stages; ++st) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0): this wave's copies of the stage have landed
-        __syncthreads();
-        if (st + 1 < stages)
-            copy(st + 1, (st + 1) & 1);
-        const u32x4 *base = stage + (st & 1) * kStageFrags * 64 + lane;
+    u32x4 wf[2][4], xf[2][T0];
+    // operands of step k of a stage, in registers one step ahead of their products
+    const auto read = [&](int buf, int k) __attribute__((always_inline)) {
+        const u32x4 *base = ring + buf * L::kVecs;
+        const u32x4 *at = base + k * 16 * 64 + lane;
+        const u32x4 *xat = base + (32 + 2 * T0 * half) * 64 + 8 * (lane & 15) + ((4 * k + g) ^ (lane & 7));
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const u32x4 *at = base + k * (16 + 2 * T0) * 64;
-            u32x4 wf[4], xf[T0];
+        for (int i = 0; i < 4; ++i)
+            wf[k][i] = at[(4 * quarter + i) * 64];
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
+            xf[k][t] = xat[2 * t * 64];
+    };
+    const auto products = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                wf[i] = at[(4 * quarter + i) * 64];
+                acc[i][t] = mma64(wf[k][i], xf[k][t], acc[i][t]);
+        // a read after every second product: all at the start, the waves of a SIMD wait for LDS together
 #pragma unroll
-            for (int t = 0; t < T0; ++t)
-                xf[t] = at[(16 + T0 * half + t) * 64];
-#pragma unroll
-            for (int t = 0; t < T0; ++t)
-                if (t + 1 < T0 || mine == T0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[i][t] = mma64(wf[i], xf[t], acc[i][t]);
-                }
+        for (int r = 0; r < 4 + T0; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);      // products
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4 * T0, 0);
+    };
+#pragma unroll
+    for (int st = 0; st < kStages; ++st)
+        copy(st, st);
+    __builtin_amdgcn_s_waitcnt(wait_for((kStages - 1) * kCopies, 15));
+    __syncthreads();
+    read(0, 0);
+    for (int st = 0, buf = 0; st < stages; ++st) {
+        const int next = buf + 1 < kStages ? buf + 1 : 0;
+        read(buf, 1);
+        products(0);
+        __builtin_amdgcn_sched_barrier(0);
+        // this wave's copies of the next stage have landed, and it has read all of this one
+        __builtin_amdgcn_s_waitcnt(wait_for((kStages - 2) * kCopies, 0));
+        __syncthreads();
+        copy(st + kStages, buf);
+        read(next, 0);                          // after the last stage: what lies in LDS, and is not used
+        products(1);
+        __builtin_amdgcn_sched_barrier(0);
+        buf = next;
     }
+    __builtin_amdgcn_s_waitcnt(wait_for(0, 15));        // no copy outlives its workgroup's LDS
     f32x4 ws[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -566,7 +599,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 #pragma unroll
     for (int t = 0; t < T0; ++t) {
         const int m = m0 + 16 * (T0 * half + t) + (lane & 15);
-        if (t >= mine || m >= a.M)
+        if (m >= a.M)
             continue;
         const float xs = a.x_scale[m];
 #pragma unroll
@@ -577,6 +610,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
         }
     }
 }
+
 
 // ---------------------------------------------------------------------------
 // Host side
@@ -661,58 +695,78 @@ const void *tiles_kernel(int t0)
          : t0 == 5 ? tiles_fn<5>() : t0 == 6 ? tiles_fn<6>() : t0 == 7 ? tiles_fn<7>() : tiles_fn<8>();
 }
 
-constexpr size_t tiles_lds(int t0) { return (size_t)2 * 2 * (16 + 2 * t0) * 1024; }
+int tiles_lds(int t0)
+{
+    return t0 == 1 ? TilesLayout<1>::kBytes : t0 == 2 ? TilesLayout<2>::kBytes : t0 == 3 ? TilesLayout<3>::kBytes
+         : t0 == 4 ? TilesLayout<4>::kBytes : t0 == 5 ? TilesLayout<5>::kBytes : t0 == 6 ? TilesLayout<6>::kBytes
+         : t0 == 7 ? TilesLayout<7>::kBytes : TilesLayout<8>::kBytes;
+}
 
+// A tile shape and the time of its rounds over 256 CUs, in us over K = 7168
+// (other K change both kernels' alike).
+struct Tiling {
+    int r, t;                   // 16 r rows by 16 t tokens, or 256 rows by 32 t tokens
+    float us;
+};
+
+// product_rows: a round is as long as the bytes a workgroup loads, 2.25 us
+// (r + t).  Of equal ones the most tokens, which read the weight least often
+// (3584 x 7168, 128 tokens: 2 x 4 14.8, 4 x 2 15.7, 4 x 4 and 2 x 2 17 us or more).
+Tiling rows_tiling(int M, int N)
+{
+    Tiling best{0, 0, 0.0f};
+    for (int t = min(4, (M + 15) / 16); t >= 1; --t)
+        for (int r = 1; r <= 4; r *= 2) {
+            const long long count = (long long)((N + 16 * r - 1) / (16 * r)) * ((M + 16 * t - 1) / (16 * t));
+            const float us = (float)((count + 255) / 256) * 2.25f * (float)(r + t);
+            if (!best.r || us < best.us)
+                best = Tiling{r, t, us};
+        }
+    return best;
+}
+
+// product_tiles: a round measured at 6288 rows and 200 to 4000 tokens; three
+// stages fit LDS up to t = 4, two above.
+Tiling tiles_tiling(int M, int N)
+{
+    static const float round_us[9] = {0.0f, 36.0f, 41.0f, 47.0f, 51.0f, 73.0f, 76.0f, 83.0f, 89.0f};
+    Tiling best{0, 0, 0.0f};
+    for (int t = 8; t >= 1; --t) {
+        const long long count = ((long long)N + 255) / 256 * ((M + 32 * t - 1) / (32 * t));
+        const float us = (float)((count + 255) / 256) * round_us[t];
+        if (!best.r || us < best.us)
+            best = Tiling{16, t, us};
+    }
+    return best;
+}
+
+// Up to 64 tokens the rows kernel reads the weight once.  Above, the shorter
+// of both: 400 tokens of 6288 x 7168 54 against 42 us, of 3584 x 7168 26
+// against 36 us, 800 of 1500 x 7168 25 against 29 us.
 hipError_t launch_product(PArgs a, hipStream_t stream)
 {
     void *params[] = {&a};
-    if (a.M > 384) {
-        // token tile: rounds over 256 CUs, each as long as its LDS traffic (48 + 5 frags KiB a K step)
-        int best = 16;
-        long long best_cost = 0;
-        const long long nt = (a.N + 255) / 256;
-        for (int f = 16; f >= 2; --f) {
-            const long long tiles = nt * ((a.M + 16 * f - 1) / (16 * f));
-            const long long cost = (tiles + 255) / 256 * (48 + 5 * f);
-            if (!best_cost || cost < best_cost) {
-                best_cost = cost;
-                best = f;
-            }
+    const Tiling rows = rows_tiling(a.M, a.N);
+    if (a.M > 64) {
+        const Tiling tiles = tiles_tiling(a.M, a.N);
+        if (tiles.us < rows.us) {
+            a.n_tiles = (a.N + 255) / 256;
+            a.m_tiles = (a.M + 32 * tiles.t - 1) / (32 * tiles.t);
+            return hipLaunchKernel(tiles_kernel(tiles.t), dim3((unsigned)((long long)a.n_tiles * a.m_tiles)),
+                                   dim3(512), params, (size_t)tiles_lds(tiles.t), stream);
         }
-        a.frags = best;
-        a.n_tiles = (int)nt;
-        a.m_tiles = (a.M + 16 * best - 1) / (16 * best);
-        const int t0 = (best + 1) / 2;
-        return hipLaunchKernel(tiles_kernel(t0),
-                               dim3((unsigned)(nt * a.m_tiles)), dim3(512), params, tiles_lds(t0), stream);
     }
-    // the tile with the shortest way: rounds over 256 CUs, each as long as the
-    // bytes a workgroup loads.  Of equal ones the most tokens, which read the weight
-    // least often (3584 x 7168, 128 tokens: 2 x 4 14.8, 4 x 2 15.7, 4 x 4 and 2 x 2 17 us or more)
-    int rt = 0, mt = 0;
-    long long way = 0;
-    for (int t = min(4, (a.M + 15) / 16); t >= 1; --t)
-        for (int r = 1; r <= 4; r *= 2) {
-            const long long count = (long long)((a.N + 16 * r - 1) / (16 * r)) * ((a.M + 16 * t - 1) / (16 * t));
-            const long long w = (count + 255) / 256 * (r + t);
-            if (!rt || w < way) {
-                way = w;
-                rt = r;
-                mt = t;
-            }
-        }
-    a.m_tiles = (a.M + 16 * mt - 1) / (16 * mt);
-    a.n_tiles = (a.N + 16 * rt - 1) / (16 * rt);
-    const void *fn = a.m_tiles == 1 ? rows_kernel<true>(rt, mt) : rows_kernel<false>(rt, mt);
-    return hipLaunchKernel(fn, dim3((unsigned)((long long)a.n_tiles * a.m_tiles)),
-                           dim3(512), params, 0, stream);
+    a.m_tiles = (a.M + 16 * rows.t - 1) / (16 * rows.t);
+    a.n_tiles = (a.N + 16 * rows.r - 1) / (16 * rows.r);
+    const void *fn = a.m_tiles == 1 ? rows_kernel<true>(rows.r, rows.t) : rows_kernel<false>(rows.r, rows.t);
+    return hipLaunchKernel(fn, dim3((unsigned)((long long)a.n_tiles * a.m_tiles)), dim3(512), params, 0, stream);
 }
 
 void raise_limits()
 {
     for (int t0 = 1; t0 <= 8; ++t0)
         (void)hipFuncSetAttribute(tiles_kernel(t0),
-                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)tiles_lds(t0));
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, tiles_lds(t0));
 }
 
 }  // namespace
@@ -755,6 +809,8 @@ skinny_status skinny_int8_prepare(const void *Wq, int N, int K, long long ldw, c
         return bad(SKINNY_ERR_INVALID_ARG, "Wq or w_scale is NULL, or N=%d, K=%d is not positive", N, K);
     if (!is_type((int)out_type))
         return bad(SKINNY_ERR_INVALID_ARG, "output type %d is none of BF16, F32 and F16", (int)out_type);
+    if (N > kMaxRows)
+        return bad(SKINNY_ERR_SHAPE, "N=%d: at most %d", N, kMaxRows);
     if (K % 16 || K >= 131072)
         return bad(SKINNY_ERR_SHAPE, "K=%d must be a multiple of 16 below 131072", K);
     if (ldw < K)
@@ -808,6 +864,8 @@ skinny_status skinny_int8_run(const skinny_int8_plan *p, const void *xq, long lo
         return bad(SKINNY_ERR_INVALID_ARG, "plan is NULL");
     if (M < 0)
         return bad(SKINNY_ERR_INVALID_ARG, "M=%d is negative", M);
+    if (M > kMaxRows)
+        return bad(SKINNY_ERR_SHAPE, "M=%d: at most %d", M, kMaxRows);
     if (M == 0)
         return SKINNY_OK;
     if (!xq || !x_scale || !out)

@@ -69,6 +69,12 @@ def test_int8_prepare_refusals(w, n, k, ldw, ws, out, want):
     assert sk.last_error()
 
 
+def test_int8_prepare_refuses_rows_past_its_counts():
+    plan = ctypes.c_void_p(123)
+    st = sk.load_library().skinny_int8_prepare(P, 0x7FFFF001, 16, 16, P, 0, None, ctypes.byref(plan))
+    assert st == SHAPE and plan.value is None and "at most" in sk.last_error()
+
+
 def test_int8_null_plans():
     lib = sk.load_library()
     assert lib.skinny_int8_prepare(P, 16, 64, 64, P, 0, None, None) == INVALID
