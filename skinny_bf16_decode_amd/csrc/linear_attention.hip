@@ -1086,33 +1086,43 @@ struct Shape {
     int cols, col_tiles, part, places, multi;
 };
 
-constexpr int kMinPart = 256;
 constexpr int kSlots = 512;     // workgroups the chip runs at once: two on each of 256 CUs
+constexpr int kOnePass = 384;   // tokens up to which nothing is done in parts
+
+// Tokens of a part, for workgroups of `cols` columns.  The average is all that
+// the host knows of the lengths.
+int part_of(int tokens, int sequences, int heads, int dv, int cols)
+{
+    const long long columns = (long long)heads * ((dv + cols - 1) / cols), count = sequences > 0 ? sequences : 1;
+    const long long average = ((long long)tokens + count - 1) / count;
+    // as many parts as run at once, the same number for every sequence of the average length
+    const long long units = columns * count, per_sequence = units < kSlots ? kSlots / units : 1;
+    const long long even = ((average + per_sequence - 1) / per_sequence + kChunk - 1) / kChunk * kChunk;
+    // none shorter than 192 tokens: parts are done twice.  While there are CUs left, of 64 tokens, since a lone
+    // workgroup waits most of a chunk's 5 us (27 sequences, 5022 tokens, one head: parts of 64, 128, 256 30, 36,
+    // 52 us).  Where sequences are short, only the far longer ones are cut
+    const auto fits = [&](int part, int most) { return columns * (tokens / part + count) <= most; };
+    const int least = average < 80 ? kOnePass : fits(64, 160) ? 64 : fits(192, kSlots) ? 192 : 256;
+    return (int)(even > least ? even : least);
+}
 
 Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
 {
     Shape s;
-    // 128 columns a workgroup, or 64: where there are no more, or a last tile would be half empty; and for
-    // the four-wave kernels of 64 < dk <= 128, where that makes enough workgroups of whole sequences (16
-    // prompts of 2048 tokens, 12 heads of 128: 208 against 226 us, no part is done twice), or where there are
-    // few of either (1500 tokens: 42 against 50 us)
-    const long long wide = (dv + 127) / 128, narrow = (dv + 63) / 64;
-    const bool whole = heads * narrow * sequences >= 3 * kSlots / 4 && (long long)tokens <= 4096LL * sequences;
-    const bool few = heads * wide * (tokens / kMinPart + sequences) <= 128;
-    s.cols = dv <= 64 || (dv > 128 && dv <= 192) || (dk > 64 && dk <= 128 && (whole || few)) ? 64 : 128;
+    // 128 columns a workgroup, or 64: where there are no more, or a last tile would be half empty; where the
+    // wide ones leave many CUs with one workgroup or none; and where that makes enough workgroups of whole
+    // sequences, of which no part is done twice (16 prompts of 2048 tokens, 12 heads of 128: 181 against 203 us)
+    const int part = part_of(tokens, sequences, heads, dv, 128);
+    const long long wide = (dv + 127) / 128, narrow = (dv + 63) / 64, parts = tokens / part;
+    const bool few = heads * wide * (parts > sequences ? parts : sequences) <= 300;
+    const bool whole = heads * wide * sequences <= 300 && heads * narrow * sequences >= 3 * kSlots / 4 &&
+                       (long long)tokens <= 4096LL * sequences;
+    s.cols = dv <= 64 || (dv > 128 && dv <= 192) || few || whole ? 64 : 128;
     s.col_tiles = (dv + s.cols - 1) / s.cols;
-    // as many parts as run at once, the same number for every sequence of the
-    // average length (the lengths are on the device), none shorter than kMinPart
-    const long long units = (long long)heads * s.col_tiles * (sequences > 0 ? sequences : 1);
-    const long long per_sequence = units < kSlots ? kSlots / units : 1;
-    const long long average = sequences > 0 ? ((long long)tokens + sequences - 1) / sequences : 0;
-    long long part = ((average + per_sequence - 1) / per_sequence + kChunk - 1) / kChunk * kChunk;
-    if (part < kMinPart)
-        part = kMinPart;
-    s.multi = part < tokens;
+    s.part = s.cols == 128 ? part : part_of(tokens, sequences, heads, dv, 64);
+    s.multi = tokens > kOnePass && s.part < tokens;
     if (!s.multi)                               // past every start: sequence i is place i
-        part = ((long long)tokens / kChunk + 1) * kChunk;
-    s.part = (int)part;
+        s.part = (tokens / kChunk + 1) * kChunk;
     s.places = tokens / s.part + sequences;
     return s;
 }
