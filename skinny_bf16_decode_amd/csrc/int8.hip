@@ -477,15 +477,29 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
 }
 
 // Many tokens: 256 weight rows by 32 T0 tokens a workgroup of eight waves, each
-// a quarter of the rows by half of the tokens, 4 x T0 products a K step.  Both operands are copied to LDS, two K steps a stage, as
-// many stages ahead as LDS has room for (1000 tokens: up to 3) -- w lies in MFMA order, x goes by lines, its 16-byte chunks in an
-// order without bank conflicts -- and read into registers one step ahead of the
+// a quarter of the rows by half of the tokens, 4 x T0 products a K step.  Both
+// operands are copied to LDS, two K steps a stage and up to three stages ahead
+// -- w lies in MFMA order, x goes by lines, its 16-byte chunks in an order
+// without bank conflicts -- and read into registers one step ahead of the
 // products.  Bound by the matrix units and LDS side by side: 28 products of 16
 // cycles against 11 reads of 1 KiB a wave and step (T0 = 7).  Reads ahead, and
-// spread over the products, made 1000 x 7168 x 18432 228 -> 186 us at
-// T0 = 8, 4000 x 6288 x 7168 193 -> 174 us (2070 TOP/s).
+// spread over the products, made 4000 x 6288 x 7168 193 -> 166 us (2180 TOP/s;
+// the library's product alone, without scales, 178 us); a third stage at T0 = 3
+// made 800 x 6288 x 7168 65 -> 51 us.
 // s_waitcnt for at most `vm` vector memory and `lgkm` LDS operations under way.
 constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (vm >> 4) << 14 | 0x70 | lgkm << 8; }
+
+// Waits until at most VM of this wave's copies to LDS and LGKM of its LDS reads
+// are under way, then for the workgroup.  Not __syncthreads, which may wait for
+// every copy.
+template <int VM, int LGKM>
+__device__ __forceinline__ void landed()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_for(VM, LGKM));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
 template <int T0>
 struct TilesLayout {
@@ -574,8 +588,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 #pragma unroll
     for (int st = 0; st < kStages; ++st)
         copy(st, st);
-    __builtin_amdgcn_s_waitcnt(wait_for((kStages - 1) * kCopies, 15));
-    __syncthreads();
+    landed<(kStages - 1) * kCopies, 15>();
     read(0, 0);
     for (int st = 0, buf = 0; st < stages; ++st) {
         const int next = buf + 1 < kStages ? buf + 1 : 0;
@@ -583,8 +596,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
         products(0);
         __builtin_amdgcn_sched_barrier(0);
         // this wave's copies of the next stage have landed, and it has read all of this one
-        __builtin_amdgcn_s_waitcnt(wait_for((kStages - 2) * kCopies, 0));
-        __syncthreads();
+        landed<(kStages - 2) * kCopies, 0>();
         copy(st + kStages, buf);
         read(next, 0);                          // after the last stage: what lies in LDS, and is not used
         products(1);
