@@ -56,6 +56,7 @@ struct LArgs {
     int part;                   // tokens of a part of a sequence, a multiple of 64
     int places;                 // parts a launch provides for
     int col_tiles;              // workgroups along dv
+    int groups;                 // key heads of all places
     int multi;                  // a sequence may have more than one part
     float scale;
 };
@@ -187,21 +188,25 @@ __device__ __forceinline__ float inverse_power(float p) { return __uint_as_float
 // Whether any lane of the wave saw a value that is not finite: acc gathers x * 0.
 __device__ __forceinline__ bool wave_any_nan(float acc) { return __ballot(acc != 0.0f) != 0ull; }
 
-// The place of a workgroup: its sequence is the last that starts at or before it.
-__device__ __forceinline__ bool locate(const LArgs &a, int place, Place &p)
+// The place of a workgroup, see linear_places.h; false if it is empty.
+__device__ __forceinline__ bool locate(const LArgs &a, int block, int &place, Place &p)
 {
-    const int lane = threadIdx.x & 63;
-    int count = 0;
-    for (int i0 = 0; i0 < a.sequences; i0 += 64) {
-        const int i = i0 + lane;
-        bool at = false;
-        if (i < a.sequences)
-            at = first_place(a.starts[i], a.tokens, a.part, i) <= place;
-        count += __popcll(__ballot(at));
+    int seq = block;
+    if (block >= a.sequences) {
+        const int lane = threadIdx.x & 63;
+        int count = 0;
+        for (int i0 = 0; i0 < a.sequences; i0 += 64) {
+            const int i = i0 + lane;
+            bool by = false;
+            if (i < a.sequences)
+                by = extra_starts_by(a.starts[i], a.tokens, a.part, block - a.sequences);
+            count += __popcll(__ballot(by));
+        }
+        if (count == 0)
+            return false;
+        seq = __builtin_amdgcn_readfirstlane(count - 1);
     }
-    if (count == 0)
-        return false;
-    const int seq = __builtin_amdgcn_readfirstlane(count - 1);
+    place = block_place(a.starts[seq], a.tokens, a.part, a.sequences, block, seq);
     return place_of(a.starts[seq], a.starts[seq + 1], a.tokens, a.part, place, seq, p);
 }
 
@@ -621,16 +626,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
     unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
     u32x4 *scores = reinterpret_cast<u32x4 *>(lds + L::kScores / 2);
 
-    // consecutive logical ids -- the column tiles of a head, the heads that
-    // share keys -- on one XCD, whose L2 then serves their common q and k
-    const unsigned xcd = blockIdx.x & 7u, turn = blockIdx.x >> 3, q8 = gridDim.x >> 3, r8 = gridDim.x & 7u;
-    const unsigned id = xcd * q8 + (xcd < r8 ? xcd : r8) + turn;
+    // the workgroups that share keys -- the column tiles of a head, the heads of a key head -- on one XCD, whose
+    // L2 then serves their common q and k; the next such group on the next XCD
+    const unsigned xcd = blockIdx.x & 7u, turn = blockIdx.x >> 3, of_group = (unsigned)(a.share * a.col_tiles);
+    const unsigned eight = turn / of_group, group = eight * 8u + xcd;
+    if (group >= (unsigned)a.groups)
+        return;
+    const unsigned id = group * of_group + (turn - eight * of_group);
     const int tile = (int)(id % (unsigned)a.col_tiles);
     const unsigned hp = id / (unsigned)a.col_tiles;
-    const int head = (int)(hp % (unsigned)a.heads), place = (int)(hp / (unsigned)a.heads);
+    const int head = (int)(hp % (unsigned)a.heads), block = (int)(hp / (unsigned)a.heads);
 
     Place p;
-    if (!locate(a, place, p))
+    int place;
+    if (!locate(a, block, place, p))
         return;
     const int parts = parts_of(p.len, a.part);
     if (!OUT && p.part == parts - 1)
@@ -1084,6 +1093,7 @@ __global__ __launch_bounds__(kThreads, 4) void linear_step(LArgs a)
 // Launch shape of a prompt, from its sizes alone.
 struct Shape {
     int cols, col_tiles, part, places, multi;
+    int eight;                  // eight waves of 16 columns, one workgroup a CU, in place of four of 32
 };
 
 constexpr int kSlots = 512;     // workgroups the chip runs at once: two on each of 256 CUs
@@ -1111,15 +1121,24 @@ Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
     Shape s;
     // 128 columns a workgroup, or 64: where there are no more, or a last tile would be half empty; where the
     // wide ones leave many CUs with one workgroup or none; and where that makes enough workgroups of whole
-    // sequences, of which no part is done twice (16 prompts of 2048 tokens, 12 heads of 128: 181 against 203 us)
+    // sequences, of which no part is done twice (24 sequences of 12001 tokens, 12 heads, dk 64: 88 against 96 us)
     const int part = part_of(tokens, sequences, heads, dv, 128);
     const long long wide = (dv + 127) / 128, narrow = (dv + 63) / 64, parts = tokens / part;
     const bool few = heads * wide * (parts > sequences ? parts : sequences) <= 300;
     const bool whole = heads * wide * sequences <= 300 && heads * narrow * sequences >= 3 * kSlots / 4 &&
                        (long long)tokens <= 4096LL * sequences;
-    s.cols = dv <= 64 || (dv > 128 && dv <= 192) || few || whole ? 64 : 128;
+    // 64 < dk <= 128: one workgroup of eight waves a CU, sequences uncut, where there are that many and few more
+    // (16 prompts of 2048 tokens, 12 heads of 128: 149 us); two of four waves a CU past that, which wait less in
+    // all (24 prompts: 254 against 282 us)
+    const long long units = heads * wide * sequences, average = sequences > 0 ? tokens / sequences : 0;
+    const bool middle = dk > 64 && dk <= 128 && dv > 64 && (dv <= 128 || dv > 192);
+    s.eight = middle && units <= kSlots / 2 && average <= 4096 && (units >= 128 || (units >= 96 && average <= 384));
+    const bool many = middle && units > kSlots / 2;
+    s.cols = dv <= 64 || (dv > 128 && dv <= 192) || ((few || whole) && !s.eight && !many) ? 64 : 128;
     s.col_tiles = (dv + s.cols - 1) / s.cols;
     s.part = s.cols == 128 ? part : part_of(tokens, sequences, heads, dv, 64);
+    if (s.eight)                                // room for lengths about the average
+        s.part = (int)((average + average / 8) / kChunk + 1) * kChunk;
     s.multi = tokens > kOnePass && s.part < tokens;
     if (!s.multi)                               // past every start: sequence i is place i
         s.part = (tokens / kChunk + 1) * kChunk;
@@ -1155,7 +1174,7 @@ hipError_t launch_prompt(const LArgs &a, hipStream_t stream)
         reinterpret_cast<const void *>(linear_chunks<H, DK, WAVES, NV, true>), hipFuncAttributeMaxDynamicSharedMemorySize,
         Layout<DK, WAVES, NV, true>::kBytes);
     (void)raised;
-    const dim3 grid((unsigned)((long long)a.places * a.heads * a.col_tiles));
+    const dim3 grid((unsigned)(((long long)a.groups + 7) / 8 * 8 * a.share * a.col_tiles));
     hipError_t e = hipSuccess;
     if (a.multi) {
         e = launch_one(linear_chunks<H, DK, WAVES, NV, false>, grid, 64 * WAVES, Layout<DK, WAVES, NV, false>::kBytes, a,
@@ -1171,15 +1190,17 @@ hipError_t launch_prompt(const LArgs &a, hipStream_t stream)
 }
 
 template <bool H>
-hipError_t launch_prompt_type(const LArgs &a, int cols, hipStream_t stream)
+hipError_t launch_prompt_type(const LArgs &a, const Shape &s, hipStream_t stream)
 {
+    const bool wide = s.cols == 128;
     if (a.dk > 128)
-        return cols == 128 ? launch_prompt<H, 256, 8, 1>(a, stream) : launch_prompt<H, 256, 4, 1>(a, stream);
+        return wide ? launch_prompt<H, 256, 8, 1>(a, stream) : launch_prompt<H, 256, 4, 1>(a, stream);
     if (a.dk > 64)
-        return cols == 128 ? launch_prompt<H, 128, 4, 2>(a, stream) : launch_prompt<H, 128, 4, 1>(a, stream);
+        return s.eight ? launch_prompt<H, 128, 8, 1>(a, stream)
+               : wide  ? launch_prompt<H, 128, 4, 2>(a, stream) : launch_prompt<H, 128, 4, 1>(a, stream);
     if (a.dk > 32)
-        return cols == 128 ? launch_prompt<H, 64, 8, 1>(a, stream) : launch_prompt<H, 64, 4, 1>(a, stream);
-    return cols == 128 ? launch_prompt<H, 32, 8, 1>(a, stream) : launch_prompt<H, 32, 4, 1>(a, stream);
+        return wide ? launch_prompt<H, 64, 8, 1>(a, stream) : launch_prompt<H, 64, 4, 1>(a, stream);
+    return wide ? launch_prompt<H, 32, 8, 1>(a, stream) : launch_prompt<H, 32, 4, 1>(a, stream);
 }
 
 constexpr long long kMaxTokenStride = 1 << 24;
@@ -1208,6 +1229,8 @@ skinny_status check_linear(const skinny_linear_args *p, bool prompt)
     if (p->heads < 1 || p->heads > 65535 || p->key_heads < 1 || p->heads % p->key_heads)
         return bad(SKINNY_ERR_SHAPE, "heads=%d must be 1..65535 and a multiple of key_heads=%d", p->heads,
                    p->key_heads);
+    if (p->tokens > 0x7FFFF000)
+        return bad(SKINNY_ERR_SHAPE, "tokens=%d: at most %d", p->tokens, 0x7FFFF000);
     if (p->sequences > 65535)
         return bad(SKINNY_ERR_SHAPE, "sequences=%d: at most 65535", p->sequences);
     if (p->dk < 8 || p->dk > 256 || p->dk % 8 || p->dv < 8 || p->dv > 1024 || p->dv % 8)
@@ -1297,7 +1320,7 @@ extern "C" {
 
 size_t skinny_linear_workspace(int tokens, int sequences, int heads, int dk, int dv)
 {
-    if (tokens < 0 || sequences < 0 || heads < 1 || dk < 8 || dk > 256 || dv < 8 || dv > 1024)
+    if (tokens < 0 || tokens > 0x7FFFF000 || sequences < 0 || heads < 1 || dk < 8 || dk > 256 || dv < 8 || dv > 1024)
         return 0;
     return workspace_of(shape_of(tokens, sequences, heads, dk, dv), sequences, heads, dk, dv);
 }
@@ -1310,7 +1333,7 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
     if (p->sequences == 0)
         return SKINNY_OK;
     const Shape s = shape_of(p->tokens, p->sequences, p->heads, p->dk, p->dv);
-    if ((long long)s.places * p->heads * s.col_tiles > 0x7FFFFFFFLL)
+    if ((long long)s.places * p->heads * s.col_tiles > 0x7F000000LL)
         return bad(SKINNY_ERR_SHAPE, "tokens=%d, sequences=%d and heads=%d are too many for one call", p->tokens,
                    p->sequences, p->heads);
     const size_t need = workspace_of(s, p->sequences, p->heads, p->dk, p->dv);
@@ -1323,6 +1346,7 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
     a.part = s.part;
     a.places = s.places;
     a.col_tiles = s.col_tiles;
+    a.groups = s.places * p->key_heads;
     a.multi = s.multi;
     if (s.multi) {
         char *ws = static_cast<char *>(p->workspace);
@@ -1330,8 +1354,8 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
         a.ws_decay = reinterpret_cast<double *>(ws += state_bytes(s, p->heads, p->dk, p->dv));
         a.ws_serial = reinterpret_cast<int *>(ws + decay_bytes(s, p->heads));
     }
-    return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s.cols, (hipStream_t)stream)
-                                             : launch_prompt_type<false>(a, s.cols, (hipStream_t)stream));
+    return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s, (hipStream_t)stream)
+                                             : launch_prompt_type<false>(a, s, (hipStream_t)stream));
 }
 
 skinny_status skinny_linear_step(const skinny_linear_args *p, void *stream)

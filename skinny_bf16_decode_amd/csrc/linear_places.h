@@ -41,4 +41,24 @@ SKINNY_HD bool place_of(int start, int end, int tokens, int size, int place, int
     return p.part >= 0 && p.part < parts_of(p.len, size);
 }
 
+// Workgroups take the places in another order: block b < sequences the first
+// part of sequence b, and block sequences + e the extra part e: sequence i has
+// those from starts[i] / size on, as many as it has parts less one.  The parts
+// that are surely there come first, so that they fill the chip evenly; most of
+// the extra ones may be empty (16 prompts of 700 tokens, 12 heads, the places
+// in their own order: 36 of 192 workgroups on one XCD of 32 CUs, 121 against
+// 66 us).  A sequence of more than j whole parts ends past starts / size + j,
+// where the next one's extra parts begin, so the sequence of extra part e is
+// the last one with starts / size <= e.
+SKINNY_HD bool extra_starts_by(int start, int tokens, int size, int extra)
+{
+    return cut_to(start, 0, tokens) / size <= extra;
+}
+
+// Place of block b, `seq` being b or the extra part's sequence.
+SKINNY_HD int block_place(int start, int tokens, int size, int sequences, int block, int seq)
+{
+    return block < sequences ? first_place(start, tokens, size, block) : block - sequences + 1 + seq;
+}
+
 }  // namespace skinny
