@@ -483,7 +483,7 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
 // without bank conflicts -- and read into registers one step ahead of the
 // products.  Bound by the matrix units and LDS side by side: 28 products of 16
 // cycles against 11 reads of 1 KiB a wave and step (T0 = 7).  Reads ahead, and
-// spread over the products, made 4000 x 6288 x 7168 193 -> 166 us (2180 TOP/s;
+// spread over the products, made 4000 x 6288 x 7168 193 -> 165 to 169 us (2130 TOP/s;
 // the library's product alone, without scales, 178 us); a third stage at T0 = 3
 // made 800 x 6288 x 7168 65 -> 51 us.
 // s_waitcnt for at most `vm` vector memory and `lgkm` LDS operations under way.
