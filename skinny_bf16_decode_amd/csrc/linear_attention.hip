@@ -15,7 +15,7 @@
 //
 // which are four matrix products a chunk.  A workgroup of four or eight waves
 // walks the chunks of one (sequence part, head, 64 or 128 value columns); each
-// wave keeps the state of its own 16 columns in registers, in the result layout
+// wave keeps the state of its own 16 or 32 columns in registers, in the result layout
 // of the 16x16x32 MFMA, from one chunk to the next.
 #include <hip/hip_runtime.h>
 
@@ -613,6 +613,11 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
 }
 
 // One part of a sequence for one head and 16 WAVES NV value columns, 16 NV a wave.
+// Bound by the waits of a chunk's four products, one after the other with three
+// barriers between: 5 us a chunk alone on a CU at dk = dv = 128, the matrix
+// units busy for 30 % of it and the vector units for a third (32768 tokens of
+// 12 heads: 67 us for the parts' own states, 124 us for the outputs, against
+// 85 us for the bytes; 16 sequences of 2048 tokens, whole: 143 us).
 // OUT: outputs, and the sequence's new state after its last part.  Otherwise:
 // what the part alone adds to the state, for the parts after it.
 template <bool H, int DK, int WAVES, int NV, bool OUT>
@@ -1018,7 +1023,8 @@ __global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
 // One new token of each sequence.  A workgroup takes 32 value columns of one
 // (sequence, head): 8 threads of four columns by 32 rows of the state, so that
 // every load of the state is under way at once and a single sequence still
-// gives several workgroups a head.  Bound by the state's bytes, 8 dk dv a head.
+// gives several workgroups a head.  Bound by the state's bytes, 8 dk dv a head.  64
+// sequences of 12 heads of 128: 20.6 us, 4.9 TB/s of a copy's 4.8; one: 4.2 us.
 template <bool H>
 __global__ __launch_bounds__(kThreads, 4) void linear_step(LArgs a)
 {
