@@ -63,6 +63,19 @@ def _ints(name, t, count, index):
     return t.data_ptr()
 
 
+def _workspace(nbytes, device, stream):
+    """Memory for one call on `stream` (an object, a handle or None, the
+    current one).  It comes from that stream's own memory and goes back to it:
+    the allocator orders what is freed and taken again on one stream only, and
+    on another one a block may still be in use, before the call or after it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _call(entry, q, k, v, log_decay, out, sequences, starts, state_in, state_out, slots, scale, workspace, stream):
     dtype, shape = v.dtype, v.shape
     kind = _TYPES.get(dtype)
@@ -133,16 +146,15 @@ def prompt(q, k, v, log_decay, out, starts, state_in=None, state_out=None, slots
     dv]; slots int32 [sequences] names each sequence's state, all different
     (None: 0, 1, ...); a slot outside the pool is no state.  scale: dk ** -0.5
     if None.  workspace: a tensor of at least workspace_bytes(...) bytes, which
-    must not serve two calls at once; None allocates one for the call."""
+    must not serve two calls at once; None allocates one for the call, in the
+    memory of the stream that it runs on."""
     if starts.dim() != 1 or starts.shape[0] < 1:
         raise ValueError("starts must be int32 [sequences + 1]")
     sequences = starts.shape[0] - 1
     if workspace is None and v.dim() == 3 and q.dim() == 3:
         need = workspace_bytes(v.shape[0], sequences, v.shape[1], q.shape[2], v.shape[2])
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
-            if stream is not None and hasattr(stream, "cuda_stream"):
-                workspace.record_stream(stream)
+            workspace = _workspace(need, v.device, stream)
     _call(load_library().skinny_linear_prompt, q, k, v, log_decay, out, sequences, starts, state_in, state_out,
           slots, scale, workspace, stream)
     return out
