@@ -186,7 +186,25 @@ def stream_handle(stream, index):
     if stream is None:
         import torch
         return torch._C._cuda_getCurrentRawStream(index)
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if stream.device_index != index:
+        raise ValueError(f"the tensors are on cuda:{index}, the stream is of cuda:{stream.device_index}")
+    return int(stream.cuda_stream)
+
+
+def call_on(index, stream, entry, *args):
+    """entry(*args, handle of the stream), its error raised, with GPU `index`
+    current: a default stream's handle names the current GPU's, whichever that is."""
+    import torch
+    handle = stream_handle(stream, index)
+    if torch._C._cuda_getDevice() == index:
+        status = entry(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = entry(*args, handle)
+    if status:
+        _raise(status)
 
 
 def probe_read(buf_ptr: int, nbytes: int, sink_ptr: int, stream=None) -> None:

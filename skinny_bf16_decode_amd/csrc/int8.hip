@@ -774,6 +774,7 @@ hipError_t launch_product(PArgs a, hipStream_t stream)
     return hipLaunchKernel(fn, dim3((unsigned)((long long)a.n_tiles * a.m_tiles)), dim3(512), params, 0, stream);
 }
 
+// Dynamic LDS past 64 KiB has to be asked for, on every device that the kernels run on.
 void raise_limits()
 {
     for (int t0 = 1; t0 <= 8; ++t0)
@@ -842,6 +843,7 @@ skinny_status skinny_int8_prepare(const void *Wq, int N, int K, long long ldw, c
         delete p;
         return st;
     }
+    raise_limits();
     hipError_t e = hipMalloc(&p->w, (size_t)count * 16);
     if (e == hipSuccess)
         e = hipMalloc(reinterpret_cast<void **>(&p->w_scale), (size_t)N * sizeof(float));
@@ -904,8 +906,6 @@ skinny_status skinny_int8_run(const skinny_int8_plan *p, const void *xq, long lo
     a.pitch = p->pitch;
     a.type = p->out;
     a.vec = (uintptr_t)out % (4 * eb) == 0 && ldo % 4 == 0 && (uintptr_t)residual % (4 * eb) == 0 && ldr % 4 == 0;
-    static const bool raised = (raise_limits(), true);
-    (void)raised;
     const hipError_t e = launch_product(a, (hipStream_t)stream);
     return e == hipSuccess ? SKINNY_OK : hip_bad(e, "int8 product launch");
 }

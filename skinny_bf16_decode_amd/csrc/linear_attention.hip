@@ -19,6 +19,7 @@
 // of the 16x16x32 MFMA, from one chunk to the next.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -1175,14 +1176,23 @@ hipError_t launch_one(void (*fn)(LArgs), dim3 grid, int threads, size_t lds, con
     return hipLaunchKernel(reinterpret_cast<const void *>(fn), grid, dim3(threads), params, lds, stream);
 }
 
+// Dynamic LDS past 64 KiB has to be asked for, once on every device: `done` has a bit for each.
+void raise_limit(void (*fn)(LArgs), int bytes, std::atomic<unsigned long long> &done)
+{
+    int device = 0;
+    (void)hipGetDevice(&device);
+    const unsigned long long bit = 1ull << (device & 63);
+    if (done.load(std::memory_order_relaxed) & bit)
+        return;
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    done.fetch_or(bit, std::memory_order_relaxed);
+}
+
 template <bool H, int DK, int WAVES, int NV>
 hipError_t launch_prompt(const LArgs &a, hipStream_t stream)
 {
-    // dynamic LDS past 64 KiB has to be asked for, once
-    static const hipError_t raised = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(linear_chunks<H, DK, WAVES, NV, true>), hipFuncAttributeMaxDynamicSharedMemorySize,
-        Layout<DK, WAVES, NV, true>::kBytes);
-    (void)raised;
+    static std::atomic<unsigned long long> raised{0};
+    raise_limit(linear_chunks<H, DK, WAVES, NV, true>, Layout<DK, WAVES, NV, true>::kBytes, raised);
     const dim3 grid((unsigned)(((long long)a.groups + 7) / 8 * 8 * a.share * a.col_tiles));
     hipError_t e = hipSuccess;
     if (a.multi) {

@@ -19,7 +19,7 @@ import ctypes
 
 import torch
 
-from . import _raise, load_library, stream_handle
+from . import _raise, call_on, load_library, stream_handle
 
 TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
@@ -61,10 +61,8 @@ def quantize_rows(x, q, scale, stream=None):
         raise ValueError("x rows must have unit stride")
     ldq = _rows("q", q, torch.int8, m, k, index)
     _scales("scale", scale, m, index)
-    status = load_library().skinny_quantize_rows(x.data_ptr(), kind, m, k, ldx if m > 1 else k, q.data_ptr(), ldq,
-                                                 scale.data_ptr(), stream_handle(stream, index))
-    if status:
-        _raise(status)
+    call_on(index, stream, load_library().skinny_quantize_rows, x.data_ptr(), kind, m, k, ldx if m > 1 else k,
+            q.data_ptr(), ldq, scale.data_ptr())
     return q, scale
 
 
@@ -111,10 +109,8 @@ class PreparedInt8:
         if residual is not None:
             ldr = _rows("residual", residual, self.out_dtype, m, self.n, index)
             res = residual.data_ptr()
-        status = load_library().skinny_int8_run(self._plan, xq.data_ptr(), ldx, x_scale.data_ptr(), res, ldr,
-                                                out.data_ptr(), ldo, m, stream_handle(stream, index))
-        if status:
-            _raise(status)
+        call_on(index, stream, load_library().skinny_int8_run, self._plan, xq.data_ptr(), ldx, x_scale.data_ptr(),
+                res, ldr, out.data_ptr(), ldo, m)
         return out
 
     def close(self):

@@ -17,7 +17,7 @@ import struct
 
 import torch
 
-from . import IN_BF16, IN_F16, _raise, load_library, stream_handle
+from . import IN_BF16, IN_F16, call_on, load_library
 
 _TYPES = {torch.bfloat16: IN_BF16, torch.float16: IN_F16}
 _P, _LL, _I = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int
@@ -125,12 +125,10 @@ def _call(entry, q, k, v, log_decay, out, sequences, starts, state_in, state_out
     if tokens <= 1:                     # the strides of a single token say nothing
         qt = kt = vt = ot = 0
     gt, gh = log_decay.stride()
-    status = entry(_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(), ip, op,
-                              start_ptr, slot_ptr, wp, wb, qt, qh, kt, kh, vt, vh, ot, oh, gt, gh, i_slot, i_head,
-                              o_slot, o_head, kind, tokens, sequences, heads, key_heads, dk, dv, pool, scale),
-                   stream_handle(stream, index))
-    if status:
-        _raise(status)
+    call_on(index, stream, entry,
+            _ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(), ip, op, start_ptr,
+                       slot_ptr, wp, wb, qt, qh, kt, kh, vt, vh, ot, oh, gt, gh, i_slot, i_head, o_slot, o_head, kind,
+                       tokens, sequences, heads, key_heads, dk, dv, pool, scale))
 
 
 def prompt(q, k, v, log_decay, out, starts, state_in=None, state_out=None, slots=None, scale=None, workspace=None,

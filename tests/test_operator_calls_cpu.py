@@ -105,3 +105,52 @@ def attention_args(index=0, tokens=8, step=False):
 def test_workspace_is_of_the_stream_that_the_prompt_runs_on(gpu, stream, handle):
     la.prompt(*attention_args(), stream=stream)
     assert gpu.log == [("alloc", 0, handle), ("skinny_linear_prompt", 0, handle)]
+
+
+def calls(index):
+    """name, call(stream) of every entry, with tensors on GPU `index`."""
+    from skinny_bf16_decode_amd import int8
+    x, q, scale = (OnGpu(t, s, index) for t, s in ((torch.bfloat16, (4, 64)), (torch.int8, (4, 64)),
+                                                   (torch.float32, (4,))))
+    plan = int8.PreparedInt8.__new__(int8.PreparedInt8)
+    plan.n, plan.k, plan.out_dtype, plan._index, plan._plan = 32, 64, torch.bfloat16, index, None
+    out = OnGpu(torch.bfloat16, (4, 32), index)
+
+    def run(stream):
+        plan._plan = 1
+        try:
+            plan.run(q, scale, out, stream=stream)
+        finally:
+            plan._plan = None               # nothing to destroy
+
+    return [("skinny_quantize_rows", lambda stream: int8.quantize_rows(x, q, scale, stream=stream)),
+            ("skinny_int8_run", run),
+            ("skinny_linear_prompt", lambda stream: la.prompt(*attention_args(index), stream=stream)),
+            ("skinny_linear_step", lambda stream: la.step(*attention_args(index, step=True), stream=stream))]
+
+
+@pytest.mark.parametrize("index", [0, 1])
+@pytest.mark.parametrize("which", range(4))
+def test_calls_run_on_their_tensors_gpu(gpu, which, index):
+    """The library launches on the current GPU: it has to be the tensors', whichever is current outside."""
+    gpu.need = 0
+    name, call = calls(index)[which]
+    for stream, handle in ((None, CURRENT), (Stream(0x55, f"cuda:{index}"), 0x55), (0x55, 0x55)):
+        gpu.log.clear()
+        call(stream)
+        assert gpu.log == [(name, index, handle)] and gpu.device == 0
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_a_stream_of_another_gpu_is_refused(gpu, which):
+    gpu.need = 0
+    with pytest.raises(ValueError, match="cuda:1, the stream is of cuda:0"):
+        calls(1)[which][1](Stream(0x55, "cuda:0"))
+    assert gpu.log == []
+
+
+def test_workspace_on_another_gpu(gpu):
+    for stream, handle in ((None, CURRENT), (Stream(0x55, "cuda:1"), 0x55), (0x55, 0x55)):
+        gpu.log.clear()
+        la.prompt(*attention_args(1), stream=stream)
+        assert gpu.log == [("alloc", 1, handle), ("skinny_linear_prompt", 1, handle)]
