@@ -181,32 +181,6 @@ def _stream_handle(stream):
     return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def stream_handle(stream, index):
-    """hipStream_t of the given stream (an object or a handle), or of the current one of GPU `index`."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
-    if not hasattr(stream, "cuda_stream"):
-        return int(stream)
-    if stream.device_index != index:
-        raise ValueError(f"the tensors are on cuda:{index}, the stream is of cuda:{stream.device_index}")
-    return int(stream.cuda_stream)
-
-
-def call_on(index, stream, entry, *args):
-    """entry(*args, handle of the stream), its error raised, with GPU `index`
-    current: a default stream's handle names the current GPU's, whichever that is."""
-    import torch
-    handle = stream_handle(stream, index)
-    if torch._C._cuda_getDevice() == index:
-        status = entry(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            status = entry(*args, handle)
-    if status:
-        _raise(status)
-
-
 def probe_read(buf_ptr: int, nbytes: int, sink_ptr: int, stream=None) -> None:
     """Measurement only: stream nbytes from buf with 16-byte nontemporal loads."""
     _raise(load_library().skinny_probe_read(ctypes.c_void_p(buf_ptr), nbytes,

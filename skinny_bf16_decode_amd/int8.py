@@ -19,7 +19,8 @@ import ctypes
 
 import torch
 
-from . import _raise, call_on, load_library, stream_handle
+from . import _raise, load_library
+from .calls import call_on, stream_handle
 
 TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 

@@ -17,7 +17,8 @@ import struct
 
 import torch
 
-from . import IN_BF16, IN_F16, call_on, load_library
+from . import IN_BF16, IN_F16, load_library
+from .calls import call_on
 
 _TYPES = {torch.bfloat16: IN_BF16, torch.float16: IN_F16}
 _P, _LL, _I = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int
