@@ -24,6 +24,7 @@
 #include <stdio.h>
 
 #include "linear_places.h"
+#include "linear_scales.h"
 #include "skinny_internal.h"
 
 namespace skinny {
@@ -174,18 +175,17 @@ __device__ __forceinline__ float wave_max(float x)
     return dpp_max<0xB1>(x);    // quad_perm [1,0,3,2]
 }
 
-// Power of two that brings values of at most `top` below 2^15, and its inverse:
-// an FP16 split of the scaled values is good to 2^-40 of `top`.
-__device__ __forceinline__ void half_range(float top, float &mul, float &back)
+// See linear_scales.h.  An FP16 split of the scaled values, two terms cut off, is good to 2^-21 of a value, and to
+// 2^-38 of `top` where the value is far smaller (FP16's subnormal step, 2^-24, against 2^14).
+__device__ __forceinline__ void half_range(float top, unsigned least, float &mul, float &back)
 {
-    unsigned e = __float_as_uint(top) >> 23;
-    e = e < 15u ? 15u : (e > 254u ? 254u : e);
-    mul = __uint_as_float((268u - e) << 23);
-    back = __uint_as_float((e - 14u) << 23);
+    unsigned m, b;
+    half_range_bits(__float_as_uint(top), least, m, b);
+    mul = __uint_as_float(m);
+    back = __uint_as_float(b);
 }
 
-// 1 / p of a power of two between 2^-126 and 2^126
-__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float(inverse_power_bits(__float_as_uint(p))); }
 
 // Whether any lane of the wave saw a value that is not finite: acc gathers x * 0.
 __device__ __forceinline__ bool wave_any_nan(float acc) { return __ballot(acc != 0.0f) != 0ull; }
@@ -558,7 +558,7 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
 #pragma unroll
                 for (int p = 0; p < 8; ++p)
                     top = fmaxf(top, fabsf(x[j][p]));
-            half_range(wave_max(top), mul, back[n]);
+            half_range(wave_max(top), kLeastExponent, mul, back[n]);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -785,7 +785,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                     }
                     if constexpr (H) {
                         float mul, back;
-                        half_range(wave_max(top), mul, back);
+                        half_range(wave_max(top), kLeastScoreExponent, mul, back);
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
                             x[r] *= mul;
@@ -816,7 +816,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 top = fmaxf(top, fabsf(S[n][i][r]));
-                    half_range(wave_max(top), s_mul, s_back);
+                    half_range(wave_max(top), kLeastExponent, s_mul, s_back);
                 }
 #pragma unroll
                 for (int j = 0; j < DK / 32; ++j) {
@@ -849,7 +849,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                                 acc[i][n] = mma16<H>(f[n][m], qf[i], acc[i][n]);
                 }
                 __syncthreads();
-                // + scores V; FP16 scores carry powers of two (all steps below are exact in them)
+                // + scores V; FP16 scores carry powers of two, into which the sum is brought: exact, and finite for
+                // states below 2^58 (see linear_scales.h)
                 float back[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
