@@ -156,27 +156,25 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[TERMS])
     }
 }
 
-template <int CTRL>
-__device__ __forceinline__ float dpp_max(float x)
-{
-    return fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true)));
-}
-
-// Largest value over the wave, in every lane (values >= 0; NaN is passed over).
-__device__ __forceinline__ float wave_max(float x)
+// Largest value over the four lanes of one column, l % 16 (values >= 0; NaN is passed over).
+__device__ __forceinline__ float column_max(float x)
 {
     auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
     r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-    x = dpp_max<0x140>(x);      // row_mirror
-    x = dpp_max<0x141>(x);      // row_half_mirror
-    x = dpp_max<0x4E>(x);       // quad_perm [2,3,0,1]
-    return dpp_max<0xB1>(x);    // quad_perm [1,0,3,2]
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Value of the column that lane group g's result row r belongs to, lane 4 g + r of 16.
+__device__ __forceinline__ float of_row(float x, int r)
+{
+    return __uint_as_float(__builtin_amdgcn_ds_bpermute(4 * (4 * ((threadIdx.x & 63) >> 4) + r), __float_as_uint(x)));
 }
 
 // See linear_scales.h.  An FP16 split of the scaled values, two terms cut off, is good to 2^-21 of a value, and to
-// 2^-38 of `top` where the value is far smaller (FP16's subnormal step, 2^-24, against 2^14).
+// 2^-38 of `top` where the value is far smaller (FP16's subnormal step, 2^-24, against 2^14).  So the power is one for
+// each sum that the values enter -- a value column, a token's scores of one tile -- and not one for several, of which
+// the smaller would lose its bits to the larger.
 __device__ __forceinline__ void half_range(float top, unsigned least, float &mul, float &back)
 {
     unsigned m, b;
@@ -558,7 +556,7 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
 #pragma unroll
                 for (int p = 0; p < 8; ++p)
                     top = fmaxf(top, fabsf(x[j][p]));
-            half_range(wave_max(top), kLeastExponent, mul, back[n]);
+            half_range(column_max(top), kLeastExponent, mul, back[n]);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -628,7 +626,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
     constexpr int kGateWave = WAVES == 8 ? 7 : 2;   // it has the least of the scores to do
     extern __shared__ __align__(16) unsigned short lds[];
     __shared__ Decays decays[2];
-    __shared__ float score_back[4][2];
+    __shared__ float score_back[4][2][16];
     const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4;
     unsigned short *qs = lds + L::kQ / 2, *ks = lds + L::kK / 2, *vs = lds + L::kV / 2;
     u32x4 *scores = reinterpret_cast<u32x4 *>(lds + L::kScores / 2);
@@ -785,12 +783,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                     }
                     if constexpr (H) {
                         float mul, back;
-                        half_range(wave_max(top), kLeastScoreExponent, mul, back);
+                        half_range(column_max(top), kLeastScoreExponent, mul, back);
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
                             x[r] *= mul;
-                        if (lane == 0)
-                            score_back[tt][j] = back;
+                        if (g == 0)
+                            score_back[tt][j][lane] = back;
                     }
                     u32x4 f[2];
                     split8<H, 2>(x, f);
@@ -806,17 +804,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
 #pragma unroll
                     for (int n = 0; n < NV; ++n)
                         acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                float s_mul = 1.0f, s_back = 1.0f;
+                float s_mul[NV], s_back[NV];
                 if constexpr (H) {
-                    float top = 0.0f;
 #pragma unroll
-                    for (int n = 0; n < NV; ++n)
+                    for (int n = 0; n < NV; ++n) {
+                        float top = 0.0f;
 #pragma unroll
                         for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 top = fmaxf(top, fabsf(S[n][i][r]));
-                    half_range(wave_max(top), kLeastExponent, s_mul, s_back);
+                        half_range(column_max(top), kLeastExponent, s_mul[n], s_back[n]);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < DK / 32; ++j) {
@@ -836,7 +835,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                         if constexpr (H) {
 #pragma unroll
                             for (int r = 0; r < 8; ++r)
-                                x[r] *= s_mul;
+                                x[r] *= s_mul[n];
                         }
                         split8<H, 2>(x, f[n]);
                     }
@@ -848,17 +847,28 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                             for (int n = 0; n < NV; ++n)
                                 acc[i][n] = mma16<H>(f[n][m], qf[i], acc[i][n]);
                 }
+                if constexpr (H) {
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float b = of_row(s_back[n], r);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                acc[i][n][r] *= b;
+                        }
+                }
                 __syncthreads();
-                // + scores V; FP16 scores carry powers of two, into which the sum is brought: exact, and finite for
-                // states below 2^58 (see linear_scales.h)
+                // + scores V; a token's FP16 scores carry a power of two, into which its sum is brought: exact, and
+                // finite for states below 2^58 (see linear_scales.h)
                 float back[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     back[i] = 1.0f;
                     float f = d.grown[16 * i + (lane & 15)] * a.scale;
                     if constexpr (H) {
-                        back[i] = score_back[i][0];
-                        f *= s_back * inverse_power(back[i]);
+                        back[i] = score_back[i][0][lane & 15];
+                        f *= inverse_power(back[i]);
                     }
 #pragma unroll
                     for (int n = 0; n < NV; ++n)
@@ -876,13 +886,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                     for (int i = 2 * j; i < 4; ++i) {
                         if constexpr (H) {
                             if (j) {
-                                const float f = back[i] * inverse_power(score_back[i][1]);
+                                const float next = score_back[i][1][lane & 15], f = back[i] * inverse_power(next);
 #pragma unroll
                                 for (int n = 0; n < NV; ++n)
 #pragma unroll
                                     for (int r = 0; r < 4; ++r)
                                         acc[i][n][r] *= f;
-                                back[i] = score_back[i][1];
+                                back[i] = next;
                             }
                         }
 #pragma unroll
