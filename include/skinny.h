@@ -457,8 +457,11 @@ void skinny_int8_destroy(skinny_int8_plan *plan);
  * log decays g [tokens][heads] and states S [pool][heads][dk][dv] in fp32;
  * value head h reads key head h / (heads / key_heads).  g is a log of a decay:
  * at most 0, -inf for a state that is forgotten (larger values are taken as
- * they are, as far as fp32 goes).  All arithmetic on states, decays and sums
- * is fp32 or wider.  A value that is not finite reaches the outputs and states
+ * they are, as far as fp32 goes).  States and sums are fp32, sums of decays
+ * wider.  A prompt's matrix products take their fp32 operands (the state and
+ * the scores for the outputs, the decayed v for the state) with all 24 bits for
+ * BF16 inputs, and with 22 for FP16 ones, in a range for each column of v and
+ * each token; a step multiplies in fp32.  A value that is not finite reaches the outputs and states
  * that depend on it by the formulas above and no others.
  */
 typedef struct {

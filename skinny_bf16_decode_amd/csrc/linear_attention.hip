@@ -113,19 +113,28 @@ __device__ __forceinline__ void unpack2(unsigned int w, float &lo, float &hi)
     hi = to_float<H>((unsigned short)(w >> 16));
 }
 
-// Two fp32 values as the sum of TERMS pairs of 16-bit values, each term the
-// rounded rest, which is exact.  BF16 (8 bits and a sign a term): 17 bits for
-// two terms, all 24 for three.  FP16 (the caller scales into its range; terms
-// cut off, the form that takes two values at once): 22 bits.
-template <bool H, int TERMS>
-__device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[TERMS])
+// 16-bit terms of an fp32 operand of a matrix product.  Three BF16 terms (8 bits
+// and a sign each) hold all 24 bits.  With two, 17 bits, what cancellation left
+// of a sum over the state was off by 2.5e-6 of the terms' size, 35 times as far
+// as in a step, which multiplies in fp32 (prompts 5 to 11 % longer with three:
+// 16 of 2048 tokens 152 -> 167 us).  Two FP16 terms hold 22 bits, and that sum is
+// off by 1.1e-7, against a step's 0.7e-7; a third made FP16 prompts 9 to 14 %
+// longer for little more, and is not taken.
+template <bool H>
+constexpr int kTerms = H ? 2 : 3;
+
+// Two fp32 values as the sum of kTerms pairs of 16-bit values, each term the
+// rounded rest, which is exact.  FP16 terms (the caller scales into their range,
+// see half_range) are cut off, the form that takes two values at once.
+template <bool H>
+__device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[kTerms<H>])
 {
 #pragma unroll
-    for (int i = 0; i < TERMS; ++i) {
+    for (int i = 0; i < kTerms<H>; ++i) {
         if constexpr (H) {
             const auto p = __builtin_amdgcn_cvt_pkrtz(a, b);
             w[i] = __builtin_bit_cast(unsigned int, p);
-            if (i + 1 < TERMS) {
+            if (i + 1 < kTerms<H>) {
                 a -= (float)p[0];
                 b -= (float)p[1];
             }
@@ -133,7 +142,7 @@ __device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[TERMS
             typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
             const bf16x2 p = {(__bf16)a, (__bf16)b};
             w[i] = __builtin_bit_cast(unsigned int, p);
-            if (i + 1 < TERMS) {
+            if (i + 1 < kTerms<H>) {
                 asm("" : "+v"(w[i]));       // else the low half is rounded a second time, alone
                 a -= __uint_as_float(w[i] << 16);
                 b -= __uint_as_float(w[i] & 0xFFFF0000u);
@@ -142,16 +151,16 @@ __device__ __forceinline__ void split2(float a, float b, unsigned int (&w)[TERMS
     }
 }
 
-// Eight fp32 values into TERMS MFMA operands.
-template <bool H, int TERMS>
-__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[TERMS])
+// Eight fp32 values into kTerms MFMA operands.
+template <bool H>
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[kTerms<H>])
 {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        unsigned int w[TERMS];
-        split2<H, TERMS>(x[2 * p], x[2 * p + 1], w);
+        unsigned int w[kTerms<H>];
+        split2<H>(x[2 * p], x[2 * p + 1], w);
 #pragma unroll
-        for (int i = 0; i < TERMS; ++i)
+        for (int i = 0; i < kTerms<H>; ++i)
             f[i][p] = w[i];
     }
 }
@@ -168,7 +177,9 @@ __device__ __forceinline__ float column_max(float x)
 // Value of the column that lane group g's result row r belongs to, lane 4 g + r of 16.
 __device__ __forceinline__ float of_row(float x, int r)
 {
-    return __uint_as_float(__builtin_amdgcn_ds_bpermute(4 * (4 * ((threadIdx.x & 63) >> 4) + r), __float_as_uint(x)));
+    int first = 4 * (4 * ((threadIdx.x & 63) >> 4));
+    asm volatile("" : "+v"(first));             // one address kept over the chunks, not one for every r
+    return __uint_as_float(__builtin_amdgcn_ds_bpermute(first + 4 * r, __float_as_uint(x)));
 }
 
 // See linear_scales.h.  An FP16 split of the scaled values, two terms cut off, is good to 2^-21 of a value, and to
@@ -426,7 +437,7 @@ struct Layout {
     static constexpr int kK = kQ + (OUT ? kChunk * kQPitch * 2 : 0);
     static constexpr int kV = kK + kChunk * kKPitch * 2;
     static constexpr int kScores = kV + kChunk * kVPitch * 2;
-    static constexpr int kBytes = kScores + (OUT ? kScoreSlots * 2 * 64 * 16 : 0);
+    static constexpr int kBytes = kScores + (OUT ? kScoreSlots * 3 * 64 * 16 : 0);
 };
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -531,17 +542,14 @@ __device__ __forceinline__ void decayed_values(u32x4 v, const Decays &d, int j, 
 }
 
 // S = exp(G_63) S + sum_s k_s (exp(G_63 - G_s) v_s)^T over the chunk in LDS.
-// k is exact in 16 bits; the decayed v is fp32 and goes in as three BF16 terms
-// (24 bits), or two FP16 terms after a power of two (22 bits), so the state
-// keeps fp32's accuracy on the matrix units.
+// k is exact in 16 bits; the decayed v is fp32 and goes in as kTerms.
 template <bool H, int DK, int WAVES, int NV, bool OUT>
 __device__ __forceinline__ void update_state(const unsigned short *lds, const Decays &d, f32x4 (&S)[NV][DK / 16])
 {
     using L = Layout<DK, WAVES, NV, OUT>;
-    constexpr int kTerms = H ? 2 : 3;
     const unsigned short *ks = lds + L::kK / 2, *vs = lds + L::kV / 2 + 16 * NV * wave_id();
     const float total = d.total;
-    u32x4 f[NV][2][kTerms];
+    u32x4 f[NV][2][kTerms<H>];
     float back[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
@@ -565,7 +573,7 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            split8<H, kTerms>(x[j], f[n][j]);
+            split8<H>(x[j], f[n][j]);
     }
     u32x4 k[2][2];                              // of this row tile and the next
 #pragma unroll
@@ -593,7 +601,7 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int m = 0; m < kTerms; ++m)
+            for (int m = 0; m < kTerms<H>; ++m)
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     if constexpr (H)
@@ -619,8 +627,10 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
 // 85 us for the bytes; 16 sequences of 2048 tokens, whole: 143 us).
 // OUT: outputs, and the sequence's new state after its last part.  Otherwise:
 // what the part alone adds to the state, for the parts after it.
+// Registers for two waves a SIMD; for one where LDS holds one workgroup a CU and
+// that has four waves (dk = 256: with two it spilled 5 registers).
 template <bool H, int DK, int WAVES, int NV, bool OUT>
-__global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
+__global__ __launch_bounds__(64 * WAVES, DK == 256 && WAVES == 4 && OUT ? 1 : 2) void linear_chunks(LArgs a)
 {
     using L = Layout<DK, WAVES, NV, OUT>;
     constexpr int kGateWave = WAVES == 8 ? 7 : 2;   // it has the least of the scores to do
@@ -790,14 +800,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                         if (g == 0)
                             score_back[tt][j][lane] = back;
                     }
-                    u32x4 f[2];
-                    split8<H, 2>(x, f);
-                    scores[(job * 2 + 0) * 64 + lane] = f[0];
-                    scores[(job * 2 + 1) * 64 + lane] = f[1];
+                    u32x4 f[kTerms<H>];
+                    split8<H>(x, f);
+#pragma unroll
+                    for (int m = 0; m < kTerms<H>; ++m)
+                        scores[(job * kTerms<H> + m) * 64 + lane] = f[m];
                 }
                 if (more)
                     tq.load(qp + at * a.q_token, left);
-                // S^T q of all 64 tokens, the state in two terms
+                // S^T q of all 64 tokens
                 f32x4 acc[4][NV];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -819,7 +830,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                 }
 #pragma unroll
                 for (int j = 0; j < DK / 32; ++j) {
-                    u32x4 qf[4], f[NV][2];
+                    u32x4 qf[4], f[NV][kTerms<H>];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         qf[i] = query_operand(qs, L::kQPitch, 16 * i, j);
@@ -837,10 +848,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                             for (int r = 0; r < 8; ++r)
                                 x[r] *= s_mul[n];
                         }
-                        split8<H, 2>(x, f[n]);
+                        split8<H>(x, f[n]);
                     }
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < kTerms<H>; ++m)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -896,8 +907,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                             }
                         }
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const u32x4 pf = scores[(score_slot(i, j) * 2 + m) * 64 + lane];
+                        for (int m = 0; m < kTerms<H>; ++m) {
+                            const u32x4 pf = scores[(score_slot(i, j) * kTerms<H> + m) * 64 + lane];
 #pragma unroll
                             for (int n = 0; n < NV; ++n)
                                 acc[i][n] = mma16<H>(vf[n], pf, acc[i][n]);
@@ -926,6 +937,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                     recur<H, DK, WAVES, NV, OUT>(a, lds, d, rows, T, o, col0);
                 } else {
                     const __amdgpu_buffer_rsrc_t dst = make_rsrc(o);
+                    unsigned first = out_off;
+                    asm volatile("" : "+v"(first));     // kept over the chunks alone, not with every row's
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         unsigned int w[2 * NV];
@@ -937,7 +950,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_chunks(LArgs a)
                         // the whole offset per lane, none in a scalar register: the compiler may write the data
                         // registers of a store with a scalar offset in the very next instruction, and this chip was
                         // seen to store what that one wrote (16-byte stores; see the test of the built code)
-                        const unsigned to = 16 * i + (lane & 15) < rows ? out_off + 16 * i * out_step : kSkip;
+                        const unsigned to = (lane & 15) < rows - 16 * i ? first + 16 * i * out_step : kSkip;
                         if constexpr (NV == 2)
                             __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, dst, to, 0, 0);
                         else

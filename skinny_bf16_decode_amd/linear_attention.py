@@ -7,8 +7,9 @@ matrix units, long sequences split over the chip) or for one new token of each
 sequence (``step``).  The states stay in a pool of fp32 [dk, dv] matrices, one
 [heads, dk, dv] slot a sequence.  q, k, v and out are views with a contiguous
 last dimension, so the column ranges of a packed projection's output can be
-passed in place.  Argument marshalling only: the kernels are in
-csrc/linear_attention.hip.
+passed in place.  States and sums are fp32; a prompt's matrix products take
+fp32 operands with all 24 bits for BF16 inputs and with 22 for FP16 ones.
+Argument marshalling only: the kernels are in csrc/linear_attention.hip.
 """
 from __future__ import annotations
 
