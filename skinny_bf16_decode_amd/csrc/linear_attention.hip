@@ -25,6 +25,7 @@
 
 #include "linear_places.h"
 #include "linear_scales.h"
+#include "linear_shape.h"
 #include "skinny_internal.h"
 
 namespace skinny {
@@ -37,7 +38,6 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
-constexpr int kChunk = 64;
 constexpr int kThreads = 256;
 
 // Kernel arguments.  Strides are in elements.
@@ -49,9 +49,11 @@ struct LArgs {
     float *state_out;
     const int *starts;          // prompt: [sequences + 1]
     const int *slots;           // [sequences], or NULL: sequence i holds slot i
-    float *ws_state;            // prompt in parts: [place][head][dk][dv]
-    double *ws_decay;           // [place][head], sums of log2 decays
-    int *ws_serial;             // [sequence][head], the part from which on the sequence is taken in one go
+    // prompt in parts, see the states of linear_places.h
+    float *ws_part;             // [later part][head][dk][dv]
+    float *ws_start;            // [start][head][dk][dv]
+    double *ws_decay;           // [later part][head], sums of log2 decays of the part before
+    int *ws_serial;             // [start][head], the part from which on the sequence is taken in one go
     long long q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head, g_token, g_head;
     long long in_slot, in_head, so_slot, so_head;
     int tokens, sequences, heads, share, dk, dv, pool;
@@ -200,7 +202,7 @@ __device__ __forceinline__ float inverse_power(float p) { return __uint_as_float
 __device__ __forceinline__ bool wave_any_nan(float acc) { return __ballot(acc != 0.0f) != 0ull; }
 
 // The place of a workgroup, see linear_places.h; false if it is empty.
-__device__ __forceinline__ bool locate(const LArgs &a, int block, int &place, Place &p)
+__device__ __forceinline__ bool locate(const LArgs &a, int block, Place &p)
 {
     int seq = block;
     if (block >= a.sequences) {
@@ -217,7 +219,7 @@ __device__ __forceinline__ bool locate(const LArgs &a, int block, int &place, Pl
             return false;
         seq = __builtin_amdgcn_readfirstlane(count - 1);
     }
-    place = block_place(a.starts[seq], a.tokens, a.part, a.sequences, block, seq);
+    const int place = block_place(a.starts[seq], a.tokens, a.part, a.sequences, block, seq);
     return place_of(a.starts[seq], a.starts[seq + 1], a.tokens, a.part, place, seq, p);
 }
 
@@ -655,8 +657,7 @@ __global__ __launch_bounds__(64 * WAVES, DK == 256 && WAVES == 4 && OUT ? 1 : 2)
     const int head = (int)(hp % (unsigned)a.heads), block = (int)(hp / (unsigned)a.heads);
 
     Place p;
-    int place;
-    if (!locate(a, block, place, p))
+    if (!locate(a, block, p))
         return;
     const int parts = parts_of(p.len, a.part);
     if (!OUT && p.part == parts - 1)
@@ -664,9 +665,12 @@ __global__ __launch_bounds__(64 * WAVES, DK == 256 && WAVES == 4 && OUT ? 1 : 2)
     const int t0 = p.part * a.part;
     int n_tok = min(p.len - t0, a.part);
     bool last = p.part == parts - 1;
+    // of the sequence's start, and of the part after this one; used where there are several parts
+    const long long start_at = (long long)start_state(p.first, a.tokens, a.part, a.sequences, p.seq) * a.heads + head;
+    const long long next_at = (long long)part_state(p.first, a.tokens, a.part, p.part + 1) * a.heads + head;
     if (OUT && a.multi && parts > 1) {
         // a join that is no sum (see linear_join): the part before it goes on to the end
-        const int serial = a.ws_serial[(long long)p.seq * a.heads + head];
+        const int serial = a.ws_serial[start_at];
         if (serial < p.part)
             return;
         if (serial == p.part) {
@@ -689,7 +693,6 @@ __global__ __launch_bounds__(64 * WAVES, DK == 256 && WAVES == 4 && OUT ? 1 : 2)
     const int wave_col = col0 + 16 * NV * wave;
     const int out_col = wave_col + 4 * NV * g;  // dv is a multiple of 8: 4 NV columns are all in or all out
     const unsigned out_off = out_col < a.dv ? (lane & 15) * out_step + 2 * out_col : kSkip;
-    const long long ws_off = ((long long)place * a.heads + head) * a.dk * a.dv;
 
     f32x4 S[NV][DK / 16];
     f32x4 memory[NV * (DK / 16)], *T = memory;         // the state of a wave that goes token by token
@@ -698,7 +701,7 @@ __global__ __launch_bounds__(64 * WAVES, DK == 256 && WAVES == 4 && OUT ? 1 : 2)
     if constexpr (OUT) {
         const float *from = nullptr;
         if (a.multi && parts > 1)
-            from = a.ws_state + ws_off;
+            from = p.part == 0 ? a.ws_start + start_at * a.dk * a.dv : a.ws_part + (next_at - a.heads) * a.dk * a.dv;
         else if (a.state_in && slot >= 0)
             from = a.state_in + slot * a.in_slot + head * a.in_head;
 #pragma unroll
@@ -976,14 +979,14 @@ __global__ __launch_bounds__(64 * WAVES, DK == 256 && WAVES == 4 && OUT ? 1 : 2)
                 odd += S[i / (DK / 16)][i % (DK / 16)][r] * 0.0f;
         slow = attempt == 1;
         if (wave == kGateWave && lane == 0 && tile == 0) {
-            a.ws_decay[(long long)place * a.heads + head] = sum;
+            a.ws_decay[next_at] = sum;
             if (p.part == 0)
-                a.ws_serial[(long long)p.seq * a.heads + head] = 0x7FFFFFFF;
+                a.ws_serial[start_at] = 0x7FFFFFFF;
         }
         if (slow || !__syncthreads_or(odd != 0.0f))
             break;
     }
-    float *to = a.ws_state + ws_off;
+    float *to = a.ws_part + next_at * a.dk * a.dv;
     if constexpr (OUT) {
         if (!last || !a.state_out || slot < 0)
             return;
@@ -1008,8 +1011,7 @@ __global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
 {
     const int head = blockIdx.y, seq = blockIdx.z;
     Place p;
-    const int place0 = first_place(a.starts[seq], a.tokens, a.part, seq);
-    place_of(a.starts[seq], a.starts[seq + 1], a.tokens, a.part, place0, seq, p);
+    place_of(a.starts[seq], a.starts[seq + 1], a.tokens, a.part, first_place(a.starts[seq], a.tokens, a.part, seq), seq, p);
     const int parts = parts_of(p.len, a.part);
     const int at = (blockIdx.x * kThreads + threadIdx.x) * 4, size = a.dk * a.dv;
     if (parts < 2 || at >= size)
@@ -1018,30 +1020,32 @@ __global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
     f32x4 S = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (a.state_in && slot >= 0)
         S = *reinterpret_cast<const f32x4 *>(a.state_in + slot * a.in_slot + head * a.in_head + at);
-    float *w = a.ws_state + ((long long)place0 * a.heads + head) * size + at;
-    const double *decay = a.ws_decay + (long long)place0 * a.heads + head;
+    const long long start_at = (long long)start_state(p.first, a.tokens, a.part, a.sequences, seq) * a.heads + head;
+    const long long part_at = (long long)part_state(p.first, a.tokens, a.part, 1) * a.heads + head;
+    *reinterpret_cast<f32x4 *>(a.ws_start + start_at * size + at) = S;
+    float *w = a.ws_part + part_at * size + at;
+    const double *decay = a.ws_decay + part_at;
     const long long step = (long long)a.heads * size;
     constexpr int kAhead = 8;                   // parts whose loads are under way at once
-    for (int j0 = 0; j0 < parts; j0 += kAhead) {
+    for (int j0 = 0; j0 + 1 < parts; j0 += kAhead) {
         f32x4 add[kAhead];
         double log2[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int j = min(j0 + u, parts - 1);   // the last part's place is there, and not used
+            const int j = min(j0 + u, parts - 2);
             add[u] = *reinterpret_cast<const f32x4 *>(w + j * step);
             log2[u] = decay[(long long)j * a.heads];
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int j = j0 + u;
-            if (j < parts)
-                *reinterpret_cast<f32x4 *>(w + j * step) = S;
             if (j + 1 < parts) {
                 const float f = __builtin_amdgcn_exp2f((float)log2[u]);
                 const float odd = ((S[0] + S[1]) + (S[2] + S[3])) * 0.0f;
                 if (!(f < INFINITY) || (f == 0.0f && odd != 0.0f))
-                    atomicMin(&a.ws_serial[(long long)seq * a.heads + head], j);
+                    atomicMin(&a.ws_serial[start_at], j);
                 S = S * f + add[u];
+                *reinterpret_cast<f32x4 *>(w + j * step) = S;
             }
         }
     }
@@ -1126,73 +1130,21 @@ __global__ __launch_bounds__(kThreads, 4) void linear_step(LArgs a)
 // Host side
 // ---------------------------------------------------------------------------
 
-// Launch shape of a prompt, from its sizes alone.
-struct Shape {
-    int cols, col_tiles, part, places, multi;
-    int eight;                  // eight waves of 16 columns, one workgroup a CU, in place of four of 32
+// The workspace: states of parts and of starts, decays, the parts that go on.
+struct Workspace {
+    size_t parts, starts;       // states
+    size_t state;               // bytes of one
+
+    size_t bytes(int heads) const
+    {
+        return (parts + starts) * state + parts * heads * sizeof(double) + starts * heads * sizeof(int);
+    }
 };
 
-constexpr int kSlots = 512;     // workgroups the chip runs at once: two on each of 256 CUs
-constexpr int kOnePass = 384;   // tokens up to which nothing is done in parts
-
-// Tokens of a part, for workgroups of `cols` columns.  The average is all that
-// the host knows of the lengths.
-int part_of(int tokens, int sequences, int heads, int dv, int cols)
+Workspace workspace_of(int tokens, int sequences, int heads, int dk, int dv)
 {
-    const long long columns = (long long)heads * ((dv + cols - 1) / cols), count = sequences > 0 ? sequences : 1;
-    const long long average = ((long long)tokens + count - 1) / count;
-    // as many parts as run at once, the same number for every sequence of the average length
-    const long long units = columns * count, per_sequence = units < kSlots ? kSlots / units : 1;
-    const long long even = ((average + per_sequence - 1) / per_sequence + kChunk - 1) / kChunk * kChunk;
-    // none shorter than 192 tokens: parts are done twice.  While there are CUs left, of 64 tokens, since a lone
-    // workgroup waits most of a chunk's 5 us (27 sequences, 5022 tokens, one head: parts of 64, 128, 256 30, 36,
-    // 52 us).  Where sequences are short, only the far longer ones are cut
-    const auto fits = [&](int part, int most) { return columns * (tokens / part + count) <= most; };
-    const int least = average < 80 ? kOnePass : fits(64, 160) ? 64 : fits(192, kSlots) ? 192 : 256;
-    return (int)(even > least ? even : least);
-}
-
-Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
-{
-    Shape s;
-    // 128 columns a workgroup, or 64: where there are no more, or a last tile would be half empty; where the
-    // wide ones leave many CUs with one workgroup or none; and where that makes enough workgroups of whole
-    // sequences, of which no part is done twice (24 sequences of 12001 tokens, 12 heads, dk 64: 88 against 96 us)
-    const int part = part_of(tokens, sequences, heads, dv, 128);
-    const long long wide = (dv + 127) / 128, narrow = (dv + 63) / 64, parts = tokens / part;
-    const bool few = heads * wide * (parts > sequences ? parts : sequences) <= 300;
-    const bool whole = heads * wide * sequences <= 300 && heads * narrow * sequences >= 3 * kSlots / 4 &&
-                       (long long)tokens <= 4096LL * sequences;
-    // 64 < dk <= 128: one workgroup of eight waves a CU, sequences uncut, where there are that many and few more
-    // (16 prompts of 2048 tokens, 12 heads of 128: 149 us); two of four waves a CU past that, which wait less in
-    // all (24 prompts: 254 against 282 us)
-    const long long units = heads * wide * sequences, average = sequences > 0 ? tokens / sequences : 0;
-    const bool middle = dk > 64 && dk <= 128 && dv > 64 && (dv <= 128 || dv > 192);
-    s.eight = middle && units <= kSlots / 2 && average <= 4096 && (units >= 128 || (units >= 96 && average <= 384));
-    const bool many = middle && units > kSlots / 2;
-    s.cols = dv <= 64 || (dv > 128 && dv <= 192) || ((few || whole) && !s.eight && !many) ? 64 : 128;
-    s.col_tiles = (dv + s.cols - 1) / s.cols;
-    s.part = s.cols == 128 ? part : part_of(tokens, sequences, heads, dv, 64);
-    if (s.eight)                                // room for lengths about the average
-        s.part = (int)((average + average / 8) / kChunk + 1) * kChunk;
-    s.multi = tokens > kOnePass && s.part < tokens;
-    if (!s.multi)                               // past every start: sequence i is place i
-        s.part = (tokens / kChunk + 1) * kChunk;
-    s.places = tokens / s.part + sequences;
-    return s;
-}
-
-size_t state_bytes(const Shape &s, int heads, int dk, int dv)
-{
-    return s.multi ? (size_t)s.places * heads * dk * dv * sizeof(float) : 0;
-}
-
-size_t decay_bytes(const Shape &s, int heads) { return (size_t)s.places * heads * sizeof(double); }
-
-size_t workspace_of(const Shape &s, int sequences, int heads, int dk, int dv)
-{
-    return s.multi ? state_bytes(s, heads, dk, dv) + decay_bytes(s, heads) + (size_t)sequences * heads * sizeof(int)
-                   : 0;
+    const size_t parts = tokens > kOnePass ? (size_t)most_extra_parts(tokens, sequences, heads, dv) : 0;
+    return Workspace{parts, parts < (size_t)sequences ? parts : (size_t)sequences, (size_t)heads * dk * dv * sizeof(float)};
 }
 
 hipError_t launch_one(void (*fn)(LArgs), dim3 grid, int threads, size_t lds, const LArgs &a, hipStream_t stream)
@@ -1367,7 +1319,7 @@ size_t skinny_linear_workspace(int tokens, int sequences, int heads, int dk, int
 {
     if (tokens < 0 || tokens > 0x7FFFF000 || sequences < 0 || heads < 1 || dk < 8 || dk > 256 || dv < 8 || dv > 1024)
         return 0;
-    return workspace_of(shape_of(tokens, sequences, heads, dk, dv), sequences, heads, dk, dv);
+    return workspace_of(tokens, sequences, heads, dk, dv).bytes(heads);
 }
 
 skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
@@ -1381,7 +1333,8 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
     if ((long long)s.places * p->heads * s.col_tiles > 0x7F000000LL)
         return bad(SKINNY_ERR_SHAPE, "tokens=%d, sequences=%d and heads=%d are too many for one call", p->tokens,
                    p->sequences, p->heads);
-    const size_t need = workspace_of(s, p->sequences, p->heads, p->dk, p->dv);
+    const Workspace w = workspace_of(p->tokens, p->sequences, p->heads, p->dk, p->dv);
+    const size_t need = s.multi ? w.bytes(p->heads) : 0;
     if (need && (!p->workspace || p->workspace_bytes < need))
         return bad(SKINNY_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu are needed",
                    p->workspace ? p->workspace_bytes : (size_t)0, need);
@@ -1399,9 +1352,10 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
     a.multi = s.multi;
     if (s.multi) {
         char *ws = static_cast<char *>(p->workspace);
-        a.ws_state = reinterpret_cast<float *>(ws);
-        a.ws_decay = reinterpret_cast<double *>(ws += state_bytes(s, p->heads, p->dk, p->dv));
-        a.ws_serial = reinterpret_cast<int *>(ws + decay_bytes(s, p->heads));
+        a.ws_part = reinterpret_cast<float *>(ws);
+        a.ws_start = reinterpret_cast<float *>(ws += w.parts * w.state);
+        a.ws_decay = reinterpret_cast<double *>(ws += w.starts * w.state);
+        a.ws_serial = reinterpret_cast<int *>(ws + w.parts * p->heads * sizeof(double));
     }
     return launched(p->type == SKINNY_IN_F16 ? launch_prompt_type<true>(a, s, (hipStream_t)stream)
                                              : launch_prompt_type<false>(a, s, (hipStream_t)stream));

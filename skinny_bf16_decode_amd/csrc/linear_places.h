@@ -61,4 +61,26 @@ SKINNY_HD int block_place(int start, int tokens, int size, int sequences, int bl
     return block < sequences ? first_place(start, tokens, size, block) : block - sequences + 1 + seq;
 }
 
+// States in the workspace.  A sequence in several parts has one for its start
+// and one for every later part: what the part before it adds, then the state it
+// starts from.  The later parts' lie in the order of the extra parts, tokens /
+// size of them whatever the sequences; the starts', behind them, by sequence, or
+// by their sequence's first extra part, whichever are fewer.  No other sequence
+// has a state here.
+SKINNY_HD int extra_states(int tokens, int size) { return tokens / size; }
+
+SKINNY_HD int start_states(int tokens, int size, int sequences)
+{
+    return sequences < extra_states(tokens, size) ? sequences : extra_states(tokens, size);
+}
+
+// Of part `part` >= 1 of a sequence in several.
+SKINNY_HD int part_state(int start, int tokens, int size, int part) { return cut_to(start, 0, tokens) / size + part - 1; }
+
+// Of the start of sequence `seq`, among the starts'.
+SKINNY_HD int start_state(int start, int tokens, int size, int sequences, int seq)
+{
+    return sequences < extra_states(tokens, size) ? seq : cut_to(start, 0, tokens) / size;
+}
+
 }  // namespace skinny

@@ -41,7 +41,7 @@ assert _ARGS.size == ctypes.sizeof(_Args)
 
 
 def workspace_bytes(tokens: int, sequences: int, heads: int, dk: int, dv: int) -> int:
-    """Bytes of workspace a prompt call of these sizes needs (may be 0)."""
+    """Bytes of workspace a prompt call of these sizes needs (may be 0): no less for more tokens or sequences."""
     return load_library().skinny_linear_workspace(tokens, sequences, heads, dk, dv)
 
 
