@@ -4,9 +4,12 @@
     attention on the columns in place -> gate -> 8 bits -> projection back,
     added to the residual stream
 
-The packed projection has the rows of kda.py's: q, k, v and the gate of 12
-heads of 128 (rows 0..6143), 128 rows this layer does not read, then one decay
-logit a head and pads.  The two projections are PreparedInt8 plans, the
+The packed projection has as many rows as kda.py's, and q, k, v and the gate of
+12 heads of 128 in the same places (rows 0..6143); then come 128 rows that this
+layer does not read, one decay logit a head, and pads.  It is another layer than
+KDA's and KDA weights do not run on it: those decay each channel (their F_A rows,
+through F_B), their rows 6272..6283 are beta, and their recurrence has a delta
+term, which this one has not.  The two projections are PreparedInt8 plans, the
 sequences' states a pool of fp32 [heads, 128, 128] matrices; a prompt of any
 lengths and a decode step share both.  The elementwise parts between them
 (lengths of q and k, gate, decay) are torch's.
@@ -57,12 +60,14 @@ class LinearLayer:
         self.packed.run(*self._quantized(x), rows)
         q, k, v, gate = (rows[:, i * WIDTH:(i + 1) * WIDTH].view(tokens, HEADS, DIM) for i in range(4))
         for part in (q, k):                     # unit length, in place
-            part /= part.float().norm(dim=-1, keepdim=True).clamp(min=1e-6).to(torch.bfloat16)
+            part /= part.float().norm(dim=-1, keepdim=True).clamp(min=1e-6)     # fp32, rounded once
         logit = rows[:, DECAY_COLUMN:DECAY_COLUMN + HEADS].float()
         return q, k, v, gate, -self.decay_rate * torch.nn.functional.softplus(logit)
 
     def finish(self, mixed, gate, residual):
         """residual [tokens, hidden] fp32, plus the projection of the gated heads (in place); returns it."""
+        # gate and product in BF16, the type of both: their roundings, 2^-8 of a value, are about the 8 bits' that
+        # follow, half a step of 127 to the row's largest
         gated = (mixed * torch.sigmoid(gate)).view(mixed.shape[0], WIDTH)
         return self.out.run(*self._quantized(gated), residual, residual=residual)
 
