@@ -412,7 +412,8 @@ typedef enum {
  * multiplied by 2^64 on the way, so that 127 / max stays finite.  M = 0 does
  * nothing.  Any K >= 1 and any pitch >= K; x must be aligned to its elements.
  * Pitches and pointers that are multiples of 16 bytes (x) and 8 bytes (q) are
- * read and written in whole vectors.  Asynchronous on `stream`; one launch.
+ * read and written in whole vectors.  Asynchronous on `stream`; one launch (more
+ * for more than 4 million rows).
  */
 skinny_status skinny_quantize_rows(const void *x, skinny_type type, int M, int K, long long ldx, void *q,
                                    long long ldq, float *scale, void *stream);

@@ -648,17 +648,31 @@ skinny_status hip_bad(hipError_t e, const char *what)
 bool is_type(int t) { return t == SKINNY_TYPE_BF16 || t == SKINNY_TYPE_F32 || t == SKINNY_TYPE_F16; }
 int type_bytes(int t) { return t == SKINNY_TYPE_F32 ? 4 : 2; }
 
+// One workgroup a row, in several launches where their threads pass 2^32 - 1, the most that one may have.
+hipError_t launch_rows(const void *fn, QArgs a, int M, int type_bytes, unsigned threads, hipStream_t stream)
+{
+    void *params[] = {&a};
+    const int most = (int)(0xFFFFFFFFu / threads);
+    for (int left = M; left > 0; left -= most) {
+        const int rows = left < most ? left : most;
+        const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)rows), dim3(threads), params, 0, stream);
+        if (e != hipSuccess)
+            return e;
+        a.x = static_cast<const char *>(a.x) + rows * a.ldx * type_bytes;
+        a.q += rows * a.ldq;
+        a.scale += rows;
+    }
+    return hipSuccess;
+}
+
 template <int TYPE>
 hipError_t launch_quantize(const QArgs &a, int M, hipStream_t stream)
 {
-    constexpr int kVec = Elem<TYPE>::kVec;
-    QArgs copy = a;
-    void *params[] = {&copy};
+    constexpr int kVec = Elem<TYPE>::kVec, kBytes = sizeof(typename Elem<TYPE>::raw);
     const bool vec = a.K % kVec == 0 && (uintptr_t)a.x % 16 == 0 && a.ldx % kVec == 0 &&
                      (uintptr_t)a.q % kVec == 0 && a.ldq % kVec == 0;
     if (!vec)
-        return hipLaunchKernel(reinterpret_cast<const void *>(quantize_element<TYPE>), dim3(M), dim3(256), params, 0,
-                               stream);
+        return launch_rows(reinterpret_cast<const void *>(quantize_element<TYPE>), a, M, kBytes, 256, stream);
     const int vecs = a.K / kVec;
     // four vectors a thread, 64 to 1024 threads
     int threads = 64;
@@ -670,7 +684,7 @@ hipError_t launch_quantize(const QArgs &a, int M, hipStream_t stream)
                      : per <= 4 ? reinterpret_cast<const void *>(quantize_vector<TYPE, 4>)
                      : per <= 5 ? reinterpret_cast<const void *>(quantize_vector<TYPE, 5>)
                                 : reinterpret_cast<const void *>(quantize_vector<TYPE, 0>);
-    return hipLaunchKernel(fn, dim3(M), dim3(threads), params, 0, stream);
+    return launch_rows(fn, a, M, kBytes, (unsigned)threads, stream);
 }
 
 // Two units ahead where there are few registers to fill (one row tile, one
