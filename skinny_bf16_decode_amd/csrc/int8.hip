@@ -259,10 +259,11 @@ struct PArgs {
 // Weight rows into MFMA operands: lane l of step s of row tile t takes row
 // 16 t + l % 16, bytes 64 s + 16 (l / 16) .. + 15, so that a wave's load of an
 // operand is 1 KiB in a row.
+// Vectors `first` .. count - 1.
 __global__ __launch_bounds__(256) void lay_out(const signed char *w, long long ldw, int N, int K, int pitch,
-                                               u32x4 *out, long long count)
+                                               u32x4 *out, long long first, long long count)
 {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long i = first + (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= count)
         return;
     const int lane = (int)(i & 63);
@@ -771,21 +772,47 @@ Tiling tiles_tiling(int M, int N)
 // against 36 us, 800 of 1500 x 7168 25 against 29 us.
 hipError_t launch_product(PArgs a, hipStream_t stream)
 {
+    constexpr unsigned kThreads = 512;
+    constexpr int kSplit = 256;                 // rows and tokens of the largest tile: both halves begin on one
     void *params[] = {&a};
     const Tiling rows = rows_tiling(a.M, a.N);
-    if (a.M > 64) {
-        const Tiling tiles = tiles_tiling(a.M, a.N);
-        if (tiles.us < rows.us) {
-            a.n_tiles = (a.N + 255) / 256;
-            a.m_tiles = (a.M + 32 * tiles.t - 1) / (32 * tiles.t);
-            return hipLaunchKernel(tiles_kernel(tiles.t), dim3((unsigned)((long long)a.n_tiles * a.m_tiles)),
-                                   dim3(512), params, (size_t)tiles_lds(tiles.t), stream);
+    const Tiling tiles = a.M > 64 ? tiles_tiling(a.M, a.N) : rows;
+    const bool many = tiles.us < rows.us;
+    const int n_rows = many ? 256 : 16 * rows.r, tokens = many ? 32 * tiles.t : 16 * rows.t;
+    const long long n_tiles = ((long long)a.N + n_rows - 1) / n_rows, m_tiles = ((long long)a.M + tokens - 1) / tokens;
+    if (n_tiles * m_tiles > 0xFFFFFFFFu / kThreads) {
+        // more threads than a launch may have: the two halves of the longer side, one after the other
+        const int bytes = type_bytes(a.type);
+        PArgs second = a;
+        if (a.M >= a.N) {
+            const int first = a.M / 2 / kSplit * kSplit;
+            second.M = a.M - first;
+            second.x += first * a.ldx;
+            second.x_scale += first;
+            second.out = static_cast<char *>(a.out) + first * a.ldo * bytes;
+            if (a.res)
+                second.res = static_cast<const char *>(a.res) + first * a.ldr * bytes;
+            a.M = first;
+        } else {
+            const int first = a.N / 2 / kSplit * kSplit;
+            second.N = a.N - first;
+            second.w += (long long)(first / 16) * a.pitch * 64;
+            second.w_scale += first;
+            second.out = static_cast<char *>(a.out) + (long long)first * bytes;
+            if (a.res)
+                second.res = static_cast<const char *>(a.res) + (long long)first * bytes;
+            a.N = first;
         }
+        const hipError_t e = launch_product(a, stream);
+        return e == hipSuccess ? launch_product(second, stream) : e;
     }
-    a.m_tiles = (a.M + 16 * rows.t - 1) / (16 * rows.t);
-    a.n_tiles = (a.N + 16 * rows.r - 1) / (16 * rows.r);
-    const void *fn = a.m_tiles == 1 ? rows_kernel<true>(rows.r, rows.t) : rows_kernel<false>(rows.r, rows.t);
-    return hipLaunchKernel(fn, dim3((unsigned)((long long)a.n_tiles * a.m_tiles)), dim3(512), params, 0, stream);
+    a.n_tiles = (int)n_tiles;
+    a.m_tiles = (int)m_tiles;
+    const void *fn = many                ? tiles_kernel(tiles.t)
+                     : a.m_tiles == 1 ? rows_kernel<true>(rows.r, rows.t)
+                                      : rows_kernel<false>(rows.r, rows.t);
+    return hipLaunchKernel(fn, dim3((unsigned)(n_tiles * m_tiles)), dim3(kThreads), params,
+                           many ? (size_t)tiles_lds(tiles.t) : 0, stream);
 }
 
 // Dynamic LDS past 64 KiB has to be asked for, on every device that the kernels run on.
@@ -846,7 +873,7 @@ skinny_status skinny_int8_prepare(const void *Wq, int N, int K, long long ldw, c
         return bad(SKINNY_ERR_ALIGN, "w_scale must be 4-byte aligned");
     const int steps = (K + kStep - 1) / kStep, pitch = (steps + 1) / 2 * 2;
     const long long tiles = ((long long)N + 15) / 16, count = tiles * pitch * 64;
-    if (count >= 1LL << 36 || (count + 255) / 256 > 0x7FFFFFFFLL)
+    if (count >= 1LL << 36)
         return bad(SKINNY_ERR_SHAPE, "N=%d by K=%d is too large", N, K);
     skinny_int8_plan *p = new (std::nothrow) skinny_int8_plan{N, K, pitch, out_type, 0, nullptr, nullptr};
     if (!p)
@@ -864,13 +891,14 @@ skinny_status skinny_int8_prepare(const void *Wq, int N, int K, long long ldw, c
     const hipStream_t s = (hipStream_t)stream;
     if (e == hipSuccess)
         e = hipMemcpyAsync(p->w_scale, w_scale, (size_t)N * sizeof(float), hipMemcpyDeviceToDevice, s);
-    if (e == hipSuccess) {
-        const signed char *src = static_cast<const signed char *>(Wq);
-        u32x4 *dst = static_cast<u32x4 *>(p->w);
+    const signed char *src = static_cast<const signed char *>(Wq);
+    u32x4 *dst = static_cast<u32x4 *>(p->w);
+    constexpr long long kMost = 1LL << 31;      // vectors a launch: it may not have 2^32 threads
+    for (long long first = 0; e == hipSuccess && first < count; first += kMost) {
         int n = N, k = K, ks = pitch;
-        long long ld = ldw, c = count;
-        void *params[] = {&src, &ld, &n, &k, &ks, &dst, &c};
-        e = hipLaunchKernel(reinterpret_cast<const void *>(lay_out), dim3((unsigned)((count + 255) / 256)), dim3(256),
+        long long ld = ldw, c = count, f = first, left = count - first < kMost ? count - first : kMost;
+        void *params[] = {&src, &ld, &n, &k, &ks, &dst, &f, &c};
+        e = hipLaunchKernel(reinterpret_cast<const void *>(lay_out), dim3((unsigned)((left + 255) / 256)), dim3(256),
                             params, 0, s);
     }
     if (e == hipSuccess)
