@@ -502,7 +502,9 @@ size_t skinny_linear_workspace(int tokens, int sequences, int heads, int dk, int
  * dv <= 1024, multiples of 8.  starts is read on the device, clamped to
  * 0 .. tokens; it should rise from 0 to tokens (tokens outside every sequence
  * are not written).  Asynchronous on `stream`; one launch, or three where a
- * sequence may be long; capturable.
+ * sequence may be long; capturable.  A call whose sequences and parts times
+ * heads pass 8 to 16 million workgroups of 64 or 128 columns is refused
+ * (SKINNY_ERR_SHAPE): give it some of the heads at a time.
  */
 skinny_status skinny_linear_prompt(const skinny_linear_args *args, void *stream);
 

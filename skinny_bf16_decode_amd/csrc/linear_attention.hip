@@ -1200,6 +1200,13 @@ hipError_t launch_prompt_type(const LArgs &a, const Shape &s, hipStream_t stream
     return wide ? launch_prompt<H, 32, 8, 1>(a, stream) : launch_prompt<H, 32, 4, 1>(a, stream);
 }
 
+// Threads of a workgroup of the form that launch_prompt_type takes.
+int threads_of(const Shape &s, int dk)
+{
+    const bool wide_waves = dk > 64 && dk <= 128 && !s.eight;
+    return s.cols == 128 && !wide_waves ? 512 : 256;
+}
+
 constexpr long long kMaxTokenStride = 1 << 24;
 
 skinny_status bad(skinny_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
@@ -1330,7 +1337,8 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
     if (p->sequences == 0)
         return SKINNY_OK;
     const Shape s = shape_of(p->tokens, p->sequences, p->heads, p->dk, p->dv);
-    if ((long long)s.places * p->heads * s.col_tiles > 0x7F000000LL)
+    // a launch of 2^32 threads or more runs a part of them and reports nothing; 8 more key heads' fill the last XCDs
+    if (((long long)s.places * p->key_heads + 8) * (p->heads / p->key_heads) * s.col_tiles > 0xFFFFFFFFLL / threads_of(s, p->dk))
         return bad(SKINNY_ERR_SHAPE, "tokens=%d, sequences=%d and heads=%d are too many for one call", p->tokens,
                    p->sequences, p->heads);
     const Workspace w = workspace_of(p->tokens, p->sequences, p->heads, p->dk, p->dv);

@@ -43,3 +43,17 @@ def test_many_short_sequences():
     assert la.workspace_bytes(200000, 2000, heads, dk, dv) <= 2 * (200000 // 256) * (state + heads * 8)
     assert la.workspace_bytes(100000, 512, heads, dk, dv) <= 2 * (100000 // 256) * (state + heads * 8)
     assert la.workspace_bytes(100000, 65535, heads, dk, dv) <= 2 * (100000 // 256) * (state + heads * 8)
+
+
+def test_more_workgroups_than_a_launch_has_are_refused():
+    """2^32 threads in one launch would run a part of them without an error."""
+    import ctypes
+
+    import skinny_bf16_decode_amd as sk
+    p = 0x10000                 # a 16-byte aligned address that is never read
+    for heads, key_heads, dk, dv in ((300, 300, 32, 32), (256, 1, 128, 128), (32, 16, 64, 1024)):
+        a = la._Args(q=p, k=p, v=p, out=p, log_decay=p, starts=p, q_token=64, k_token=64, v_token=64, out_token=64,
+                     type=0, tokens=65535, sequences=65535, heads=heads, key_heads=key_heads, dk=dk, dv=dv, pool=0,
+                     scale=1.0, workspace=p, workspace_bytes=1 << 50)
+        assert sk.load_library().skinny_linear_prompt(ctypes.byref(a), None) == 2, (heads, dv)
+        assert "too many" in sk.last_error()
