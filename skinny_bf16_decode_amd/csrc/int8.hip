@@ -136,7 +136,8 @@ __device__ __forceinline__ int to_int8(float v, const RowScale &r)
 // One workgroup a row.  The row is read once: up to VECS 16-byte vectors a
 // thread stay in registers between the maximum and the rounding (VECS = 0: the
 // row is longer than that, and read again).  Bound by bytes: K (2 or 4 read +
-// 1 written) a row.  6001 x 7168 in BF16: 23.2 us, 5.6 TB/s; 4 rows: 3.0 us.
+// 1 1 written) a row.  6001 x 7168 in BF16: 23.2 us, 5.6 TB/s, in fp32 (4-byte
+// stores) 38 us, 5.7 TB/s; 4 rows: 3.0 us.
 template <int TYPE, int VECS>
 __global__ __launch_bounds__(1024) void quantize_vector(QArgs a)
 {
@@ -375,11 +376,13 @@ __device__ __forceinline__ unsigned logical_id()
 // at the end through LDS.  Loads go into registers, D units ahead.  x is read
 // in whole lines, eight rows of 128 bytes a load, and passes through the wave's
 // own LDS on its way into operands: gathered by the operands' lanes, 64 bytes
-// of 16 rows a load, it held the CU's one load path longest (64 x 7168 x 18432:
-// 53 against 36 us; x alone takes 17 us, w alone 22).  What bounds it is that
-// path: 16 K (RT + MT) bytes a workgroup, most of them w's and late (132 MB at
-// 3.6 TB/s there, 45 MB at 4.8 TB/s for one token of 6288 x 7168).  NT: the
-// weight passes by once (a single token tile) and need not stay in the caches.
+// of 16 rows a load, 64 x 7168 x 18432 took 53 against 36 us.  What bounds it is
+// a workgroup's 16 K (RT + MT) bytes of loads: x alone takes 17 us there and w
+// alone 22, so the two add (132 MB of w at 3.6 TB/s; 45 MB at 4.8 TB/s for one
+// token of 6288 x 7168).  They come at some 21 bytes a cycle and CU; whether that
+// is the rate of its path or the wait for the units under way has not been told
+// apart.  NT: the weight passes by once (a single token tile) and need not stay
+// in the caches.
 template <int RT, int MT, int D, bool NT>
 __global__ __launch_bounds__(512) void product_rows(PArgs a)
 {
@@ -477,16 +480,6 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
     }
 }
 
-// Many tokens: 256 weight rows by 32 T0 tokens a workgroup of eight waves, each
-// a quarter of the rows by half of the tokens, 4 x T0 products a K step.  Both
-// operands are copied to LDS, two K steps a stage and up to three stages ahead
-// -- w lies in MFMA order, x goes by lines, its 16-byte chunks in an order
-// without bank conflicts -- and read into registers one step ahead of the
-// products.  Bound by the matrix units and LDS side by side: 28 products of 16
-// cycles against 11 reads of 1 KiB a wave and step (T0 = 7).  Reads ahead, and
-// spread over the products, made 4000 x 6288 x 7168 193 -> 165 to 169 us (2130 TOP/s;
-// the library's product alone, without scales, 178 us); a third stage at T0 = 3
-// made 800 x 6288 x 7168 65 -> 51 us.
 // s_waitcnt for at most `vm` vector memory and `lgkm` LDS operations under way.
 constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (vm >> 4) << 14 | 0x70 | lgkm << 8; }
 
@@ -510,6 +503,16 @@ struct TilesLayout {
     static constexpr int kBytes = kStages * kVecs * 16;
 };
 
+// Many tokens: 256 weight rows by 32 T0 tokens a workgroup of eight waves, each
+// a quarter of the rows by half of the tokens, 4 x T0 products a K step.  Both
+// operands are copied to LDS, two K steps a stage and up to three stages ahead
+// -- w lies in MFMA order, x goes by lines, its 16-byte chunks in an order
+// without bank conflicts -- and read into registers one step ahead of the
+// products.  Bound by the matrix units and LDS side by side: 28 products of 16
+// cycles against 11 reads of 1 KiB a wave and step (T0 = 7).  Reads ahead, and
+// spread over the products, made 4000 x 6288 x 7168 193 -> 165 to 169 us (2130 TOP/s;
+// the library's product alone, without scales, 178 us); a third stage at T0 = 3
+// made 800 x 6288 x 7168 65 -> 51 us.
 template <int T0>
 __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 {
@@ -729,8 +732,11 @@ int tiles_lds(int t0)
          : t0 == 7 ? TilesLayout<7>::kBytes : TilesLayout<8>::kBytes;
 }
 
-// A tile shape and the time of its rounds over 256 CUs, in us over K = 7168
-// (other K change both kernels' alike).
+// A tile shape and the time of its rounds over 256 CUs, in us over K = 7168.
+// Other K change both kernels' alike, but for starts and ends: over 512 to 6288
+// rows and 72 to 3200 tokens the kernel taken was within a geometric mean of 3.0,
+// 1.8, 1.1 and 0.7 % of the better one at K = 512, 1536, 7168 and 18432 (at
+// worst 1.2 to 1.7 times it, 3200 tokens of 512 rows).
 struct Tiling {
     int r, t;                   // 16 r rows by 16 t tokens, or 256 rows by 32 t tokens
     float us;
@@ -767,8 +773,8 @@ Tiling tiles_tiling(int M, int N)
     return best;
 }
 
-// Up to 64 tokens the rows kernel reads the weight once.  Above, the shorter
-// of both: 400 tokens of 6288 x 7168 54 against 42 us, of 3584 x 7168 26
+// Up to 64 tokens the rows kernel, which reads the weight once for every token
+// tile (one to four).  Above, the shorter of both: 400 tokens of 6288 x 7168 54 against 42 us, of 3584 x 7168 26
 // against 36 us, 800 of 1500 x 7168 25 against 29 us.
 hipError_t launch_product(PArgs a, hipStream_t stream)
 {

@@ -623,10 +623,10 @@ __device__ __forceinline__ void update_state(const unsigned short *lds, const De
 
 // One part of a sequence for one head and 16 WAVES NV value columns, 16 NV a wave.
 // Bound by the waits of a chunk's four products, one after the other with three
-// barriers between: 5 us a chunk alone on a CU at dk = dv = 128, the matrix
-// units busy for 30 % of it and the vector units for a third (32768 tokens of
-// 12 heads: 67 us for the parts' own states, 124 us for the outputs, against
-// 85 us for the bytes; 16 sequences of 2048 tokens, whole: 143 us).
+// barriers between: 5 to 6 us a chunk alone on a CU at dk = dv = 128, the matrix
+// units busy for a third of it and the vector units for two fifths (BF16, 32768
+// tokens of 12 heads: 65 us for the parts' own states, 132 us for the outputs,
+// against 85 us for the bytes; 16 sequences of 2048 tokens, whole: 159 us).
 // OUT: outputs, and the sequence's new state after its last part.  Otherwise:
 // what the part alone adds to the state, for the parts after it.
 // Registers for two waves a SIMD; for one where LDS holds one workgroup a CU and

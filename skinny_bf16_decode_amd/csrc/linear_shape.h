@@ -14,7 +14,9 @@ struct Shape {
     int eight;                  // eight waves of 16 columns, one workgroup a CU, in place of four of 32
 };
 
-constexpr int kSlots = 512;     // workgroups the chip runs at once: two on each of 256 CUs
+// Workgroups the chip runs at once, two on each of 256 CUs: what the widest form
+// holds.  It stands for all (four waves at dk <= 64 fit three, eight waves one or two).
+constexpr int kSlots = 512;
 constexpr int kOnePass = 384;   // tokens up to which nothing is done in parts
 
 // Tokens of a part, for workgroups of `cols` columns.  The average is all that
@@ -26,9 +28,11 @@ inline int part_of(int tokens, int sequences, int heads, int dv, int cols)
     // as many parts as run at once, the same number for every sequence of the average length
     const long long units = columns * count, per_sequence = units < kSlots ? kSlots / units : 1;
     const long long even = ((average + per_sequence - 1) / per_sequence + kChunk - 1) / kChunk * kChunk;
-    // none shorter than 192 tokens: parts are done twice.  While there are CUs left, of 64 tokens, since a lone
-    // workgroup waits most of a chunk's 5 us (27 sequences, 5022 tokens, one head: parts of 64, 128, 256 30, 36,
-    // 52 us).  Where sequences are short, only the far longer ones are cut
+    // none shorter than 192 tokens, or 256 where those do not all run at once: parts are done twice.  While there
+    // are CUs left, of 64 tokens, since a lone workgroup waits most of a chunk's 5 us (8 sequences, 1720 tokens, two
+    // heads of 128: parts of 64, 128, 256 24, 27, 37 us).  Where sequences are short, only the far longer ones are
+    // cut, for every part that a launch has room for costs time (1000 sequences of 70 tokens, 12 heads, dk 64: parts
+    // of 64, 192, 384 780, 721, 663 us; with one of 1200 tokens among 41, two heads, 23, 26, 38 us)
     const auto fits = [&](int part, int most) { return columns * (tokens / part + count) <= most; };
     const int least = average < 80 ? kOnePass : fits(64, 160) ? 64 : fits(192, kSlots) ? 192 : 256;
     return (int)(even > least ? even : least);
@@ -38,16 +42,20 @@ inline Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
 {
     Shape s;
     // 128 columns a workgroup, or 64: where there are no more, or a last tile would be half empty; where the
-    // wide ones leave many CUs with one workgroup or none; and where that makes enough workgroups of whole
-    // sequences, of which no part is done twice (24 sequences of 12001 tokens, 12 heads, dk 64: 88 against 96 us)
+    // wide ones leave many CUs with one workgroup or none (1000 tokens, 12 heads of 128: 35 against 42 us); and where
+    // that makes enough workgroups of whole sequences, of which no part is done twice (20 of 3000 tokens, 12 heads,
+    // dk 64: 211 against 308 us), unless they are so long that uneven ones leave CUs idle (20 of 7000 in the mean,
+    // uneven: 765 against 664 us)
     const int part = part_of(tokens, sequences, heads, dv, 128);
     const long long wide = (dv + 127) / 128, narrow = (dv + 63) / 64, parts = tokens / part;
     const bool few = heads * wide * (parts > sequences ? parts : sequences) <= 300;
     const bool whole = heads * wide * sequences <= 300 && heads * narrow * sequences >= 3 * kSlots / 4 &&
                        (long long)tokens <= 4096LL * sequences;
     // 64 < dk <= 128: one workgroup of eight waves a CU, sequences uncut, where there are that many and few more
-    // (16 prompts of 2048 tokens, 12 heads of 128: 149 us); two of four waves a CU past that, which wait less in
-    // all (24 prompts: 254 against 282 us)
+    // (12 heads of 128, 16 prompts of 2048 tokens: 168 against 195 us); two of four waves a CU past that, which wait
+    // less in all (24 prompts: 274 against 317 us).  Fewer leave CUs idle (8 of 2048 tokens: 151 against 120 us),
+    // which short ones make up for (8 of 380: 39 against 47 us); long ones may be too uneven (16 of 6000: 707
+    // against 576 us with lengths within 30 %, but 461 against 517 with equal ones, and the host knows neither)
     const long long units = heads * wide * sequences, average = sequences > 0 ? tokens / sequences : 0;
     const bool middle = dk > 64 && dk <= 128 && dv > 64 && (dv <= 128 || dv > 192);
     s.eight = middle && units <= kSlots / 2 && average <= 4096 && (units >= 128 || (units >= 96 && average <= 384));
