@@ -21,7 +21,9 @@ def stream_handle(stream, index):
 
 def call_on(index, stream, entry, *args):
     """entry(*args, handle of the stream), its error raised, with GPU `index`
-    current: a default stream's handle names the current GPU's, whichever that is."""
+    current: a default stream's handle names the current GPU's, whichever that is.
+    The tensors of a call on a given stream are the caller's to order with that
+    stream and to keep until it has run."""
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream_handle(stream, index)
     if torch._C._cuda_getDevice() == index:
         status = entry(*args, handle)

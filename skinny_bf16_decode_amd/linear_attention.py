@@ -73,7 +73,8 @@ def _workspace(nbytes, device, stream):
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # the default stream's handle is 0, of which ExternalStream makes a new stream
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 

@@ -89,7 +89,9 @@ def gpu(monkeypatch):
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "stream", on_stream)
     monkeypatch.setattr(torch.cuda, "device", on_device)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle, device))
+    # as torch's: of handle 0 a new stream
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle or 0x99, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0, device))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: CURRENT, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: g.device, raising=False)
     return g
@@ -154,3 +156,10 @@ def test_workspace_on_another_gpu(gpu):
         gpu.log.clear()
         la.prompt(*attention_args(1), stream=stream)
         assert gpu.log == [("alloc", 1, handle), ("skinny_linear_prompt", 1, handle)]
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_workspace_on_the_default_stream_by_its_handle(gpu, index):
+    """Which is 0, what torch.cuda.current_stream().cuda_stream mostly is."""
+    la.prompt(*attention_args(index), stream=0)
+    assert gpu.log == [("alloc", index, 0), ("skinny_linear_prompt", index, 0)]
