@@ -196,7 +196,10 @@ __device__ __forceinline__ void half_range(float top, unsigned least, float &mul
     back = __uint_as_float(b);
 }
 
-__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float(inverse_power_bits(__float_as_uint(p))); }
+__device__ __forceinline__ float inverse_power(float p)
+{
+    return __uint_as_float(inverse_power_bits(__float_as_uint(p)));
+}
 
 // Whether any lane of the wave saw a value that is not finite: acc gathers x * 0.
 __device__ __forceinline__ bool wave_any_nan(float acc) { return __ballot(acc != 0.0f) != 0ull; }
@@ -1011,7 +1014,8 @@ __global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
 {
     const int head = blockIdx.y, seq = blockIdx.z;
     Place p;
-    place_of(a.starts[seq], a.starts[seq + 1], a.tokens, a.part, first_place(a.starts[seq], a.tokens, a.part, seq), seq, p);
+    const int start = a.starts[seq];
+    place_of(start, a.starts[seq + 1], a.tokens, a.part, first_place(start, a.tokens, a.part, seq), seq, p);
     const int parts = parts_of(p.len, a.part);
     const int at = (blockIdx.x * kThreads + threadIdx.x) * 4, size = a.dk * a.dv;
     if (parts < 2 || at >= size)
@@ -1055,7 +1059,7 @@ __global__ __launch_bounds__(kThreads) void linear_join(LArgs a)
 // (sequence, head): 8 threads of four columns by 32 rows of the state, so that
 // every load of the state is under way at once and a single sequence still
 // gives several workgroups a head.  Bound by the state's bytes, 8 dk dv a head.  64
-// sequences of 12 heads of 128: 20.6 us, 4.9 TB/s of a copy's 4.8; one: 4.2 us.
+// sequences of 12 heads of 128: 20.6 us, 4.9 TB/s of a copy's 4.8; one: 3.8 us.
 template <bool H>
 __global__ __launch_bounds__(kThreads, 4) void linear_step(LArgs a)
 {
@@ -1144,7 +1148,8 @@ struct Workspace {
 Workspace workspace_of(int tokens, int sequences, int heads, int dk, int dv)
 {
     const size_t parts = tokens > kOnePass ? (size_t)most_extra_parts(tokens, sequences, heads, dv) : 0;
-    return Workspace{parts, parts < (size_t)sequences ? parts : (size_t)sequences, (size_t)heads * dk * dv * sizeof(float)};
+    const size_t starts = parts < (size_t)sequences ? parts : (size_t)sequences;
+    return Workspace{parts, starts, (size_t)heads * dk * dv * sizeof(float)};
 }
 
 hipError_t launch_one(void (*fn)(LArgs), dim3 grid, int threads, size_t lds, const LArgs &a, hipStream_t stream)
@@ -1338,7 +1343,8 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *p, void *stream)
         return SKINNY_OK;
     const Shape s = shape_of(p->tokens, p->sequences, p->heads, p->dk, p->dv);
     // a launch of 2^32 threads or more runs a part of them and reports nothing; 8 more key heads' fill the last XCDs
-    if (((long long)s.places * p->key_heads + 8) * (p->heads / p->key_heads) * s.col_tiles > 0xFFFFFFFFLL / threads_of(s, p->dk))
+    const long long most = 0xFFFFFFFFLL / threads_of(s, p->dk);
+    if (((long long)s.places * p->key_heads + 8) * (p->heads / p->key_heads) * s.col_tiles > most)
         return bad(SKINNY_ERR_SHAPE, "tokens=%d, sequences=%d and heads=%d are too many for one call", p->tokens,
                    p->sequences, p->heads);
     const Workspace w = workspace_of(p->tokens, p->sequences, p->heads, p->dk, p->dv);

@@ -81,8 +81,8 @@ inline Shape shape_of(int tokens, int sequences, int heads, int dk, int dv)
 inline int most_extra_parts(int tokens, int sequences, int heads, int dv)
 {
     const long long columns = (long long)heads * ((dv + 127) / 128);
-    const long long few = cut_to(tokens / kChunk, 0, (int)(kSlots / columns)), many = cut_to(tokens / 256, 0, sequences);
-    return (int)(few > many ? few : many);
+    const int few = cut_to(tokens / kChunk, 0, (int)(kSlots / columns)), many = cut_to(tokens / 256, 0, sequences);
+    return few > many ? few : many;
 }
 
 }  // namespace skinny
