@@ -512,6 +512,147 @@ skinny_status skinny_linear_prompt(const skinny_linear_args *args, void *stream)
 skinny_status skinny_linear_step(const skinny_linear_args *args, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Blocks of 32 values with a power of two, and products with 4-bit weights
+ * ---------------------------------------------------------------------------
+ *
+ * The formats of OCP Microscaling Formats v1.0: 32 neighbouring values of a row
+ * share a power of two, held as a byte (e8m0: 2^(byte - 127), 255 is NaN); a
+ * value is one of e2m1's in 4 bits (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives; the first of a byte's two in its low half) or of e4m3's in 8 (up
+ * to 448, NaN but no infinity).  Rows of codes and of powers have pitches in
+ * bytes.  K is a multiple of 32.
+ */
+
+/*
+ * skinny_quantize_blocks -- rows of v [M][K] to codes of `bits` (4 or 8) in q
+ * (row m at m * ldq bytes) and powers in scale (row m at m * lds), where v = x
+ * (element m * ldx + k, `type`) or, with a gate (NULL for none; element
+ * m * ldg + k, the same type), v = x (gate / (1 + exp(-gate))) in fp32:
+ *
+ *   power = max(floor(log2 max |v|) - e, -127), e = 2 (4 bits) or 8
+ *   q = nearest(v 2^-power), ties to even, past 6 or 448 that value
+ *
+ * A block of zeros has byte 0; one with an infinity or NaN byte 255, codes 0.
+ * x and gate must be aligned to their elements; whole 16-byte vectors of them
+ * (and 4 or 8 bytes of q) are fastest.  M = 0 does nothing.  Asynchronous on
+ * `stream`; one launch (more for more than 2^33 values); capturable.
+ */
+skinny_status skinny_quantize_blocks(const void *x, skinny_type type, int M, int K, long long ldx, const void *gate,
+                                     long long ldg, int bits, void *q, long long ldq, void *scale, long long lds,
+                                     void *stream);
+
+/*
+ * skinny_expand_blocks -- what codes stand for: out[m][k] (element m * ldo + k)
+ * = value 2^power, rounded once to `type`.
+ */
+skinny_status skinny_expand_blocks(const void *q, int bits, int M, int K, long long ldq, const void *scale,
+                                   long long lds, void *out, skinny_type type, long long ldo, void *stream);
+
+typedef struct skinny_mxfp4_plan skinny_mxfp4_plan;
+
+/*
+ * skinny_mxfp4_prepare -- a plan for a 4-bit weight Wq [N][K / 2 bytes] (row n
+ * at n * ldw) with powers w_scale [N][K / 32] (row n at n * ldws).  Both are
+ * copied, laid out in the order in which the matrix units take them, on
+ * `stream`, which is waited for, so the caller may free them afterwards.  Must
+ * not be called during graph capture.  N >= 1; K % 32 == 0 and K <= 2^22.
+ */
+skinny_status skinny_mxfp4_prepare(const void *Wq, int N, int K, long long ldw, const void *w_scale, long long ldws,
+                                   skinny_type out_type, void *stream, skinny_mxfp4_plan **plan);
+
+/*
+ * skinny_mxfp4_run -- for M >= 0 tokens, asynchronously on `stream`,
+ *
+ *   out[m][n] = sum over blocks 2^(x power + w power) sum in the block (x w)  (+ residual[m][n])
+ *
+ * xq: codes of `bits` (4 or 8), row m at m * ldx bytes, 16-byte aligned,
+ * ldx % 16 == 0 and <= 2^22; x_scale: row m at m * ldxs, <= 2^22, any alignment.
+ * Products are exact (but for 8-bit values below 2^-133) and sums fp32, in an
+ * order that depends on the sizes alone.  residual
+ * (NULL for none) and out have the plan's out type, elements m * ldr + n and
+ * m * ldo + n; residual may be out itself (ldr == ldo) but must not otherwise
+ * overlap out.  A NaN (a power of 255, an 8-bit code) reaches the outputs that
+ * its row makes.  No allocation or synchronisation: may be captured in a graph.
+ * Runs change nothing in a plan, so one plan may run on several streams at once.
+ */
+skinny_status skinny_mxfp4_run(const skinny_mxfp4_plan *plan, const void *xq, int bits, long long ldx,
+                               const void *x_scale, long long ldxs, const void *residual, long long ldr, void *out,
+                               long long ldo, int M, void *stream);
+
+/* skinny_mxfp4_destroy -- frees the plan after synchronising its device.  NULL is a no-op. */
+void skinny_mxfp4_destroy(skinny_mxfp4_plan *plan);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Norms before and after a block, with its gate and residual
+ * ---------------------------------------------------------------------------
+ */
+typedef enum {
+    SKINNY_ROWS_NONE = 0,
+    SKINNY_ROWS_INT8 = 1,       /* skinny_quantize_rows': q [M][K], fp32 scale [M] */
+    SKINNY_ROWS_MX4 = 2,        /* skinny_quantize_blocks' 4 and 8 bits: q and scale with pitches in bytes */
+    SKINNY_ROWS_MX8 = 3
+} skinny_rows_kind;
+
+typedef struct {
+    const void *x, *weight;     /* [M][K] and [K] */
+    void *out;                  /* [M][K], or NULL */
+    void *q, *scale;            /* of q_kind */
+    long long ldx, ldo;         /* in elements */
+    long long ldq, lds;         /* in bytes */
+    double eps;                 /* 2^-120 to 2^120 */
+    int x_type, weight_type, out_type;  /* skinny_type */
+    int q_kind;                 /* skinny_rows_kind */
+    int M, K;
+} skinny_norm_args;
+
+/*
+ * skinny_norm_rows -- the root-mean-square norm of each row,
+ *
+ *   n = (x r) weight,  r = 1 / sqrt(sum x^2 / K + eps),
+ *
+ * to out (rounded once) and, from its fp32 values, to q and scale; at least one
+ * of the two is asked for.  The squares are summed and r is computed in 64
+ * bits, r is rounded to fp32 once, and the two products are rounded one after
+ * the other.  Types are free of each other; M >= 0 and K >= 1 (blocks: whole
+ * ones), any pitches; pointers aligned to their elements (K % 8 == 0 and
+ * 16-byte aligned rows are fastest).  out may be x itself; nothing else may
+ * overlap.  Asynchronous on `stream`; one launch (more for more than 4 million
+ * rows); capturable.
+ */
+skinny_status skinny_norm_rows(const skinny_norm_args *args, void *stream);
+
+typedef struct {
+    const void *residual, *y;   /* [M][K] */
+    const void *weight;         /* [K]: the norm of y; NULL: none */
+    const void *gate;           /* [M][K], or [K] with ldg = 0; NULL: none */
+    void *out;                  /* [M][K] of the residual's type; may be residual or y (the same type) itself */
+    const void *next_weight;    /* [K]: the norm of out, to next_out (NULL: not) and q; NULL: none */
+    void *next_out, *q, *scale;
+    long long ldr, ldy, ldg, ldo, ldn;  /* in elements; ldn: of next_out */
+    long long ldq, lds;         /* in bytes */
+    double eps;                 /* of both norms */
+    float alpha, beta;
+    int residual_type, y_type, weight_type, gate_type, next_weight_type, next_type;     /* skinny_type */
+    int q_kind;                 /* skinny_rows_kind */
+    int sigmoid;                /* 1: the gate is 1 / (1 + exp(-gate)) */
+    int M, K;
+} skinny_join_args;
+
+/*
+ * skinny_join_rows -- a block's end and the next one's beginning:
+ *
+ *   out = beta residual + alpha (gate z),  z = norm(y) by weight, or y
+ *   next_out, q = norm(out) by next_weight, of out as it is held
+ *
+ * each product and sum rounded to fp32 in that order, norms as in
+ * skinny_norm_rows.  Asynchronous on `stream`; one launch (more for more than 4
+ * million rows); capturable.
+ */
+skinny_status skinny_join_rows(const skinny_join_args *args, void *stream);
+
+/*
  * Measurement helpers (not part of the projection).  They put the projection's
  * timings in context: the decode-step cost the pages care about is streaming
  * the weight at HBM speed, so a bench compares against what a plain stream of

@@ -121,6 +121,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "skinny_linear_workspace": (sz, [i, i, i, i, i]),
         "skinny_linear_prompt": (i, [vp, vp]),
         "skinny_linear_step": (i, [vp, vp]),
+        "skinny_quantize_blocks": (i, [vp, i, i, i, ll, vp, ll, i, vp, ll, vp, ll, vp]),
+        "skinny_expand_blocks": (i, [vp, i, i, i, ll, vp, ll, vp, i, ll, vp]),
+        "skinny_mxfp4_prepare": (i, [vp, i, i, ll, vp, ll, i, vp, ctypes.POINTER(planp)]),
+        "skinny_mxfp4_run": (i, [planp, vp, i, ll, vp, ll, vp, ll, vp, ll, i, vp]),
+        "skinny_mxfp4_destroy": (None, [planp]),
+        "skinny_norm_rows": (i, [vp, vp]),
+        "skinny_join_rows": (i, [vp, vp]),
         "skinny_probe_read": (i, [vp, sz, vp, vp]),
         "skinny_probe_read_blocks": (i, []),
         "skinny_probe_empty": (i, [vp]),

@@ -8,9 +8,9 @@
 #include <hip/hip_runtime.h>
 
 #include <new>
-#include <stdarg.h>
-#include <stdio.h>
 
+#include "operators.h"
+#include "rows.h"
 #include "skinny_internal.h"
 
 // A prepared 8-bit weight.
@@ -26,8 +26,6 @@ struct skinny_int8_plan {
 namespace skinny {
 namespace {
 
-typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
-typedef __attribute__((ext_vector_type(2))) unsigned int u32x2;
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
@@ -37,56 +35,6 @@ constexpr int kStep = 64;       // bytes of K a 16x16x64 MFMA takes
 // Rows to 8-bit integers
 // ---------------------------------------------------------------------------
 
-template <int TYPE>
-struct Elem;
-template <>
-struct Elem<SKINNY_TYPE_BF16> {
-    typedef unsigned short raw;
-    static constexpr int kVec = 8;
-    static __device__ __forceinline__ float get(raw v) { return __uint_as_float((unsigned)v << 16); }
-    static __device__ __forceinline__ raw put(float v) { return __builtin_bit_cast(raw, (__bf16)v); }
-    static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[8])
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const unsigned int w = v[i];
-            f[2 * i] = __uint_as_float(w << 16);
-            f[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-        }
-    }
-};
-template <>
-struct Elem<SKINNY_TYPE_F16> {
-    typedef unsigned short raw;
-    static constexpr int kVec = 8;
-    static __device__ __forceinline__ float get(raw v) { return (float)__builtin_bit_cast(_Float16, v); }
-    static __device__ __forceinline__ raw put(float v) { return __builtin_bit_cast(raw, (_Float16)v); }
-    static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[8])
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const unsigned int w = v[i];
-            f[2 * i] = get((raw)(w & 0xFFFFu));
-            f[2 * i + 1] = get((raw)(w >> 16));
-        }
-    }
-};
-template <>
-struct Elem<SKINNY_TYPE_F32> {
-    typedef float raw;
-    static constexpr int kVec = 4;
-    static __device__ __forceinline__ float get(raw v) { return v; }
-    static __device__ __forceinline__ raw put(float v) { return v; }
-    static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[4])
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const unsigned int w = v[i];
-            f[i] = __uint_as_float(w);
-        }
-    }
-};
-
 struct QArgs {
     const void *x;
     signed char *q;
@@ -94,44 +42,6 @@ struct QArgs {
     long long ldx, ldq;
     int K;
 };
-
-// Magnitude bits of an fp32 value: ordered as unsigned integers like the
-// values, with infinity and NaN (which a maximum of floats would drop) on top.
-__device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-__device__ __forceinline__ unsigned wave_max_u(unsigned v)
-{
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-        const unsigned o = (unsigned)__shfl_xor((int)v, s, 64);
-        v = o > v ? o : v;
-    }
-    return v;
-}
-
-// What a row's values are multiplied with, in two steps: lift (a power of
-// two), then 127 / (lifted maximum), rounded to fp32 once.
-struct RowScale {
-    float lift, inverse;
-    bool fine;                  // finite and not all zero
-};
-
-__device__ __forceinline__ RowScale row_scale(unsigned top_bits, float &scale)
-{
-    RowScale r;
-    const float top = __uint_as_float(top_bits);
-    const bool finite = top_bits < 0x7F800000u;
-    r.fine = finite && top_bits != 0u;
-    r.lift = top < 0x1p-60f ? 0x1p64f : 1.0f;
-    r.inverse = r.fine ? __fdiv_rn(127.0f, top * r.lift) : 0.0f;
-    scale = finite ? __fdiv_rn(top, 127.0f) : __uint_as_float(0x7FC00000u);
-    return r;
-}
-
-__device__ __forceinline__ int to_int8(float v, const RowScale &r)
-{
-    return r.fine ? (int)rintf(__fmul_rn(__fmul_rn(v, r.lift), r.inverse)) : 0;
-}
 
 // One workgroup a row.  The row is read once: up to VECS 16-byte vectors a
 // thread stay in registers between the maximum and the rounding (VECS = 0: the
@@ -631,26 +541,6 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-
-skinny_status bad(skinny_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-skinny_status bad(skinny_status s, const char *fmt, ...)
-{
-    char buf[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_error("%s", buf);
-    return s;
-}
-
-skinny_status hip_bad(hipError_t e, const char *what)
-{
-    return bad(e == hipErrorOutOfMemory ? SKINNY_ERR_NOMEM : SKINNY_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool is_type(int t) { return t == SKINNY_TYPE_BF16 || t == SKINNY_TYPE_F32 || t == SKINNY_TYPE_F16; }
-int type_bytes(int t) { return t == SKINNY_TYPE_F32 ? 4 : 2; }
 
 // One workgroup a row, in several launches where their threads pass 2^32 - 1, the most that one may have.
 hipError_t launch_rows(const void *fn, QArgs a, int M, int type_bytes, unsigned threads, hipStream_t stream)

@@ -1,0 +1,887 @@
+// HIP kernels and entry points of blocks of 32 values with a power of two
+// (microscaled floating point), and of products with weights in them, for
+// gfx950 (CDNA4):
+//
+//   byte = power + 127, power = floor(log2 max |v|) - top,  q = nearest(v 2^-power)
+//   out[m][n] = sum over blocks b of 2^(xs[m][b] + ws[n][b] - 254) sum_{k in b} x[m][k] W[n][k]  (+ residual[m][n])
+//
+// W in 4 bits (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), x in 4 or
+// 8 (e4m3).  The matrix units take codes and powers as they are
+// (v_mfma_scale_f32_16x16x128_f8f6f4) and sum in fp32.
+#include <hip/hip_runtime.h>
+
+#include <new>
+
+#include "operators.h"
+#include "rows.h"
+#include "skinny_internal.h"
+
+// A prepared 4-bit weight.
+struct skinny_mxfp4_plan {
+    int N, K;
+    int units;                  // of 256 k, in w: the last one filled with zeros
+    skinny_type out;
+    int device;
+    void *w;                    // [N / 16][units][2 steps][64 lanes][16 bytes], zero past N and K
+    unsigned *w_scale;          // [N / 32][units][64 lanes]: bytes of two row tiles at two steps
+};
+
+namespace skinny {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) int i32x4;
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+
+constexpr long long kMostThreads = 0xFFFFFFFFLL;    // a launch may have
+
+// ---------------------------------------------------------------------------
+// Rows to blocks, and back
+// ---------------------------------------------------------------------------
+
+struct BArgs {
+    const void *x, *gate;       // gate: or NULL
+    unsigned char *q, *scale;
+    long long ldx, ldg, ldq, lds;
+    unsigned octets;            // in all rows of the launch
+    unsigned per_row;
+    FastDiv by_row;
+};
+
+__device__ __forceinline__ unsigned quotient(unsigned x, const FastDiv &f)
+{
+    const unsigned t = __umulhi(x, f.mul);
+    return (t + ((x - t) >> f.s1)) >> f.s2;
+}
+
+// Eight values a thread, four threads a block, U times 256 threads a workgroup.
+template <int TYPE, int BITS, bool GATE, bool VEC, int U>
+__global__ __launch_bounds__(256) void quantize_octets(BArgs a)
+{
+    constexpr int kBytes = sizeof(typename Elem<TYPE>::raw);
+    const unsigned first = blockIdx.x * (256u * U) + threadIdx.x;
+    Octet x[U], g[U];
+    long long row[U];
+    unsigned o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const unsigned i = first + 256u * u;
+        const unsigned r = quotient(i, a.by_row);
+        row[u] = r;
+        o[u] = i - r * a.per_row;
+        if (i < a.octets) {
+            const long long K = 8LL * a.per_row;
+            x[u] = load_octet<VEC>(static_cast<const char *>(a.x) + row[u] * a.ldx * kBytes, TYPE, (int)o[u], K);
+            if (GATE)
+                g[u] = load_octet<VEC>(static_cast<const char *>(a.gate) + row[u] * a.ldg * kBytes, TYPE, (int)o[u], K);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (first + 256u * u >= a.octets)
+            continue;                           // whole blocks: all four lanes of a quad or none
+        float f[8];
+        unpack_octet(x[u], TYPE, f);
+        if (GATE) {
+            float h[8];
+            unpack_octet(g[u], TYPE, h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] *= h[e] / (1.0f + expf(-h[e]));
+        }
+        unsigned byte;
+        const u32x2 codes = block_codes<BITS>(f, byte);
+        store_codes<VEC, BITS>(a.q + row[u] * a.ldq, (int)o[u], codes);
+        if ((o[u] & 3) == 0)
+            a.scale[row[u] * a.lds + (o[u] >> 2)] = (unsigned char)byte;
+    }
+}
+
+struct XArgs {
+    const unsigned char *q, *scale;
+    void *out;
+    long long ldq, lds, ldo;
+    int type;
+    unsigned octets, per_row;
+    FastDiv by_row;
+};
+
+template <int BITS, bool VEC>
+__global__ __launch_bounds__(256) void expand_octets(XArgs a)
+{
+    const unsigned i = blockIdx.x * 256u + threadIdx.x;
+    if (i >= a.octets)
+        return;
+    const unsigned r = quotient(i, a.by_row), o = i - r * a.per_row;
+    const unsigned char *p = a.q + r * a.ldq + (long long)o * BITS;
+    const float scale = power_of(a.scale[r * a.lds + (o >> 2)]);
+    unsigned w[BITS / 4];
+    if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < BITS / 4; ++j)
+            w[j] = reinterpret_cast<const unsigned *>(p)[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < BITS / 4; ++j)
+            w[j] = p[4 * j] | (unsigned)p[4 * j + 1] << 8 | (unsigned)p[4 * j + 2] << 16 | (unsigned)p[4 * j + 3] << 24;
+    }
+    float f[8];
+    if constexpr (BITS == 8) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
+            const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+            f[4 * j] = lo[0] * scale;
+            f[4 * j + 1] = lo[1] * scale;
+            f[4 * j + 2] = hi[0] * scale;
+            f[4 * j + 3] = hi[1] * scale;
+        }
+    } else {
+        const f32x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, 0),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, 1),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, 2),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, 3)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = v[j][0] * scale;
+            f[2 * j + 1] = v[j][1] * scale;
+        }
+    }
+    const Octet y = pack_octet(a.type, f);
+    store_octet<VEC>(static_cast<char *>(a.out) + r * a.ldo * (a.type == SKINNY_TYPE_F32 ? 4 : 2), a.type, (int)o,
+                     8LL * a.per_row, y);
+}
+
+// ---------------------------------------------------------------------------
+// The product
+// ---------------------------------------------------------------------------
+
+constexpr int kUnitBlocks = 8;  // blocks of a unit: 256 k, two MFMAs of 128
+
+struct PArgs {
+    const u32x4 *w;             // laid out by lay_out
+    const unsigned *w_scale;    // by lay_out_scales
+    const unsigned char *x, *x_scale;
+    const void *res;
+    void *out;
+    long long ldx, ldxs, ldr, ldo;      // in bytes, bytes, elements, elements
+    int M, N;
+    int x_bytes;                // of a row of x
+    int blocks;                 // K / 32
+    int units;                  // of 256 k
+    int type;                   // skinny_type of out and res
+    int vec;                    // out and res take four columns at once
+    int m_tiles;                // token tiles of the launch
+    int n_tiles;                // tiles of weight rows
+};
+
+// Weight rows into MFMA operands: at step s of unit u, lane l of row tile t
+// takes block 8 u + 2 (l / 16) + s of row 16 t + l % 16.  The blocks' order
+// inside a unit is the same for w and x, and such that a unit of a 4-bit row is
+// one line of 128 bytes.  16-byte vectors `first` .. count - 1.
+__global__ __launch_bounds__(256) void lay_out(const unsigned char *w, long long ldw, int N, int blocks, int units,
+                                               u32x4 *out, long long first, long long count)
+{
+    const long long i = first + (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= count)
+        return;
+    const int lane = (int)(i & 63), s = (int)(i >> 6) & 1;
+    const long long tu = i >> 7;
+    const long long n = tu / units * 16 + (lane & 15);
+    const int b = (int)(tu % units) * kUnitBlocks + 2 * (lane >> 4) + s;
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    if (n < N && b < blocks) {
+        const unsigned char *p = w + n * ldw + 16LL * b;
+        if (((uintptr_t)p & 15) == 0) {
+            v = *reinterpret_cast<const u32x4 *>(p);
+        } else {
+            for (int j = 0; j < 16; ++j)
+                v[j / 4] |= (unsigned)p[j] << (8 * (j % 4));
+        }
+    }
+    out[i] = v;
+}
+
+// Their powers: lane l of unit u of row tiles 2 p and 2 p + 1 has one dword,
+// the bytes of (2 p, step 0), (2 p, step 1), (2 p + 1, step 0), (2 p + 1, step 1).
+__global__ __launch_bounds__(256) void lay_out_scales(const unsigned char *s, long long lds, int N, int blocks,
+                                                      int units, unsigned *out, long long first, long long count)
+{
+    const long long i = first + (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= count)
+        return;
+    const int lane = (int)(i & 63);
+    const long long pu = i >> 6;
+    unsigned v = 0;
+    for (int j = 0; j < 4; ++j) {
+        const long long n = pu / units * 32 + 16 * (j >> 1) + (lane & 15);
+        const int b = (int)(pu % units) * kUnitBlocks + 2 * (lane >> 4) + (j & 1);
+        if (n < N && b < blocks)
+            v |= (unsigned)s[n * lds + b] << (8 * j);
+    }
+    out[i] = v;
+}
+
+// Four outputs of one token, columns n .. n + 3.
+template <int OUT>
+__device__ __forceinline__ void store4_as(const PArgs &a, int m, int n, f32x4 v)
+{
+    using E = Elem<OUT>;
+    typedef __attribute__((ext_vector_type(4))) typename E::raw raw4;
+    typename E::raw *o = static_cast<typename E::raw *>(a.out) + m * a.ldo + n;
+    const typename E::raw *res = a.res ? static_cast<const typename E::raw *>(a.res) + m * a.ldr + n : nullptr;
+    if (a.vec && n + 4 <= a.N) {
+        if (res) {
+            const raw4 x = *reinterpret_cast<const raw4 *>(res);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] += E::get(x[r]);
+        }
+        raw4 y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            y[r] = E::put(v[r]);
+        *reinterpret_cast<raw4 *>(o) = y;
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (n + r < a.N)
+            o[r] = E::put(res ? v[r] + E::get(res[r]) : v[r]);
+}
+
+__device__ __forceinline__ void store4(const PArgs &a, int m, int n, f32x4 v)
+{
+    if (a.type == SKINNY_TYPE_BF16)
+        store4_as<SKINNY_TYPE_BF16>(a, m, n, v);
+    else if (a.type == SKINNY_TYPE_F32)
+        store4_as<SKINNY_TYPE_F32>(a, m, n, v);
+    else
+        store4_as<SKINNY_TYPE_F16>(a, m, n, v);
+}
+
+// An operand of x: one vector of 32 4-bit values, or two of 16 8-bit ones.
+template <int BITS>
+struct XOp {
+    u32x4 v[BITS / 4];
+};
+
+__device__ __forceinline__ i32x8 widened(u32x4 v)
+{
+    const i32x4 w = __builtin_bit_cast(i32x4, v);
+    return __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
+// 16 rows of w by 16 tokens over 128 k, both in 4 bits; byte WB of ws is the
+// lanes' powers of w, xs those of x.
+template <int WB>
+__device__ __forceinline__ f32x4 mma128(u32x4 w, u32x4 x, f32x4 c, unsigned ws, unsigned xs)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widened(w), widened(x), c, 4, 4, WB, (int)ws, 0, (int)xs);
+}
+
+// Eight values times their power in BF16, which holds a code of either type
+// times any power that a block may have (8-bit values below 2^-133 apart).
+__device__ __forceinline__ bf16x8 bf16_of_4(unsigned w, float power)
+{
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 0);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 1);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 2);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 3);
+    return __builtin_shufflevector(__builtin_shufflevector(a, b, 0, 1, 2, 3), __builtin_shufflevector(c, d, 0, 1, 2, 3),
+                                   0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ bf16x8 bf16_of_8(unsigned lo, unsigned hi, float power)
+{
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, power, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, power, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, power, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, power, true);
+    return __builtin_shufflevector(__builtin_shufflevector(a, b, 0, 1, 2, 3), __builtin_shufflevector(c, d, 0, 1, 2, 3),
+                                   0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The 16-byte chunk of a row's unit (8 of them in 4 bits, 16 in 8) that is part
+// `part` of lane group g's operand at step s: block 2 g + s.
+template <int BITS>
+__device__ __forceinline__ int chunk_of(int g, int s, int part)
+{
+    return BITS / 4 * (2 * g + s) + part;
+}
+
+// A buffer load whose offset is past its resource reads zero and touches no
+// memory; loads to be skipped take this one (resources are smaller: 256 rows of
+// x at pitches below 2^22).  Offsets are all in the per-lane part, the one that
+// is checked whatever its value.
+constexpr unsigned kSkip = 0x7FF00000u;
+constexpr long long kMaxPitch = 1 << 22;
+constexpr int kMaxRows = 0x7FFFF000;     // of x and w: tiles are counted in 32 bits
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, unsigned bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// Consecutive logical ids on one XCD (the dispatcher deals workgroups over 8).
+__device__ __forceinline__ unsigned logical_id()
+{
+    const unsigned xcd = blockIdx.x & 7u, turn = blockIdx.x >> 3, q = gridDim.x >> 3, r = gridDim.x & 7u;
+    return xcd * q + (xcd < r ? xcd : r) + turn;
+}
+
+// The products of a unit: RT row tiles by MT token tiles, 256 k.  4-bit tokens
+// go into the scaled MFMA as they are.  8-bit ones could, but that one adds
+// neighbouring products of 8-bit codes in a fixed window: what is below 2^-13 of
+// the largest of them is lost.  They go in BF16, as does w then, at two values an
+// instruction and four cycles, and every product is added in fp32.
+template <int RT, int MT, int BITS>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[RT][MT], const u32x4 (&w)[2][RT], const XOp<BITS> (&x)[2][MT],
+                                         const unsigned *ws, const unsigned (&xs)[2][MT])
+{
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if (r % 2 == 0) {
+                    acc[r][t] = mma128<0>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
+                    acc[r][t] = mma128<1>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
+                } else {
+                    acc[r][t] = mma128<2>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
+                    acc[r][t] = mma128<3>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
+                }
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float wp[RT], xp[MT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                wp[r] = power_of(ws[r / 2] >> (16 * (r % 2) + 8 * k) & 0xFFu);
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                xp[t] = power_of(xs[k][t]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bf16x8 wv[RT], xv[MT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    wv[r] = bf16_of_4(w[k][r][j], wp[r]);
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    xv[t] = bf16_of_8(x[k][t].v[j / 2][2 * j % 4], x[k][t].v[j / 2][2 * j % 4 + 1], xp[t]);
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[r], xv[t], acc[r][t], 0, 0, 0);
+            }
+        }
+    }
+}
+
+// 16 RT weight rows by 16 MT tokens a workgroup, its eight waves taking every
+// eighth unit of 256 k: each holds all sums of the tile, which are added at the
+// end through LDS in a fixed order.  Loads go into registers, D units ahead.  x
+// is read in whole lines and passes through the wave's own LDS on its way into
+// operands, a token tile at a time.
+template <int RT, int MT, int BITS, int D, bool NT>
+__global__ __launch_bounds__(512) void product_rows(PArgs a)
+{
+    constexpr int kWaves = 8, kV = RT * MT;
+    constexpr int kLine = 32 * BITS;                    // bytes of a row's unit
+    constexpr int kPerRow = kLine / 16, kRows = 64 / kPerRow;   // vectors of a row's unit, rows of a load
+    constexpr int kLoads = 16 / kRows;                  // loads of a token tile's unit
+    constexpr int kTile = 16 * kPerRow;                 // vectors of a token tile's unit
+    constexpr int kS = (RT + 1) / 2;
+    __shared__ u32x4 shared[kWaves * kTile > 256 * kV ? kWaves * kTile : 256 * kV];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const unsigned id = logical_id();
+    const int mt = (int)(id % (unsigned)a.m_tiles), block = (int)(id / (unsigned)a.m_tiles);
+    const int n0 = block * 16 * RT, m0 = mt * 16 * MT;
+    const int row_tiles = min(RT, (a.N - n0 + 15) / 16), rows = min(16 * MT, a.M - m0);
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (long long)block * RT * a.units * 128,
+                                                (unsigned)(row_tiles * a.units) * 2048u);
+    const int pair = block * RT / 2;
+    const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.w_scale + (long long)pair * a.units * 64,
+                                                 (unsigned)((row_tiles + 1) / 2 * a.units) * 256u);
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + m0 * a.ldx, (unsigned)((rows - 1) * a.ldx) + (unsigned)a.x_bytes);
+    const __amdgpu_buffer_rsrc_t xsr = make_rsrc(a.x_scale + m0 * a.ldxs,
+                                                 (unsigned)((rows - 1) * a.ldxs) + (unsigned)a.blocks);
+    unsigned w_off[RT], x_off[MT * kLoads], xs_off[MT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        w_off[r] = (unsigned)(r * a.units) * 2048u + 16u * lane;
+    const int sub = lane / kPerRow, slot = lane % kPerRow;      // a load's row and 16-byte chunk of this lane
+#pragma unroll
+    for (int t = 0; t < MT * kLoads; ++t) {
+        const int row = kRows * t + sub;
+        x_off[t] = row < rows ? (unsigned)(row * a.ldx) + 16u * slot : kSkip;
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int row = 16 * t + (lane & 15);
+        xs_off[t] = row < rows ? (unsigned)(row * a.ldxs) + 2u * g : kSkip;
+    }
+    f32x4 acc[RT][MT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 wf[D][2][RT], xf[D][MT * kLoads];
+    unsigned ws[D][kS], xs[D][2][MT];
+    // past K neither codes nor powers of x may be read, which are other rows' and may stand for NaN
+    const auto load = [&](int d, int u) {
+        const bool in = u < a.units;
+        const unsigned wo = in ? (unsigned)u * 2048u : kSkip;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                wf[d][k][r] = __builtin_amdgcn_raw_buffer_load_b128(wr, w_off[r] + wo + 1024u * k, 0, NT ? 2 : 0);
+#pragma unroll
+        for (int r = 0; r < kS; ++r) {
+            const unsigned at = (unsigned)(r * a.units) * 256u + 4u * lane + (in ? (unsigned)u * 256u : kSkip);
+            if constexpr (RT == 1)
+                ws[d][r] = __builtin_amdgcn_raw_buffer_load_b16(wsr, at + 2u * (block & 1), 0, NT ? 2 : 0);
+            else
+                ws[d][r] = __builtin_amdgcn_raw_buffer_load_b32(wsr, at, 0, NT ? 2 : 0);
+        }
+        const unsigned xo = in && u * kLine + 16 * slot < a.x_bytes ? (unsigned)u * kLine : kSkip;
+#pragma unroll
+        for (int t = 0; t < MT * kLoads; ++t)
+            xf[d][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_off[t] + xo, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int b = kUnitBlocks * u + 2 * g + k;
+            const unsigned so = in && b < a.blocks ? (unsigned)(kUnitBlocks * u) + k : kSkip;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                xs[d][k][t] = __builtin_amdgcn_raw_buffer_load_b8(xsr, xs_off[t] + so, 0, 0);
+        }
+    };
+    // 16-byte chunk c of row r lies at c ^ (r % 8): written a row at a time and
+    // read a column at a time without bank conflicts
+    u32x4 *mine = shared + wave * kTile;
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        load(d, wave + kWaves * d);
+    for (int u = wave; u < a.units; u += kWaves * D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            XOp<BITS> x[2][MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    const int row = kRows * j + sub;
+                    mine[row * kPerRow + (slot ^ (row & 7))] = xf[d][t * kLoads + j];
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int p = 0; p < BITS / 4; ++p)
+                        x[k][t].v[p] = mine[(lane & 15) * kPerRow + (chunk_of<BITS>(g, k, p) ^ (lane & 7))];
+                __builtin_amdgcn_wave_barrier();
+            }
+            multiply<RT, MT, BITS>(acc, wf[d], x, ws[d], xs[d]);
+            load(d, u + kWaves * (d + D));
+        }
+    }
+    // waves 4..7 to LDS, 0..3 add theirs, all add the four
+    f32x4(*part)[kV][64] = reinterpret_cast<f32x4(*)[kV][64]>(shared);
+    __syncthreads();
+    if (wave >= 4) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            part[wave - 4][v][lane] = acc[v / MT][v % MT];
+    }
+    __syncthreads();
+    if (wave < 4) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            part[wave][v][lane] += acc[v / MT][v % MT];
+    }
+    __syncthreads();
+    for (int v = wave; v < kV; v += kWaves) {
+        const f32x4 sum = (part[0][v][lane] + part[1][v][lane]) + (part[2][v][lane] + part[3][v][lane]);
+        const int m = m0 + 16 * (v % MT) + (lane & 15), n = n0 + 16 * (v / MT) + 4 * g;
+        if (m < a.M && n < a.N)
+            store4(a, m, n, sum);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+bool is_bits(int bits) { return bits == 4 || bits == 8; }
+
+// Rows of a launch whose octets are counted in 31 bits.
+int rows_of_launch(int per_row) { return per_row >= 1 << 30 ? 1 : (1 << 30) / per_row; }
+
+template <int TYPE, int BITS>
+const void *quantize_kernel(bool gate, bool vec, bool many)
+{
+    if (!vec)
+        return gate ? reinterpret_cast<const void *>(quantize_octets<TYPE, BITS, true, false, 1>)
+                    : reinterpret_cast<const void *>(quantize_octets<TYPE, BITS, false, false, 1>);
+    if (gate)
+        return many ? reinterpret_cast<const void *>(quantize_octets<TYPE, BITS, true, true, 2>)
+                    : reinterpret_cast<const void *>(quantize_octets<TYPE, BITS, true, true, 1>);
+    return many ? reinterpret_cast<const void *>(quantize_octets<TYPE, BITS, false, true, 4>)
+                : reinterpret_cast<const void *>(quantize_octets<TYPE, BITS, false, true, 1>);
+}
+
+template <int BITS>
+const void *quantize_kernel_of(int type, bool gate, bool vec, bool many)
+{
+    return type == SKINNY_TYPE_F32   ? quantize_kernel<SKINNY_TYPE_F32, BITS>(gate, vec, many)
+           : type == SKINNY_TYPE_F16 ? quantize_kernel<SKINNY_TYPE_F16, BITS>(gate, vec, many)
+                                     : quantize_kernel<SKINNY_TYPE_BF16, BITS>(gate, vec, many);
+}
+
+template <int RT, int MT, int BITS, bool NT>
+const void *rows_fn()
+{
+    return reinterpret_cast<const void *>(product_rows<RT, MT, BITS, 1, NT>);
+}
+
+template <int RT, int BITS, bool NT>
+const void *rows_kernel_of(int mt)
+{
+    return mt == 1 ? rows_fn<RT, 1, BITS, NT>() : mt == 2 ? rows_fn<RT, 2, BITS, NT>()
+         : mt == 3 ? rows_fn<RT, 3, BITS, NT>() : rows_fn<RT, 4, BITS, NT>();
+}
+
+template <int BITS, bool NT>
+const void *rows_kernel(int rt, int mt)
+{
+    return rt == 1 ? rows_kernel_of<1, BITS, NT>(mt) : rt == 2 ? rows_kernel_of<2, BITS, NT>(mt)
+                                                               : rows_kernel_of<4, BITS, NT>(mt);
+}
+
+// A tile shape and the time of its rounds over 256 CUs.
+struct Tiling {
+    int r, t;                   // 16 r rows by 16 t tokens
+    float us;
+};
+
+// A round is as long as the bytes a workgroup loads; of equal ones the most tokens, which read the weight least often.
+Tiling rows_tiling(int M, int N, int bits)
+{
+    Tiling best{0, 0, 0.0f};
+    for (int t = min(4, (M + 15) / 16); t >= 1; --t)
+        for (int r = 1; r <= 4; r *= 2) {
+            const long long count = (long long)((N + 16 * r - 1) / (16 * r)) * ((M + 16 * t - 1) / (16 * t));
+            const float us = (float)((count + 255) / 256) * (float)(r + t * bits / 4);
+            if (!best.r || us < best.us)
+                best = Tiling{r, t, us};
+        }
+    return best;
+}
+
+hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
+{
+    constexpr unsigned kThreads = 512;
+    constexpr int kSplit = 256;                 // rows and tokens of the largest tile: both halves begin on one
+    void *params[] = {&a};
+    const Tiling rows = rows_tiling(a.M, a.N, bits);
+    const int n_rows = 16 * rows.r, tokens = 16 * rows.t;
+    const long long n_tiles = ((long long)a.N + n_rows - 1) / n_rows, m_tiles = ((long long)a.M + tokens - 1) / tokens;
+    if (n_tiles * m_tiles > kMostThreads / kThreads) {
+        // more threads than a launch may have: the two halves of the longer side, one after the other
+        const int bytes = type_bytes(a.type);
+        PArgs second = a;
+        if (a.M >= a.N) {
+            const int first = a.M / 2 / kSplit * kSplit;
+            second.M = a.M - first;
+            second.x += first * a.ldx;
+            second.x_scale += first * a.ldxs;
+            second.out = static_cast<char *>(a.out) + first * a.ldo * bytes;
+            if (a.res)
+                second.res = static_cast<const char *>(a.res) + first * a.ldr * bytes;
+            a.M = first;
+        } else {
+            const int first = a.N / 2 / kSplit * kSplit;
+            second.N = a.N - first;
+            second.w += (long long)(first / 16) * a.units * 128;
+            second.w_scale += (long long)(first / 32) * a.units * 64;
+            second.out = static_cast<char *>(a.out) + (long long)first * bytes;
+            if (a.res)
+                second.res = static_cast<const char *>(a.res) + (long long)first * bytes;
+            a.N = first;
+        }
+        const hipError_t e = launch_product(a, bits, stream);
+        return e == hipSuccess ? launch_product(second, bits, stream) : e;
+    }
+    a.n_tiles = (int)n_tiles;
+    a.m_tiles = (int)m_tiles;
+    const void *fn = bits == 4 ? (a.m_tiles == 1 ? rows_kernel<4, true>(rows.r, rows.t) : rows_kernel<4, false>(rows.r, rows.t))
+                               : (a.m_tiles == 1 ? rows_kernel<8, true>(rows.r, rows.t) : rows_kernel<8, false>(rows.r, rows.t));
+    return hipLaunchKernel(fn, dim3((unsigned)(n_tiles * m_tiles)), dim3(kThreads), params, 0, stream);
+}
+
+// fn(first vector, launch's end) over count vectors of 256-thread workgroups, in launches of fewer than 2^32 threads.
+template <typename F>
+hipError_t over_launches(long long count, F launch)
+{
+    constexpr long long kMost = 1LL << 31;
+    hipError_t e = hipSuccess;
+    for (long long first = 0; e == hipSuccess && first < count; first += kMost) {
+        const long long left = count - first < kMost ? count - first : kMost;
+        e = launch(first, dim3((unsigned)((left + 255) / 256)));
+    }
+    return e;
+}
+
+}  // namespace
+}  // namespace skinny
+
+using namespace skinny;
+
+extern "C" {
+
+skinny_status skinny_quantize_blocks(const void *x, skinny_type type, int M, int K, long long ldx, const void *gate,
+                                     long long ldg, int bits, void *q, long long ldq, void *scale, long long lds,
+                                     void *stream)
+{
+    if (!is_type((int)type))
+        return bad(SKINNY_ERR_INVALID_ARG, "type %d is none of BF16, F32 and F16", (int)type);
+    if (!is_bits(bits))
+        return bad(SKINNY_ERR_INVALID_ARG, "bits=%d is neither 4 nor 8", bits);
+    if (M < 0 || K < 1)
+        return bad(SKINNY_ERR_INVALID_ARG, "M=%d and K=%d: M >= 0 and K >= 1 are needed", M, K);
+    if (K % kBlock)
+        return bad(SKINNY_ERR_SHAPE, "K=%d must be a multiple of 32, whole blocks", K);
+    if (M == 0)
+        return SKINNY_OK;
+    if (!x || !q || !scale)
+        return bad(SKINNY_ERR_INVALID_ARG, "x, q or scale is NULL");
+    const int row_bytes = K / 8 * bits, blocks = K / kBlock;
+    if (ldx < K || (gate && ldg < K) || ldq < row_bytes || lds < blocks)
+        return bad(SKINNY_ERR_SHAPE, "ldx=%lld and ldg=%lld must be at least K=%d, ldq=%lld %d and lds=%lld %d", ldx, ldg,
+                   K, ldq, row_bytes, lds, blocks);
+    const int eb = type_bytes((int)type);
+    if ((uintptr_t)x % eb || (uintptr_t)gate % eb)
+        return bad(SKINNY_ERR_ALIGN, "x and gate must be aligned to their elements");
+    const bool vec = (uintptr_t)x % 16 == 0 && ldx * eb % 16 == 0 &&
+                     (!gate || ((uintptr_t)gate % 16 == 0 && ldg * eb % 16 == 0)) && (uintptr_t)q % bits == 0 &&
+                     ldq % bits == 0;
+    const int per_row = K / 8, most = rows_of_launch(per_row);
+    const bool whole = ldx == K && (!gate || ldg == K) && ldq == row_bytes && lds == blocks;
+    for (int done = 0; done < M;) {
+        const int rows = M - done < most ? M - done : most;
+        BArgs a{};
+        a.x = static_cast<const char *>(x) + done * ldx * eb;
+        a.gate = gate ? static_cast<const char *>(gate) + done * ldg * eb : nullptr;
+        a.q = static_cast<unsigned char *>(q) + done * ldq;
+        a.scale = static_cast<unsigned char *>(scale) + done * lds;
+        a.ldx = ldx;
+        a.ldg = ldg;
+        a.ldq = ldq;
+        a.lds = lds;
+        a.octets = (unsigned)rows * (unsigned)per_row;
+        // rows one after the other are one long row
+        a.per_row = whole ? a.octets : (unsigned)per_row;
+        a.by_row = make_fastdiv(a.per_row);
+        // several octets a thread once they fill the chip's threads all the same
+        const bool many = a.octets >= 1u << 20;
+        const unsigned per_group = 256u * (!vec || !many ? 1u : gate ? 2u : 4u);
+        const void *fn = bits == 4 ? quantize_kernel_of<4>((int)type, gate != nullptr, vec, many)
+                                   : quantize_kernel_of<8>((int)type, gate != nullptr, vec, many);
+        void *params[] = {&a};
+        const hipError_t e = hipLaunchKernel(fn, dim3((a.octets + per_group - 1) / per_group), dim3(256), params, 0,
+                                             (hipStream_t)stream);
+        if (e != hipSuccess)
+            return hip_bad(e, "quantize launch");
+        done += rows;
+    }
+    return SKINNY_OK;
+}
+
+skinny_status skinny_expand_blocks(const void *q, int bits, int M, int K, long long ldq, const void *scale,
+                                   long long lds, void *out, skinny_type type, long long ldo, void *stream)
+{
+    if (!is_type((int)type))
+        return bad(SKINNY_ERR_INVALID_ARG, "type %d is none of BF16, F32 and F16", (int)type);
+    if (!is_bits(bits))
+        return bad(SKINNY_ERR_INVALID_ARG, "bits=%d is neither 4 nor 8", bits);
+    if (M < 0 || K < 1)
+        return bad(SKINNY_ERR_INVALID_ARG, "M=%d and K=%d: M >= 0 and K >= 1 are needed", M, K);
+    if (K % kBlock)
+        return bad(SKINNY_ERR_SHAPE, "K=%d must be a multiple of 32, whole blocks", K);
+    if (M == 0)
+        return SKINNY_OK;
+    if (!q || !scale || !out)
+        return bad(SKINNY_ERR_INVALID_ARG, "q, scale or out is NULL");
+    const int row_bytes = K / 8 * bits, blocks = K / kBlock;
+    if (ldo < K || ldq < row_bytes || lds < blocks)
+        return bad(SKINNY_ERR_SHAPE, "ldo=%lld must be at least K=%d, ldq=%lld %d and lds=%lld %d", ldo, K, ldq,
+                   row_bytes, lds, blocks);
+    const int eb = type_bytes((int)type);
+    if ((uintptr_t)out % eb)
+        return bad(SKINNY_ERR_ALIGN, "out must be aligned to its elements");
+    const bool vec = (uintptr_t)out % 16 == 0 && ldo * eb % 16 == 0 && (uintptr_t)q % bits == 0 && ldq % bits == 0;
+    const int per_row = K / 8, most = rows_of_launch(per_row);
+    const bool whole = ldo == K && ldq == row_bytes && lds == blocks;
+    for (int done = 0; done < M;) {
+        const int rows = M - done < most ? M - done : most;
+        XArgs a{};
+        a.q = static_cast<const unsigned char *>(q) + done * ldq;
+        a.scale = static_cast<const unsigned char *>(scale) + done * lds;
+        a.out = static_cast<char *>(out) + done * ldo * eb;
+        a.ldq = ldq;
+        a.lds = lds;
+        a.ldo = ldo;
+        a.type = (int)type;
+        a.octets = (unsigned)rows * (unsigned)per_row;
+        a.per_row = whole ? a.octets : (unsigned)per_row;
+        a.by_row = make_fastdiv(a.per_row);
+        const void *fn = bits == 4 ? (vec ? reinterpret_cast<const void *>(expand_octets<4, true>)
+                                          : reinterpret_cast<const void *>(expand_octets<4, false>))
+                                   : (vec ? reinterpret_cast<const void *>(expand_octets<8, true>)
+                                          : reinterpret_cast<const void *>(expand_octets<8, false>));
+        void *params[] = {&a};
+        const hipError_t e = hipLaunchKernel(fn, dim3((a.octets + 255) / 256), dim3(256), params, 0,
+                                             (hipStream_t)stream);
+        if (e != hipSuccess)
+            return hip_bad(e, "expand launch");
+        done += rows;
+    }
+    return SKINNY_OK;
+}
+
+skinny_status skinny_mxfp4_prepare(const void *Wq, int N, int K, long long ldw, const void *w_scale, long long ldws,
+                                   skinny_type out_type, void *stream, skinny_mxfp4_plan **plan)
+{
+    if (!plan)
+        return bad(SKINNY_ERR_INVALID_ARG, "plan is NULL");
+    *plan = nullptr;
+    if (!Wq || !w_scale || N < 1 || K < 1)
+        return bad(SKINNY_ERR_INVALID_ARG, "Wq or w_scale is NULL, or N=%d, K=%d is not positive", N, K);
+    if (!is_type((int)out_type))
+        return bad(SKINNY_ERR_INVALID_ARG, "output type %d is none of BF16, F32 and F16", (int)out_type);
+    if (N > kMaxRows)
+        return bad(SKINNY_ERR_SHAPE, "N=%d: at most %d", N, kMaxRows);
+    if (K % kBlock || K > kMaxPitch)
+        return bad(SKINNY_ERR_SHAPE, "K=%d must be a multiple of 32, at most 2^22", K);
+    const int blocks = K / kBlock, units = (blocks + kUnitBlocks - 1) / kUnitBlocks;
+    if (ldw < K / 2 || ldws < blocks)
+        return bad(SKINNY_ERR_SHAPE, "ldw=%lld must be at least %d bytes and ldws=%lld %d", ldw, K / 2, ldws, blocks);
+    const long long tiles = ((long long)N + 15) / 16, count = tiles * units * 128;
+    const long long pairs = (tiles + 1) / 2, scales = pairs * units * 64;
+    if (count >= 1LL << 36)
+        return bad(SKINNY_ERR_SHAPE, "N=%d by K=%d is too large", N, K);
+    skinny_mxfp4_plan *p = new (std::nothrow) skinny_mxfp4_plan{N, K, units, out_type, 0, nullptr, nullptr};
+    if (!p)
+        return bad(SKINNY_ERR_NOMEM, "host allocation failed");
+    int cus = 0;
+    const skinny_status st = current_gfx950(&p->device, &cus);
+    if (st != SKINNY_OK) {
+        delete p;
+        return st;
+    }
+    hipError_t e = hipMalloc(&p->w, (size_t)count * 16);
+    if (e == hipSuccess)
+        e = hipMalloc(reinterpret_cast<void **>(&p->w_scale), (size_t)scales * 4);
+    const hipStream_t s = (hipStream_t)stream;
+    int n = N, b = blocks, us = units;
+    if (e == hipSuccess)
+        e = over_launches(count, [&](long long first, dim3 grid) {
+            const unsigned char *src = static_cast<const unsigned char *>(Wq);
+            u32x4 *dst = static_cast<u32x4 *>(p->w);
+            long long ld = ldw, c = count;
+            void *params[] = {&src, &ld, &n, &b, &us, &dst, &first, &c};
+            return hipLaunchKernel(reinterpret_cast<const void *>(lay_out), grid, dim3(256), params, 0, s);
+        });
+    if (e == hipSuccess)
+        e = over_launches(scales, [&](long long first, dim3 grid) {
+            const unsigned char *src = static_cast<const unsigned char *>(w_scale);
+            unsigned *dst = p->w_scale;
+            long long ld = ldws, c = scales;
+            void *params[] = {&src, &ld, &n, &b, &us, &dst, &first, &c};
+            return hipLaunchKernel(reinterpret_cast<const void *>(lay_out_scales), grid, dim3(256), params, 0, s);
+        });
+    if (e == hipSuccess)
+        e = hipStreamSynchronize(s);
+    if (e != hipSuccess) {
+        (void)hipFree(p->w);
+        (void)hipFree(p->w_scale);
+        delete p;
+        return hip_bad(e, "mxfp4 prepare");
+    }
+    *plan = p;
+    return SKINNY_OK;
+}
+
+skinny_status skinny_mxfp4_run(const skinny_mxfp4_plan *p, const void *xq, int bits, long long ldx, const void *x_scale,
+                               long long ldxs, const void *residual, long long ldr, void *out, long long ldo, int M,
+                               void *stream)
+{
+    if (!p)
+        return bad(SKINNY_ERR_INVALID_ARG, "plan is NULL");
+    if (!is_bits(bits))
+        return bad(SKINNY_ERR_INVALID_ARG, "bits=%d is neither 4 nor 8", bits);
+    if (M < 0)
+        return bad(SKINNY_ERR_INVALID_ARG, "M=%d is negative", M);
+    if (M > kMaxRows)
+        return bad(SKINNY_ERR_SHAPE, "M=%d: at most %d", M, kMaxRows);
+    if (M == 0)
+        return SKINNY_OK;
+    if (!xq || !x_scale || !out)
+        return bad(SKINNY_ERR_INVALID_ARG, "xq, x_scale or out is NULL");
+    const int row_bytes = p->K / 8 * bits, blocks = p->K / kBlock;
+    if (ldx < row_bytes || ldx % 16 || ldx > kMaxPitch || ldxs < blocks || ldxs > kMaxPitch)
+        return bad(SKINNY_ERR_SHAPE, "ldx=%lld must be a multiple of 16 bytes from %d to 2^22, ldxs=%lld from %d to 2^22",
+                   ldx, row_bytes, ldxs, blocks);
+    if (ldo < p->N || (residual && ldr < p->N))
+        return bad(SKINNY_ERR_SHAPE, "ldo=%lld and ldr=%lld must be at least N=%d", ldo, ldr, p->N);
+    const int eb = type_bytes((int)p->out);
+    if ((uintptr_t)xq % 16 || (uintptr_t)out % eb || (uintptr_t)residual % eb)
+        return bad(SKINNY_ERR_ALIGN, "xq must be 16-byte aligned, out and residual to their elements");
+    PArgs a{};
+    a.w = static_cast<const u32x4 *>(p->w);
+    a.w_scale = p->w_scale;
+    a.x = static_cast<const unsigned char *>(xq);
+    a.x_scale = static_cast<const unsigned char *>(x_scale);
+    a.res = residual;
+    a.out = out;
+    a.ldx = ldx;
+    a.ldxs = ldxs;
+    a.ldr = ldr;
+    a.ldo = ldo;
+    a.M = M;
+    a.N = p->N;
+    a.x_bytes = row_bytes;
+    a.blocks = blocks;
+    a.units = p->units;
+    a.type = p->out;
+    a.vec = (uintptr_t)out % (4 * eb) == 0 && ldo % 4 == 0 && (uintptr_t)residual % (4 * eb) == 0 && ldr % 4 == 0;
+    const hipError_t e = launch_product(a, bits, (hipStream_t)stream);
+    return e == hipSuccess ? SKINNY_OK : hip_bad(e, "mxfp4 product launch");
+}
+
+void skinny_mxfp4_destroy(skinny_mxfp4_plan *p)
+{
+    if (!p)
+        return;
+    int cur = -1;
+    (void)hipGetDevice(&cur);
+    if (cur != p->device)
+        (void)hipSetDevice(p->device);
+    (void)hipDeviceSynchronize();
+    (void)hipFree(p->w);
+    (void)hipFree(p->w_scale);
+    if (cur != p->device && cur >= 0)
+        (void)hipSetDevice(cur);
+    delete p;
+}
+
+}  // extern "C"
