@@ -275,12 +275,17 @@ __device__ __forceinline__ i32x8 widened(u32x4 v)
     return __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
-// 16 rows of w by 16 tokens over 128 k, both in 4 bits; byte WB of ws is the
-// lanes' powers of w, xs those of x.
-template <int WB>
+template <int V>
+struct Const {
+    static constexpr int value = V;
+};
+
+// 16 rows of w by 16 tokens over 128 k, both in 4 bits; byte WB of ws and XB of
+// xs are the lanes' powers.
+template <int WB, int XB>
 __device__ __forceinline__ f32x4 mma128(u32x4 w, u32x4 x, f32x4 c, unsigned ws, unsigned xs)
 {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widened(w), widened(x), c, 4, 4, WB, (int)ws, 0, (int)xs);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widened(w), widened(x), c, 4, 4, WB, (int)ws, XB, (int)xs);
 }
 
 // Eight values times their power in BF16, which holds a code of either type
@@ -348,11 +353,11 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[RT][MT], const u32x4 (&w)[
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 if (r % 2 == 0) {
-                    acc[r][t] = mma128<0>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
-                    acc[r][t] = mma128<1>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
+                    acc[r][t] = mma128<0, 0>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
+                    acc[r][t] = mma128<1, 0>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
                 } else {
-                    acc[r][t] = mma128<2>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
-                    acc[r][t] = mma128<3>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
+                    acc[r][t] = mma128<2, 0>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
+                    acc[r][t] = mma128<3, 0>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
                 }
             }
     } else {
@@ -517,6 +522,229 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
     }
 }
 
+// s_waitcnt for at most `vm` vector memory and `lgkm` LDS operations under way.
+constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (vm >> 4) << 14 | 0x70 | lgkm << 8; }
+
+// Waits until at most VM of this wave's copies to LDS and LGKM of its LDS reads
+// are under way, then for the workgroup.  Not __syncthreads, which may wait for
+// every copy.
+template <int VM, int LGKM>
+__device__ __forceinline__ void landed()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_for(VM, LGKM));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// 1 KiB, or 64 dwords, from global memory to LDS without passing through
+// registers: lane l's 16 or 4 bytes land at `lds` + 16 l or 4 l.
+typedef __attribute__((address_space(3))) void *lds_ptr;
+
+__device__ __forceinline__ void copy_vectors(__amdgpu_buffer_rsrc_t r, u32x4 *lds, unsigned offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 16, offset, 0, 0, 0);
+}
+
+__device__ __forceinline__ void copy_words(__amdgpu_buffer_rsrc_t r, u32x4 *lds, unsigned offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 4, offset, 0, 0, 0);
+}
+
+// LDS of a stage (a unit of 256 k) of product_tiles, in 16-byte vectors.
+template <int T0, bool WORDS>
+struct TilesLayout {
+    static constexpr int kXCopies = (T0 + 1) / 2;       // a wave's copies of x a stage, 8 rows each
+    static constexpr int kPCopies = !WORDS && T0 > 4 ? 2 : 1;   // of x's powers
+    static constexpr int kW = 0, kX = 32 * 64, kWs = kX + 8 * kXCopies * 64, kXs = kWs + 8 * 16;
+    static constexpr int kVecs = kXs + 8 * kPCopies * 16;
+    static constexpr int kStages = T0 <= 4 ? 3 : 2;
+    static constexpr int kBytes = kStages * kVecs * 16;
+};
+
+// Many 4-bit tokens: 256 weight rows by 32 T0 tokens a workgroup of eight
+// waves, each a quarter of the rows by half of the tokens, 4 x T0 products of 128 k
+// a step and two steps a stage.  All operands are copied to LDS, up to three
+// stages ahead -- w and its powers lie in MFMA order, x goes by lines, its 16-byte
+// chunks in an order without bank conflicts -- and read into registers one step
+// ahead of the products.  WORDS: rows of x's powers are whole aligned dwords, two
+// a row and stage; otherwise the three aligned dwords around them are copied
+// (each holds a byte of the row, so that none lies outside its memory's page).
+template <int T0, bool WORDS>
+__global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
+{
+    using L = TilesLayout<T0, WORDS>;
+    constexpr int kStages = L::kStages, kCopies = 5 + L::kXCopies + L::kPCopies;
+    extern __shared__ u32x4 ring[];             // [kStages][L::kVecs]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const int half = wave >> 2, quarter = wave & 3;
+    // four token tiles by all row tiles at a time: the 32 workgroups of an XCD
+    // then share 8 x 256 rows and 4 token tiles
+    const unsigned id = logical_id();
+    const unsigned per = 4u * (unsigned)a.n_tiles, grp = id / per, in = id - grp * per;
+    const unsigned width = min(4u, (unsigned)a.m_tiles - 4u * grp);
+    const int mt = (int)(4u * grp + in % width), nt = (int)(in / width);
+    const int n0 = nt * 256, m0 = mt * 32 * T0;
+    const int row_tiles = min(16, (a.N - n0 + 15) / 16), rows = min(32 * T0, a.M - m0);
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (long long)nt * 16 * a.units * 128,
+                                                (unsigned)(row_tiles * a.units) * 2048u);
+    const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.w_scale + (long long)nt * 8 * a.units * 64,
+                                                 (unsigned)((row_tiles + 1) / 2 * a.units) * 256u);
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + m0 * a.ldx, (unsigned)((rows - 1) * a.ldx) + (unsigned)a.x_bytes);
+    const unsigned char *xs0 = a.x_scale + m0 * a.ldxs;
+    const unsigned shift = WORDS ? 0u : (unsigned)((uintptr_t)xs0 & 3);
+    const __amdgpu_buffer_rsrc_t xsr =
+        make_rsrc(xs0 - shift, (shift + (unsigned)((rows - 1) * a.ldxs) + (unsigned)a.blocks + 3u) & ~3u);
+    // this wave's copies of a stage: row tiles 2 wave, 2 wave + 1 of w at both
+    // steps and their powers, every eighth 8 rows of x, 16-byte chunk c of row r at
+    // c ^ (r % 8), and the powers of 32 rows (WORDS) or 16
+    unsigned w_off[2], ws_off, x_off[L::kXCopies], xs_off[L::kPCopies], xs_block[L::kPCopies];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        w_off[j] = (unsigned)((2 * wave + j) * a.units) * 2048u + 16u * lane;
+    ws_off = (unsigned)(wave * a.units) * 256u + 4u * lane;
+#pragma unroll
+    for (int j = 0; j < L::kXCopies; ++j) {
+        const int row = 8 * (wave + 8 * j) + (lane >> 3);
+        x_off[j] = row < rows ? (unsigned)(row * a.ldx) + 16u * ((lane & 7) ^ (lane >> 3)) : kSkip;
+    }
+#pragma unroll
+    for (int j = 0; j < L::kPCopies; ++j) {
+        if constexpr (WORDS) {
+            const int row = 32 * wave + (lane >> 1);
+            xs_off[j] = row < rows ? (unsigned)(row * a.ldxs) + 4u * (lane & 1) : kSkip;
+            xs_block[j] = 4u * (lane & 1);
+        } else {
+            const int row = 16 * (wave + 8 * j) + (lane >> 2);
+            const unsigned at = shift + (unsigned)(row * a.ldxs), word = lane & 3;
+            xs_off[j] = row < rows && word < 3 ? (at & ~3u) + 4u * word : kSkip;
+            // the word's first byte that is the row's own
+            xs_block[j] = 4u * word > (at & 3u) ? 4u * word - (at & 3u) : 0u;
+        }
+    }
+    const int stages = a.units;
+    // the same count of copies for every stage, past the last one too: the waits below count them
+    const auto copy = [&](int st, int buf) __attribute__((always_inline)) {
+        u32x4 *base = ring + buf * L::kVecs;
+        const bool in_k = st < stages;
+        const unsigned wo = in_k ? (unsigned)st * 2048u : kSkip, xo = in_k ? (unsigned)st * 128u : kSkip;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            copy_vectors(wr, base + ((j & 1) * 16 + 2 * wave + (j >> 1)) * 64, w_off[j >> 1] + wo + (j & 1) * 1024u);
+        copy_words(wsr, base + L::kWs + wave * 16, ws_off + (in_k ? (unsigned)st * 256u : kSkip));
+#pragma unroll
+        for (int j = 0; j < L::kXCopies; ++j)
+            copy_vectors(xr, base + L::kX + (wave + 8 * j) * 64, x_off[j] + xo);
+#pragma unroll
+        for (int j = 0; j < L::kPCopies; ++j) {
+            const unsigned b = (unsigned)st * kUnitBlocks;
+            copy_words(xsr, base + L::kXs + (wave + 8 * j) * 16,
+                           xs_off[j] + (b + xs_block[j] < (unsigned)a.blocks ? b : kSkip));
+        }
+    };
+    f32x4 acc[4][T0];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
+            acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 wf[2][4], xf[2][T0];
+    unsigned ws[2], xs[T0], ws_next[2], xs_next[T0];
+    // operands of step k of a stage, in registers one step ahead of their products
+    const auto read = [&](int buf, int k) __attribute__((always_inline)) {
+        const u32x4 *base = ring + buf * L::kVecs;
+        const u32x4 *at = base + k * 16 * 64 + lane;
+        const u32x4 *xat = base + L::kX + 2 * T0 * half * 64 + 8 * (lane & 15) + ((2 * g + k) ^ (lane & 7));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            wf[k][i] = at[(4 * quarter + i) * 64];
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
+            xf[k][t] = xat[2 * t * 64];
+    };
+    const auto read_powers = [&](int buf, int st) __attribute__((always_inline)) {
+        const u32x4 *base = ring + buf * L::kVecs;
+        const unsigned *at = reinterpret_cast<const unsigned *>(base + L::kWs) + 2 * quarter * 64 + lane;
+        ws_next[0] = at[0];
+        ws_next[1] = at[64];
+        const int row = 16 * T0 * half + (lane & 15);
+        if constexpr (WORDS) {
+            const unsigned short *p = reinterpret_cast<const unsigned short *>(base + L::kXs) + 4 * row + g;
+#pragma unroll
+            for (int t = 0; t < T0; ++t)
+                xs_next[t] = p[64 * t];
+        } else {
+            const int b = kUnitBlocks * st + 2 * g;
+            // rows 16 apart begin at the same place in a dword
+            const unsigned off = (shift + (unsigned)(row * (int)a.ldxs)) & 3u;
+            const unsigned char *p = reinterpret_cast<const unsigned char *>(base + L::kXs) + 16 * row + off + 2 * g;
+#pragma unroll
+            for (int t = 0; t < T0; ++t)        // past K the bytes are the next row's
+                xs_next[t] =
+                    (b < a.blocks ? (unsigned)p[256 * t] : 0u) | (b + 1 < a.blocks ? (unsigned)p[256 * t + 1] << 8 : 0u);
+        }
+    };
+    const auto take_powers = [&]() __attribute__((always_inline)) {
+        ws[0] = ws_next[0];
+        ws[1] = ws_next[1];
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
+            xs[t] = xs_next[t];
+    };
+    const auto products = [&](auto step) __attribute__((always_inline)) {
+        constexpr int k = decltype(step)::value;
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                acc[i][t] = mma128<k, k>(wf[k][i], xf[k][t], acc[i][t], ws[i / 2], xs[t]);
+                acc[i + 1][t] = mma128<2 + k, k>(wf[k][i + 1], xf[k][t], acc[i + 1][t], ws[i / 2], xs[t]);
+            }
+        // a read after every second product: all at the start, the waves of a SIMD wait for LDS together
+#pragma unroll
+        for (int r = 0; r < 4 + T0; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, k == 1 ? 2 : 1, 0);     // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                  // products
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4 * T0, 0);
+    };
+#pragma unroll
+    for (int st = 0; st < kStages; ++st)
+        copy(st, st);
+    landed<(kStages - 1) * kCopies, 15>();
+    read(0, 0);
+    read_powers(0, 0);
+    take_powers();
+    for (int st = 0, buf = 0; st < stages; ++st) {
+        const int next = buf + 1 < kStages ? buf + 1 : 0;
+        read(buf, 1);
+        products(Const<0>{});
+        __builtin_amdgcn_sched_barrier(0);
+        // this wave's copies of the next stage have landed, and it has read all of this one
+        landed<(kStages - 2) * kCopies, 0>();
+        copy(st + kStages, buf);
+        read(next, 0);                          // after the last stage: what lies in LDS, and is not used
+        read_powers(next, st + 1);
+        products(Const<1>{});
+        __builtin_amdgcn_sched_barrier(0);
+        take_powers();
+        buf = next;
+    }
+    __builtin_amdgcn_s_waitcnt(wait_for(0, 15));        // no copy outlives its workgroup's LDS
+#pragma unroll
+    for (int t = 0; t < T0; ++t) {
+        const int m = m0 + 16 * (T0 * half + t) + (lane & 15);
+        if (m >= a.M)
+            continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 64 * quarter + 16 * i + 4 * g;
+            if (n < a.N)
+                store4(a, m, n, acc[i][t]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -567,11 +795,56 @@ const void *rows_kernel(int rt, int mt)
                                                                : rows_kernel_of<4, BITS, NT>(mt);
 }
 
-// A tile shape and the time of its rounds over 256 CUs.
+// Powers of any alignment take more registers: tiles of up to 32 * kAnyTiles tokens fit.
+constexpr int kAnyTiles = 5;
+
+template <int T0>
+const void *tiles_fn(bool words)
+{
+    if constexpr (T0 > kAnyTiles)
+        return reinterpret_cast<const void *>(product_tiles<T0, true>);
+    return words ? reinterpret_cast<const void *>(product_tiles<T0, true>)
+                 : reinterpret_cast<const void *>(product_tiles<T0, false>);
+}
+
+const void *tiles_kernel(int t0, bool words)
+{
+    return t0 == 1 ? tiles_fn<1>(words) : t0 == 2 ? tiles_fn<2>(words) : t0 == 3 ? tiles_fn<3>(words)
+         : t0 == 4 ? tiles_fn<4>(words) : t0 == 5 ? tiles_fn<5>(words) : t0 == 6 ? tiles_fn<6>(words)
+         : t0 == 7 ? tiles_fn<7>(words) : tiles_fn<8>(words);
+}
+
+template <int T0>
+int tiles_lds_of(bool words)
+{
+    return words ? TilesLayout<T0, true>::kBytes : TilesLayout<T0, false>::kBytes;
+}
+
+int tiles_lds(int t0, bool words)
+{
+    return t0 == 1 ? tiles_lds_of<1>(words) : t0 == 2 ? tiles_lds_of<2>(words) : t0 == 3 ? tiles_lds_of<3>(words)
+         : t0 == 4 ? tiles_lds_of<4>(words) : t0 == 5 ? tiles_lds_of<5>(words) : t0 == 6 ? tiles_lds_of<6>(words)
+         : t0 == 7 ? tiles_lds_of<7>(words) : tiles_lds_of<8>(words);
+}
+
+// A tile shape and the time of its rounds over 256 CUs, in us over K = 7168.
 struct Tiling {
-    int r, t;                   // 16 r rows by 16 t tokens
+    int r, t;                   // 16 r rows by 16 t tokens, or 256 rows by 32 t tokens
     float us;
 };
+
+Tiling tiles_tiling(int M, int N, bool words)
+{
+    static const float round_us[9] = {0.0f, 18.0f, 21.0f, 24.0f, 26.0f, 37.0f, 38.0f, 42.0f, 45.0f};
+    Tiling best{0, 0, 0.0f};
+    for (int t = words ? 8 : kAnyTiles; t >= 1; --t) {
+        const long long count = ((long long)N + 255) / 256 * ((M + 32 * t - 1) / (32 * t));
+        const float us = (float)((count + 255) / 256) * round_us[t];
+        if (!best.r || us < best.us)
+            best = Tiling{16, t, us};
+    }
+    return best;
+}
 
 // A round is as long as the bytes a workgroup loads; of equal ones the most tokens, which read the weight least often.
 Tiling rows_tiling(int M, int N, int bits)
@@ -580,7 +853,7 @@ Tiling rows_tiling(int M, int N, int bits)
     for (int t = min(4, (M + 15) / 16); t >= 1; --t)
         for (int r = 1; r <= 4; r *= 2) {
             const long long count = (long long)((N + 16 * r - 1) / (16 * r)) * ((M + 16 * t - 1) / (16 * t));
-            const float us = (float)((count + 255) / 256) * (float)(r + t * bits / 4);
+            const float us = (float)((count + 255) / 256) * 1.125f * (float)(r + t * bits / 4);
             if (!best.r || us < best.us)
                 best = Tiling{r, t, us};
         }
@@ -592,8 +865,11 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
     constexpr unsigned kThreads = 512;
     constexpr int kSplit = 256;                 // rows and tokens of the largest tile: both halves begin on one
     void *params[] = {&a};
+    const bool words = a.blocks % 4 == 0 && a.ldxs % 4 == 0 && (uintptr_t)a.x_scale % 4 == 0;
     const Tiling rows = rows_tiling(a.M, a.N, bits);
-    const int n_rows = 16 * rows.r, tokens = 16 * rows.t;
+    const Tiling tiles = a.M > 64 && bits == 4 ? tiles_tiling(a.M, a.N, words) : rows;
+    const bool many = tiles.us < rows.us;
+    const int n_rows = many ? 256 : 16 * rows.r, tokens = many ? 32 * tiles.t : 16 * rows.t;
     const long long n_tiles = ((long long)a.N + n_rows - 1) / n_rows, m_tiles = ((long long)a.M + tokens - 1) / tokens;
     if (n_tiles * m_tiles > kMostThreads / kThreads) {
         // more threads than a launch may have: the two halves of the longer side, one after the other
@@ -623,9 +899,20 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
     }
     a.n_tiles = (int)n_tiles;
     a.m_tiles = (int)m_tiles;
-    const void *fn = bits == 4 ? (a.m_tiles == 1 ? rows_kernel<4, true>(rows.r, rows.t) : rows_kernel<4, false>(rows.r, rows.t))
+    const void *fn = many        ? tiles_kernel(tiles.t, words)
+                     : bits == 4 ? (a.m_tiles == 1 ? rows_kernel<4, true>(rows.r, rows.t) : rows_kernel<4, false>(rows.r, rows.t))
                                : (a.m_tiles == 1 ? rows_kernel<8, true>(rows.r, rows.t) : rows_kernel<8, false>(rows.r, rows.t));
-    return hipLaunchKernel(fn, dim3((unsigned)(n_tiles * m_tiles)), dim3(kThreads), params, 0, stream);
+    return hipLaunchKernel(fn, dim3((unsigned)(n_tiles * m_tiles)), dim3(kThreads), params,
+                           many ? (size_t)tiles_lds(tiles.t, words) : 0, stream);
+}
+
+// Dynamic LDS past 64 KiB has to be asked for, on every device that the kernels run on.
+void raise_limits()
+{
+    for (int t0 = 1; t0 <= 8; ++t0)
+        for (const bool words : {true, t0 > kAnyTiles})
+            (void)hipFuncSetAttribute(tiles_kernel(t0, words), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                      tiles_lds(t0, words));
 }
 
 // fn(first vector, launch's end) over count vectors of 256-thread workgroups, in launches of fewer than 2^32 threads.
@@ -788,6 +1075,7 @@ skinny_status skinny_mxfp4_prepare(const void *Wq, int N, int K, long long ldw, 
         delete p;
         return st;
     }
+    raise_limits();
     hipError_t e = hipMalloc(&p->w, (size_t)count * 16);
     if (e == hipSuccess)
         e = hipMalloc(reinterpret_cast<void **>(&p->w_scale), (size_t)scales * 4);
