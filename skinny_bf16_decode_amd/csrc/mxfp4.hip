@@ -174,14 +174,14 @@ struct PArgs {
     int units;                  // of 256 k
     int type;                   // skinny_type of out and res
     int vec;                    // out and res take four columns at once
+    int words;                  // rows of x's powers are whole aligned dwords
     int m_tiles;                // token tiles of the launch
     int n_tiles;                // tiles of weight rows
 };
 
 // Weight rows into MFMA operands: at step s of unit u, lane l of row tile t
-// takes block 8 u + 2 (l / 16) + s of row 16 t + l % 16.  The blocks' order
-// inside a unit is the same for w and x, and such that a unit of a 4-bit row is
-// one line of 128 bytes.  16-byte vectors `first` .. count - 1.
+// takes block 8 u + 4 s + l / 16 of row 16 t + l % 16, so that a wave's load of
+// an operand is 1 KiB in a row.  16-byte vectors `first` .. count - 1.
 __global__ __launch_bounds__(256) void lay_out(const unsigned char *w, long long ldw, int N, int blocks, int units,
                                                u32x4 *out, long long first, long long count)
 {
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(256) void lay_out(const unsigned char *w, long long
     const int lane = (int)(i & 63), s = (int)(i >> 6) & 1;
     const long long tu = i >> 7;
     const long long n = tu / units * 16 + (lane & 15);
-    const int b = (int)(tu % units) * kUnitBlocks + 2 * (lane >> 4) + s;
+    const int b = (int)(tu % units) * kUnitBlocks + 4 * s + (lane >> 4);
     u32x4 v = u32x4{0u, 0u, 0u, 0u};
     if (n < N && b < blocks) {
         const unsigned char *p = w + n * ldw + 16LL * b;
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256) void lay_out_scales(const unsigned char *s, lo
     unsigned v = 0;
     for (int j = 0; j < 4; ++j) {
         const long long n = pu / units * 32 + 16 * (j >> 1) + (lane & 15);
-        const int b = (int)(pu % units) * kUnitBlocks + 2 * (lane >> 4) + (j & 1);
+        const int b = (int)(pu % units) * kUnitBlocks + 4 * (j & 1) + (lane >> 4);
         if (n < N && b < blocks)
             v |= (unsigned)s[n * lds + b] << (8 * j);
     }
@@ -280,12 +280,12 @@ struct Const {
     static constexpr int value = V;
 };
 
-// 16 rows of w by 16 tokens over 128 k, both in 4 bits; byte WB of ws and XB of
-// xs are the lanes' powers.
-template <int WB, int XB>
+// 16 rows of w by 16 tokens over 128 k, both in 4 bits; byte WB of ws and the
+// lowest of xs are the lanes' powers.
+template <int WB>
 __device__ __forceinline__ f32x4 mma128(u32x4 w, u32x4 x, f32x4 c, unsigned ws, unsigned xs)
 {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widened(w), widened(x), c, 4, 4, WB, (int)ws, XB, (int)xs);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widened(w), widened(x), c, 4, 4, WB, (int)ws, 0, (int)xs);
 }
 
 // Eight values times their power in BF16, which holds a code of either type
@@ -311,11 +311,11 @@ __device__ __forceinline__ bf16x8 bf16_of_8(unsigned lo, unsigned hi, float powe
 }
 
 // The 16-byte chunk of a row's unit (8 of them in 4 bits, 16 in 8) that is part
-// `part` of lane group g's operand at step s: block 2 g + s.
+// `part` of lane group g's operand at step s: block 4 s + g.
 template <int BITS>
 __device__ __forceinline__ int chunk_of(int g, int s, int part)
 {
-    return BITS / 4 * (2 * g + s) + part;
+    return BITS / 4 * (4 * s + g) + part;
 }
 
 // A buffer load whose offset is past its resource reads zero and touches no
@@ -353,11 +353,11 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[RT][MT], const u32x4 (&w)[
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 if (r % 2 == 0) {
-                    acc[r][t] = mma128<0, 0>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
-                    acc[r][t] = mma128<1, 0>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
+                    acc[r][t] = mma128<0>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
+                    acc[r][t] = mma128<1>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
                 } else {
-                    acc[r][t] = mma128<2, 0>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
-                    acc[r][t] = mma128<3, 0>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
+                    acc[r][t] = mma128<2>(w[0][r], x[0][t].v[0], acc[r][t], ws[r / 2], xs[0][t]);
+                    acc[r][t] = mma128<3>(w[1][r], x[1][t].v[0], acc[r][t], ws[r / 2], xs[1][t]);
                 }
             }
     } else {
@@ -369,7 +369,7 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[RT][MT], const u32x4 (&w)[
                 wp[r] = power_of(ws[r / 2] >> (16 * (r % 2) + 8 * k) & 0xFFu);
 #pragma unroll
             for (int t = 0; t < MT; ++t)
-                xp[t] = power_of(xs[k][t]);
+                xp[t] = power_of(xs[k][t] & 0xFFu);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 bf16x8 wv[RT], xv[MT];
@@ -394,13 +394,13 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[RT][MT], const u32x4 (&w)[
 // end through LDS in a fixed order.  Loads go into registers, D units ahead.  x
 // is read in whole lines and passes through the wave's own LDS on its way into
 // operands, a token tile at a time.
-template <int RT, int MT, int BITS, int D, bool NT>
+template <int RT, int MT, int BITS, int D, int XR, bool NT>
 __global__ __launch_bounds__(512) void product_rows(PArgs a)
 {
     constexpr int kWaves = 8, kV = RT * MT;
     constexpr int kLine = 32 * BITS;                    // bytes of a row's unit
     constexpr int kPerRow = kLine / 16, kRows = 64 / kPerRow;   // vectors of a row's unit, rows of a load
-    constexpr int kLoads = 16 / kRows;                  // loads of a token tile's unit
+    constexpr int kLoads = (XR + kRows - 1) / kRows;    // loads of a token tile's unit
     constexpr int kTile = 16 * kPerRow;                 // vectors of a token tile's unit
     constexpr int kS = (RT + 1) / 2;
     __shared__ u32x4 shared[kWaves * kTile > 256 * kV ? kWaves * kTile : 256 * kV];
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int row = 16 * t + (lane & 15);
-        xs_off[t] = row < rows ? (unsigned)(row * a.ldxs) + 2u * g : kSkip;
+        xs_off[t] = row < rows ? (unsigned)(row * a.ldxs) + (a.words ? 0u : (unsigned)g) : kSkip;
     }
     f32x4 acc[RT][MT];
 #pragma unroll
@@ -440,10 +440,13 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
             acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     u32x4 wf[D][2][RT], xf[D][MT * kLoads];
     unsigned ws[D][kS], xs[D][2][MT];
-    // past K neither codes nor powers of x may be read, which are other rows' and may stand for NaN
+    // Past K neither codes nor powers of x may be read, which are other rows' and
+    // may stand for NaN.  Units past the last are not loaded, which a load of
+    // nothing would pay for like any other.
     const auto load = [&](int d, int u) {
-        const bool in = u < a.units;
-        const unsigned wo = in ? (unsigned)u * 2048u : kSkip;
+        if (u >= a.units)
+            return;
+        const unsigned wo = (unsigned)u * 2048u;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -451,23 +454,33 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
                 wf[d][k][r] = __builtin_amdgcn_raw_buffer_load_b128(wr, w_off[r] + wo + 1024u * k, 0, NT ? 2 : 0);
 #pragma unroll
         for (int r = 0; r < kS; ++r) {
-            const unsigned at = (unsigned)(r * a.units) * 256u + 4u * lane + (in ? (unsigned)u * 256u : kSkip);
+            const unsigned at = (unsigned)(r * a.units) * 256u + 4u * lane + (unsigned)u * 256u;
             if constexpr (RT == 1)
                 ws[d][r] = __builtin_amdgcn_raw_buffer_load_b16(wsr, at + 2u * (block & 1), 0, NT ? 2 : 0);
             else
                 ws[d][r] = __builtin_amdgcn_raw_buffer_load_b32(wsr, at, 0, NT ? 2 : 0);
         }
-        const unsigned xo = in && u * kLine + 16 * slot < a.x_bytes ? (unsigned)u * kLine : kSkip;
+        const unsigned xo = u * kLine + 16 * slot < a.x_bytes ? (unsigned)u * kLine : kSkip;
 #pragma unroll
         for (int t = 0; t < MT * kLoads; ++t)
             xf[d][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_off[t] + xo, 0, 0);
+        const unsigned so = (unsigned)(kUnitBlocks * u);
+        if (a.words) {
+            const bool both = kUnitBlocks * u + 4 < a.blocks;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int b = kUnitBlocks * u + 2 * g + k;
-            const unsigned so = in && b < a.blocks ? (unsigned)(kUnitBlocks * u) + k : kSkip;
+            for (int t = 0; t < MT; ++t) {
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(xsr, xs_off[t] + so, 0, 0);
+                xs[d][0][t] = v[0];
+                xs[d][1][t] = both ? v[1] : 0u;
+            }
+        } else {
+            const int b = kUnitBlocks * u + g;
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                xs[d][k][t] = __builtin_amdgcn_raw_buffer_load_b8(xsr, xs_off[t] + so, 0, 0);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    xs[d][k][t] = __builtin_amdgcn_raw_buffer_load_b8(
+                        xsr, xs_off[t] + (b + 4 * k < a.blocks ? so + 4u * k : kSkip), 0, 0);
         }
     };
     // 16-byte chunk c of row r lies at c ^ (r % 8): written a row at a time and
@@ -479,7 +492,15 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
     for (int u = wave; u < a.units; u += kWaves * D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
+            if (u + kWaves * d >= a.units)
+                break;
             XOp<BITS> x[2][MT];
+            unsigned xp[2][MT];                 // the lanes' own bytes
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    xp[k][t] = a.words ? xs[d][k][t] >> (8 * g) : xs[d][k][t];
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
 #pragma unroll
@@ -495,7 +516,7 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
                         x[k][t].v[p] = mine[(lane & 15) * kPerRow + (chunk_of<BITS>(g, k, p) ^ (lane & 7))];
                 __builtin_amdgcn_wave_barrier();
             }
-            multiply<RT, MT, BITS>(acc, wf[d], x, ws[d], xs[d]);
+            multiply<RT, MT, BITS>(acc, wf[d], x, ws[d], xp);
             load(d, u + kWaves * (d + D));
         }
     }
@@ -551,31 +572,33 @@ __device__ __forceinline__ void copy_words(__amdgpu_buffer_rsrc_t r, u32x4 *lds,
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 4, offset, 0, 0, 0);
 }
 
-// LDS of a stage (a unit of 256 k) of product_tiles, in 16-byte vectors.
-template <int T0, bool WORDS>
+// LDS of product_tiles, in 16-byte vectors: stages of a step (128 k) of w and x,
+// and rings of units (256 k) of powers.
+template <int T0>
 struct TilesLayout {
-    static constexpr int kXCopies = (T0 + 1) / 2;       // a wave's copies of x a stage, 8 rows each
-    static constexpr int kPCopies = !WORDS && T0 > 4 ? 2 : 1;   // of x's powers
-    static constexpr int kW = 0, kX = 32 * 64, kWs = kX + 8 * kXCopies * 64, kXs = kWs + 8 * 16;
-    static constexpr int kVecs = kXs + 8 * kPCopies * 16;
-    static constexpr int kStages = T0 <= 4 ? 3 : 2;
-    static constexpr int kBytes = kStages * kVecs * 16;
+    static constexpr int kXCopies = (T0 + 3) / 4;       // a wave's copies of x a step, 16 rows each
+    static constexpr int kX = 16 * 64, kVecs = kX + 8 * kXCopies * 64;
+    static constexpr int kStages = T0 <= 4 ? 5 : 4;
+    static constexpr int kUnits = kStages / 2 + 1 + kStages % 2;    // of powers: read and under way
+    static constexpr int kUnitVecs = 2 * 8 * 16;        // of w, then of x
+    static constexpr int kPowers = kStages * kVecs;
+    static constexpr int kBytes = (kPowers + kUnits * kUnitVecs) * 16;
 };
 
 // Many 4-bit tokens: 256 weight rows by 32 T0 tokens a workgroup of eight
 // waves, each a quarter of the rows by half of the tokens, 4 x T0 products of 128 k
-// a step and two steps a stage.  All operands are copied to LDS, up to three
-// stages ahead -- w and its powers lie in MFMA order, x goes by lines, its 16-byte
-// chunks in an order without bank conflicts -- and read into registers one step
-// ahead of the products.  WORDS: rows of x's powers are whole aligned dwords, two
-// a row and stage; otherwise the three aligned dwords around them are copied
-// (each holds a byte of the row, so that none lies outside its memory's page).
+// a step.  All operands are copied to LDS, three or four steps ahead -- w and its
+// powers lie in MFMA order, x goes by 64 bytes of a row, its 16-byte chunks in an
+// order without bank conflicts -- and read into registers one step ahead of the
+// products.  WORDS: rows of x's powers are whole aligned dwords, two a row and
+// unit; otherwise the three aligned dwords around them are copied (each holds a
+// byte of the row, so that none lies outside its memory's page).
 template <int T0, bool WORDS>
 __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 {
-    using L = TilesLayout<T0, WORDS>;
-    constexpr int kStages = L::kStages, kCopies = 5 + L::kXCopies + L::kPCopies;
-    extern __shared__ u32x4 ring[];             // [kStages][L::kVecs]
+    using L = TilesLayout<T0>;
+    constexpr int kStages = L::kStages, kCopies = 3 + L::kXCopies;
+    extern __shared__ u32x4 ring[];             // [kStages][L::kVecs], [L::kUnits][L::kUnitVecs]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const int half = wave >> 2, quarter = wave & 3;
     // four token tiles by all row tiles at a time: the 32 workgroups of an XCD
@@ -595,52 +618,51 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
     const unsigned shift = WORDS ? 0u : (unsigned)((uintptr_t)xs0 & 3);
     const __amdgpu_buffer_rsrc_t xsr =
         make_rsrc(xs0 - shift, (shift + (unsigned)((rows - 1) * a.ldxs) + (unsigned)a.blocks + 3u) & ~3u);
-    // this wave's copies of a stage: row tiles 2 wave, 2 wave + 1 of w at both
-    // steps and their powers, every eighth 8 rows of x, 16-byte chunk c of row r at
-    // c ^ (r % 8), and the powers of 32 rows (WORDS) or 16
-    unsigned w_off[2], ws_off, x_off[L::kXCopies], xs_off[L::kPCopies], xs_block[L::kPCopies];
+    // this wave's copies of a step: row tiles 2 wave, 2 wave + 1 of w, every eighth
+    // 16 rows of x, 16-byte chunk c of row r at c ^ (r / 2 % 4); of a unit: the powers
+    // of those row tiles and of 32 (WORDS) or 16 rows of x
+    unsigned w_off[2], ws_off, x_off[L::kXCopies], xs_off, xs_block;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
         w_off[j] = (unsigned)((2 * wave + j) * a.units) * 2048u + 16u * lane;
     ws_off = (unsigned)(wave * a.units) * 256u + 4u * lane;
 #pragma unroll
     for (int j = 0; j < L::kXCopies; ++j) {
-        const int row = 8 * (wave + 8 * j) + (lane >> 3);
-        x_off[j] = row < rows ? (unsigned)(row * a.ldx) + 16u * ((lane & 7) ^ (lane >> 3)) : kSkip;
+        const int row = 16 * (wave + 8 * j) + (lane >> 2);
+        x_off[j] = row < rows ? (unsigned)(row * a.ldx) + 16u * ((lane & 3) ^ (lane >> 3 & 3)) : kSkip;
     }
-#pragma unroll
-    for (int j = 0; j < L::kPCopies; ++j) {
-        if constexpr (WORDS) {
-            const int row = 32 * wave + (lane >> 1);
-            xs_off[j] = row < rows ? (unsigned)(row * a.ldxs) + 4u * (lane & 1) : kSkip;
-            xs_block[j] = 4u * (lane & 1);
-        } else {
-            const int row = 16 * (wave + 8 * j) + (lane >> 2);
-            const unsigned at = shift + (unsigned)(row * a.ldxs), word = lane & 3;
-            xs_off[j] = row < rows && word < 3 ? (at & ~3u) + 4u * word : kSkip;
-            // the word's first byte that is the row's own
-            xs_block[j] = 4u * word > (at & 3u) ? 4u * word - (at & 3u) : 0u;
-        }
+    if constexpr (WORDS) {
+        const int row = 32 * wave + (lane >> 1);
+        xs_block = 4u * (lane & 1);
+        xs_off = row < rows ? (unsigned)(row * a.ldxs) + xs_block : kSkip;
+    } else {
+        const int row = 16 * wave + (lane >> 2);
+        const unsigned at = shift + (unsigned)(row * a.ldxs), word = lane & 3;
+        xs_off = row < rows && word < 3 ? (at & ~3u) + 4u * word : kSkip;
+        // the word's first byte that is the row's own
+        xs_block = 4u * word > (at & 3u) ? 4u * word - (at & 3u) : 0u;
     }
-    const int stages = a.units;
-    // the same count of copies for every stage, past the last one too: the waits below count them
-    const auto copy = [&](int st, int buf) __attribute__((always_inline)) {
+    const int steps = 2 * a.units;
+    // Copy c of the kCopies of step st: w, x, then a unit's powers (of w with even
+    // steps, of x with odd ones).  The same count for every step, past the last one
+    // too: the waits below count them.
+    const auto copy_xs = [&](int unit, int place) __attribute__((always_inline)) {
+        const unsigned b = (unsigned)unit * kUnitBlocks;
+        copy_words(xsr, ring + L::kPowers + place * L::kUnitVecs + 128 + wave * 16,
+                   xs_off + (b + xs_block < (unsigned)a.blocks ? b : kSkip));
+    };
+    const auto copy = [&](int c, int st, int buf, int place) __attribute__((always_inline)) {
         u32x4 *base = ring + buf * L::kVecs;
-        const bool in_k = st < stages;
-        const unsigned wo = in_k ? (unsigned)st * 2048u : kSkip, xo = in_k ? (unsigned)st * 128u : kSkip;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            copy_vectors(wr, base + ((j & 1) * 16 + 2 * wave + (j >> 1)) * 64, w_off[j >> 1] + wo + (j & 1) * 1024u);
-        copy_words(wsr, base + L::kWs + wave * 16, ws_off + (in_k ? (unsigned)st * 256u : kSkip));
-#pragma unroll
-        for (int j = 0; j < L::kXCopies; ++j)
-            copy_vectors(xr, base + L::kX + (wave + 8 * j) * 64, x_off[j] + xo);
-#pragma unroll
-        for (int j = 0; j < L::kPCopies; ++j) {
-            const unsigned b = (unsigned)st * kUnitBlocks;
-            copy_words(xsr, base + L::kXs + (wave + 8 * j) * 16,
-                           xs_off[j] + (b + xs_block[j] < (unsigned)a.blocks ? b : kSkip));
-        }
+        if (c < 2)
+            copy_vectors(wr, base + (2 * wave + c) * 64, w_off[c] + (st < steps ? (unsigned)st * 1024u : kSkip));
+        else if (c < 2 + L::kXCopies)
+            copy_vectors(xr, base + L::kX + (wave + 8 * (c - 2)) * 64,
+                         x_off[c < 2 ? 0 : c - 2 < L::kXCopies ? c - 2 : 0] + (st < steps ? (unsigned)st * 64u : kSkip));
+        else if (st % 2 == 0)
+            copy_words(wsr, ring + L::kPowers + place * L::kUnitVecs + wave * 16,
+                       ws_off + (st < steps ? (unsigned)st * 128u : kSkip));
+        else
+            copy_xs(st / 2 + 1, place);
     };
     f32x4 acc[4][T0];
 #pragma unroll
@@ -649,86 +671,82 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
         for (int t = 0; t < T0; ++t)
             acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     u32x4 wf[2][4], xf[2][T0];
-    unsigned ws[2], xs[T0], ws_next[2], xs_next[T0];
-    // operands of step k of a stage, in registers one step ahead of their products
-    const auto read = [&](int buf, int k) __attribute__((always_inline)) {
+    unsigned ws[2], ws_next[2], xs[2][T0];
+    // Part t of the operands of a step, k its parity, in registers one step ahead of their products.
+    const auto read = [&](int t, int buf, int k, int unit, int place) __attribute__((always_inline)) {
         const u32x4 *base = ring + buf * L::kVecs;
-        const u32x4 *at = base + k * 16 * 64 + lane;
-        const u32x4 *xat = base + L::kX + 2 * T0 * half * 64 + 8 * (lane & 15) + ((2 * g + k) ^ (lane & 7));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            wf[k][i] = at[(4 * quarter + i) * 64];
-#pragma unroll
-        for (int t = 0; t < T0; ++t)
-            xf[k][t] = xat[2 * t * 64];
-    };
-    const auto read_powers = [&](int buf, int st) __attribute__((always_inline)) {
-        const u32x4 *base = ring + buf * L::kVecs;
-        const unsigned *at = reinterpret_cast<const unsigned *>(base + L::kWs) + 2 * quarter * 64 + lane;
-        ws_next[0] = at[0];
-        ws_next[1] = at[64];
-        const int row = 16 * T0 * half + (lane & 15);
-        if constexpr (WORDS) {
-            const unsigned short *p = reinterpret_cast<const unsigned short *>(base + L::kXs) + 4 * row + g;
-#pragma unroll
-            for (int t = 0; t < T0; ++t)
-                xs_next[t] = p[64 * t];
-        } else {
-            const int b = kUnitBlocks * st + 2 * g;
-            // rows 16 apart begin at the same place in a dword
-            const unsigned off = (shift + (unsigned)(row * (int)a.ldxs)) & 3u;
-            const unsigned char *p = reinterpret_cast<const unsigned char *>(base + L::kXs) + 16 * row + off + 2 * g;
-#pragma unroll
-            for (int t = 0; t < T0; ++t)        // past K the bytes are the next row's
-                xs_next[t] =
-                    (b < a.blocks ? (unsigned)p[256 * t] : 0u) | (b + 1 < a.blocks ? (unsigned)p[256 * t + 1] << 8 : 0u);
+        const u32x4 *at = base + lane;
+        const u32x4 *xat = base + L::kX + T0 * half * 64 + 4 * (lane & 15) + (g ^ (lane >> 1 & 3));
+        const u32x4 *powers = ring + L::kPowers + place * L::kUnitVecs;
+        if (k == 0 && t == 0) {
+            const unsigned *wp = reinterpret_cast<const unsigned *>(powers) + 2 * quarter * 64 + lane;
+            ws_next[0] = wp[0];
+            ws_next[1] = wp[64];
         }
-    };
-    const auto take_powers = [&]() __attribute__((always_inline)) {
-        ws[0] = ws_next[0];
-        ws[1] = ws_next[1];
+        xf[k][t] = xat[t * 64];
 #pragma unroll
-        for (int t = 0; t < T0; ++t)
-            xs[t] = xs_next[t];
+        for (int i = t; i < 4; i += T0)
+            wf[k][i] = at[(4 * quarter + i) * 64];
+        const int row = 16 * T0 * half + (lane & 15);
+        // rows 16 apart begin at the same place in a dword
+        const unsigned off = WORDS ? 0u : (shift + (unsigned)(row * (int)a.ldxs)) & 3u;
+        const unsigned char *xp = reinterpret_cast<const unsigned char *>(powers + 128) + (WORDS ? 8 : 16) * row + off +
+                                  4 * k + g;
+        const bool own = WORDS || kUnitBlocks * unit + 4 * k + g < a.blocks;    // else the next row's byte
+        xs[k][t] = own ? (unsigned)xp[(WORDS ? 128 : 256) * t] : 0u;
     };
-    const auto products = [&](auto step) __attribute__((always_inline)) {
-        constexpr int k = decltype(step)::value;
+    // A step's products, k its parity, with the copies of step `st` and the reads of
+    // the next step between them: all at the start, the waves of a SIMD wait for the
+    // memory path and LDS together.
+    const auto run = [&](auto parity, int st, int buf, int st_place, int next, int unit, int place)
+                         __attribute__((always_inline)) {
+        constexpr int k = decltype(parity)::value;
 #pragma unroll
-        for (int t = 0; t < T0; ++t)
+        for (int t = 0; t < T0; ++t) {
+#pragma unroll
+            for (int c = t; c < kCopies; c += T0)
+                copy(c, st, buf, st_place);
+            read(t, next, 1 - k, unit, place);
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-                acc[i][t] = mma128<k, k>(wf[k][i], xf[k][t], acc[i][t], ws[i / 2], xs[t]);
-                acc[i + 1][t] = mma128<2 + k, k>(wf[k][i + 1], xf[k][t], acc[i + 1][t], ws[i / 2], xs[t]);
+                acc[i][t] = mma128<k>(wf[k][i], xf[k][t], acc[i][t], ws[i / 2], xs[k][t]);
+                acc[i + 1][t] = mma128<2 + k>(wf[k][i + 1], xf[k][t], acc[i + 1][t], ws[i / 2], xs[k][t]);
             }
-        // a read after every second product: all at the start, the waves of a SIMD wait for LDS together
-#pragma unroll
-        for (int r = 0; r < 4 + T0; ++r) {
-            __builtin_amdgcn_sched_group_barrier(0x100, k == 1 ? 2 : 1, 0);     // LDS reads
-            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                  // products
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4 * T0, 0);
     };
+    // step st takes buffer st % kStages, unit u place u % kUnits
+    copy_xs(0, 0);
 #pragma unroll
     for (int st = 0; st < kStages; ++st)
-        copy(st, st);
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+            copy(c, st, st, (st + 1) / 2 % L::kUnits);
     landed<(kStages - 1) * kCopies, 15>();
-    read(0, 0);
-    read_powers(0, 0);
-    take_powers();
-    for (int st = 0, buf = 0; st < stages; ++st) {
-        const int next = buf + 1 < kStages ? buf + 1 : 0;
-        read(buf, 1);
-        products(Const<0>{});
-        __builtin_amdgcn_sched_barrier(0);
-        // this wave's copies of the next stage have landed, and it has read all of this one
+#pragma unroll
+    for (int t = 0; t < T0; ++t)
+        read(t, 0, 0, 0, 0);
+    ws[0] = ws_next[0];
+    ws[1] = ws_next[1];
+    int buf = 0, place = 0;                     // of step st and of its unit
+    int ahead = (kStages + 1) / 2 % L::kUnits;  // of the unit whose powers go with step st + kStages
+    for (int st = 0; st < steps; st += 2) {
+        const int unit = st / 2, next_place = place + 1 < L::kUnits ? place + 1 : 0;
+        const int next_ahead = ahead + 1 < L::kUnits ? ahead + 1 : 0;
+        int next = buf + 1 < kStages ? buf + 1 : 0;
+        // this wave's copies of the next step have landed, and it has read all of this one
         landed<(kStages - 2) * kCopies, 0>();
-        copy(st + kStages, buf);
-        read(next, 0);                          // after the last stage: what lies in LDS, and is not used
-        read_powers(next, st + 1);
-        products(Const<1>{});
-        __builtin_amdgcn_sched_barrier(0);
-        take_powers();
+        run(Const<0>{}, st + kStages, buf, ahead, next, unit, place);
         buf = next;
+        next = buf + 1 < kStages ? buf + 1 : 0;
+        landed<(kStages - 2) * kCopies, 0>();
+        // the reads after the last step: what lies in LDS, and is not used
+        run(Const<1>{}, st + 1 + kStages, buf, kStages % 2 ? ahead : next_ahead, next, unit + 1, next_place);
+        buf = next;
+        place = next_place;
+        ahead = next_ahead;
+        ws[0] = ws_next[0];
+        ws[1] = ws_next[1];
     }
     __builtin_amdgcn_s_waitcnt(wait_for(0, 15));        // no copy outlives its workgroup's LDS
 #pragma unroll
@@ -775,36 +793,43 @@ const void *quantize_kernel_of(int type, bool gate, bool vec, bool many)
                                      : quantize_kernel<SKINNY_TYPE_BF16, BITS>(gate, vec, many);
 }
 
-template <int RT, int MT, int BITS, bool NT>
+// Two units ahead for up to four 8-bit tokens, whose loads and registers are
+// few (6288 x 7168: 6.8 against 7.2 us); one elsewhere.
+template <int RT, int MT, int BITS, int XR, bool NT>
 const void *rows_fn()
 {
-    return reinterpret_cast<const void *>(product_rows<RT, MT, BITS, 1, NT>);
+    return reinterpret_cast<const void *>(product_rows<RT, MT, BITS, BITS == 8 && XR == 4 && RT <= 2 ? 2 : 1, XR, NT>);
 }
 
 template <int RT, int BITS, bool NT>
-const void *rows_kernel_of(int mt)
+const void *rows_kernel_of(int mt, int tokens)
 {
-    return mt == 1 ? rows_fn<RT, 1, BITS, NT>() : mt == 2 ? rows_fn<RT, 2, BITS, NT>()
-         : mt == 3 ? rows_fn<RT, 3, BITS, NT>() : rows_fn<RT, 4, BITS, NT>();
+    if constexpr (RT > 1)
+        if (mt == 2)
+            return rows_fn<RT, 2, BITS, 16, NT>();
+    return tokens <= 4   ? rows_fn<RT, 1, BITS, 4, NT>()
+           : tokens <= 8 ? rows_fn<RT, 1, BITS, 8, NT>()
+                         : rows_fn<RT, 1, BITS, 16, NT>();
 }
 
 template <int BITS, bool NT>
-const void *rows_kernel(int rt, int mt)
+const void *rows_kernel(int rt, int mt, int tokens)
 {
-    return rt == 1 ? rows_kernel_of<1, BITS, NT>(mt) : rt == 2 ? rows_kernel_of<2, BITS, NT>(mt)
-                                                               : rows_kernel_of<4, BITS, NT>(mt);
+    return rt == 1 ? rows_kernel_of<1, BITS, NT>(mt, tokens) : rt == 2 ? rows_kernel_of<2, BITS, NT>(mt, tokens)
+                                                                       : rows_kernel_of<4, BITS, NT>(mt, tokens);
 }
 
 // Powers of any alignment take more registers: tiles of up to 32 * kAnyTiles tokens fit.
-constexpr int kAnyTiles = 5;
+constexpr int kAnyTiles = 4;
 
 template <int T0>
 const void *tiles_fn(bool words)
 {
     if constexpr (T0 > kAnyTiles)
         return reinterpret_cast<const void *>(product_tiles<T0, true>);
-    return words ? reinterpret_cast<const void *>(product_tiles<T0, true>)
-                 : reinterpret_cast<const void *>(product_tiles<T0, false>);
+    else
+        return words ? reinterpret_cast<const void *>(product_tiles<T0, true>)
+                     : reinterpret_cast<const void *>(product_tiles<T0, false>);
 }
 
 const void *tiles_kernel(int t0, bool words)
@@ -814,17 +839,11 @@ const void *tiles_kernel(int t0, bool words)
          : t0 == 7 ? tiles_fn<7>(words) : tiles_fn<8>(words);
 }
 
-template <int T0>
-int tiles_lds_of(bool words)
+int tiles_lds(int t0)
 {
-    return words ? TilesLayout<T0, true>::kBytes : TilesLayout<T0, false>::kBytes;
-}
-
-int tiles_lds(int t0, bool words)
-{
-    return t0 == 1 ? tiles_lds_of<1>(words) : t0 == 2 ? tiles_lds_of<2>(words) : t0 == 3 ? tiles_lds_of<3>(words)
-         : t0 == 4 ? tiles_lds_of<4>(words) : t0 == 5 ? tiles_lds_of<5>(words) : t0 == 6 ? tiles_lds_of<6>(words)
-         : t0 == 7 ? tiles_lds_of<7>(words) : tiles_lds_of<8>(words);
+    return t0 == 1 ? TilesLayout<1>::kBytes : t0 == 2 ? TilesLayout<2>::kBytes : t0 == 3 ? TilesLayout<3>::kBytes
+         : t0 == 4 ? TilesLayout<4>::kBytes : t0 == 5 ? TilesLayout<5>::kBytes : t0 == 6 ? TilesLayout<6>::kBytes
+         : t0 == 7 ? TilesLayout<7>::kBytes : TilesLayout<8>::kBytes;
 }
 
 // A tile shape and the time of its rounds over 256 CUs, in us over K = 7168.
@@ -846,17 +865,25 @@ Tiling tiles_tiling(int M, int N, bool words)
     return best;
 }
 
-// A round is as long as the bytes a workgroup loads; of equal ones the most tokens, which read the weight least often.
+// product_rows: what each further workgroup of a CU adds, measured at K = 7168
+// over 1024 to 14336 rows and 1 to 128 tokens (both grow with K alike).  16 x 32
+// tiles and those of 48 and 64 tokens were never the fastest (64 x 6288 x 7168:
+// 64 rows by 32 tokens 8.8 us, by 64 14.8).
 Tiling rows_tiling(int M, int N, int bits)
 {
+    static const struct {
+        int r, t;
+        float us4, us8;
+    } kTiles[] = {{1, 1, 1.65f, 2.45f}, {2, 1, 2.05f, 3.2f}, {4, 1, 3.2f, 5.2f}, {2, 2, 3.05f, 5.3f}, {4, 2, 5.45f, 9.7f}};
     Tiling best{0, 0, 0.0f};
-    for (int t = min(4, (M + 15) / 16); t >= 1; --t)
-        for (int r = 1; r <= 4; r *= 2) {
-            const long long count = (long long)((N + 16 * r - 1) / (16 * r)) * ((M + 16 * t - 1) / (16 * t));
-            const float us = (float)((count + 255) / 256) * 1.125f * (float)(r + t * bits / 4);
-            if (!best.r || us < best.us)
-                best = Tiling{r, t, us};
-        }
+    for (const auto &k : kTiles) {
+        if (k.t == 2 && M <= 16)
+            continue;
+        const long long count = ((long long)N + 16 * k.r - 1) / (16 * k.r) * ((M + 16 * k.t - 1) / (16 * k.t));
+        const float us = (float)((count + 255) / 256) * (bits == 4 ? k.us4 : k.us8);
+        if (!best.r || us < best.us)
+            best = Tiling{k.r, k.t, us};
+    }
     return best;
 }
 
@@ -865,7 +892,7 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
     constexpr unsigned kThreads = 512;
     constexpr int kSplit = 256;                 // rows and tokens of the largest tile: both halves begin on one
     void *params[] = {&a};
-    const bool words = a.blocks % 4 == 0 && a.ldxs % 4 == 0 && (uintptr_t)a.x_scale % 4 == 0;
+    const bool words = a.words != 0;
     const Tiling rows = rows_tiling(a.M, a.N, bits);
     const Tiling tiles = a.M > 64 && bits == 4 ? tiles_tiling(a.M, a.N, words) : rows;
     const bool many = tiles.us < rows.us;
@@ -900,10 +927,10 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
     a.n_tiles = (int)n_tiles;
     a.m_tiles = (int)m_tiles;
     const void *fn = many        ? tiles_kernel(tiles.t, words)
-                     : bits == 4 ? (a.m_tiles == 1 ? rows_kernel<4, true>(rows.r, rows.t) : rows_kernel<4, false>(rows.r, rows.t))
-                               : (a.m_tiles == 1 ? rows_kernel<8, true>(rows.r, rows.t) : rows_kernel<8, false>(rows.r, rows.t));
+                     : bits == 4 ? (a.m_tiles == 1 ? rows_kernel<4, true>(rows.r, rows.t, a.M) : rows_kernel<4, false>(rows.r, rows.t, a.M))
+                               : (a.m_tiles == 1 ? rows_kernel<8, true>(rows.r, rows.t, a.M) : rows_kernel<8, false>(rows.r, rows.t, a.M));
     return hipLaunchKernel(fn, dim3((unsigned)(n_tiles * m_tiles)), dim3(kThreads), params,
-                           many ? (size_t)tiles_lds(tiles.t, words) : 0, stream);
+                           many ? (size_t)tiles_lds(tiles.t) : 0, stream);
 }
 
 // Dynamic LDS past 64 KiB has to be asked for, on every device that the kernels run on.
@@ -912,7 +939,7 @@ void raise_limits()
     for (int t0 = 1; t0 <= 8; ++t0)
         for (const bool words : {true, t0 > kAnyTiles})
             (void)hipFuncSetAttribute(tiles_kernel(t0, words), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                      tiles_lds(t0, words));
+                                      tiles_lds(t0));
 }
 
 // fn(first vector, launch's end) over count vectors of 256-thread workgroups, in launches of fewer than 2^32 threads.
@@ -1151,6 +1178,7 @@ skinny_status skinny_mxfp4_run(const skinny_mxfp4_plan *p, const void *xq, int b
     a.blocks = blocks;
     a.units = p->units;
     a.type = p->out;
+    a.words = blocks % 4 == 0 && ldxs % 4 == 0 && (uintptr_t)x_scale % 4 == 0;
     a.vec = (uintptr_t)out % (4 * eb) == 0 && ldo % 4 == 0 && (uintptr_t)residual % (4 * eb) == 0 && ldr % 4 == 0;
     const hipError_t e = launch_product(a, bits, (hipStream_t)stream);
     return e == hipSuccess ? SKINNY_OK : hip_bad(e, "mxfp4 product launch");
