@@ -763,6 +763,188 @@ __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
     }
 }
 
+// LDS of product_tiles8, in 16-byte vectors, as TilesLayout.
+template <int T0>
+struct Tiles8Layout {
+    static constexpr int kXCopies = (T0 + 1) / 2;       // a wave's copies of x a step, 8 rows each
+    static constexpr int kX = 16 * 64, kVecs = kX + 8 * kXCopies * 64;
+    static constexpr int kStages = T0 <= 4 ? 4 : 3;
+    static constexpr int kUnits = kStages / 2 + 1 + kStages % 2;
+    static constexpr int kUnitVecs = 2 * 8 * 16;
+    static constexpr int kPowers = kStages * kVecs;
+    static constexpr int kBytes = (kPowers + kUnits * kUnitVecs) * 16;
+};
+
+// Many 8-bit tokens: product_tiles' workgroup, with both operands converted to
+// BF16 on their way from LDS to the matrix units (see multiply): a wave's w once for
+// its 16 T0 tokens, x once for its 64 rows.
+template <int T0, bool WORDS>
+__global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
+{
+    using L = Tiles8Layout<T0>;
+    constexpr int kStages = L::kStages, kCopies = 3 + L::kXCopies;
+    extern __shared__ u32x4 ring[];             // [kStages][L::kVecs], [L::kUnits][L::kUnitVecs]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const int half = wave >> 2, quarter = wave & 3;
+    const unsigned id = logical_id();
+    const unsigned per = 4u * (unsigned)a.n_tiles, grp = id / per, in = id - grp * per;
+    const unsigned width = min(4u, (unsigned)a.m_tiles - 4u * grp);
+    const int mt = (int)(4u * grp + in % width), nt = (int)(in / width);
+    const int n0 = nt * 256, m0 = mt * 32 * T0;
+    const int row_tiles = min(16, (a.N - n0 + 15) / 16), rows = min(32 * T0, a.M - m0);
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (long long)nt * 16 * a.units * 128,
+                                                (unsigned)(row_tiles * a.units) * 2048u);
+    const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.w_scale + (long long)nt * 8 * a.units * 64,
+                                                 (unsigned)((row_tiles + 1) / 2 * a.units) * 256u);
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + m0 * a.ldx, (unsigned)((rows - 1) * a.ldx) + (unsigned)a.x_bytes);
+    const unsigned char *xs0 = a.x_scale + m0 * a.ldxs;
+    const unsigned shift = WORDS ? 0u : (unsigned)((uintptr_t)xs0 & 3);
+    const __amdgpu_buffer_rsrc_t xsr =
+        make_rsrc(xs0 - shift, (shift + (unsigned)((rows - 1) * a.ldxs) + (unsigned)a.blocks + 3u) & ~3u);
+    unsigned w_off[2], ws_off, x_off[L::kXCopies], xs_off, xs_block;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        w_off[j] = (unsigned)((2 * wave + j) * a.units) * 2048u + 16u * lane;
+    ws_off = (unsigned)(wave * a.units) * 256u + 4u * lane;
+    const int chunk = (lane & 7) ^ (lane >> 3);         // of a row's 128 bytes, at c ^ (r % 8)
+#pragma unroll
+    for (int j = 0; j < L::kXCopies; ++j) {
+        const int row = 8 * (wave + 8 * j) + (lane >> 3);
+        x_off[j] = row < rows ? (unsigned)(row * a.ldx) + 16u * chunk : kSkip;
+    }
+    if constexpr (WORDS) {
+        const int row = 32 * wave + (lane >> 1);
+        xs_block = 4u * (lane & 1);
+        xs_off = row < rows ? (unsigned)(row * a.ldxs) + xs_block : kSkip;
+    } else {
+        const int row = 16 * wave + (lane >> 2);
+        const unsigned at = shift + (unsigned)(row * a.ldxs), word = lane & 3;
+        xs_off = row < rows && word < 3 ? (at & ~3u) + 4u * word : kSkip;
+        xs_block = 4u * word > (at & 3u) ? 4u * word - (at & 3u) : 0u;
+    }
+    const int steps = 2 * a.units;
+    const auto copy_xs = [&](int unit, int place) __attribute__((always_inline)) {
+        const unsigned b = (unsigned)unit * kUnitBlocks;
+        copy_words(xsr, ring + L::kPowers + place * L::kUnitVecs + 128 + wave * 16,
+                   xs_off + (b + xs_block < (unsigned)a.blocks ? b : kSkip));
+    };
+    const auto copy = [&](int c, int st, int buf, int place) __attribute__((always_inline)) {
+        u32x4 *base = ring + buf * L::kVecs;
+        if (c < 2)
+            copy_vectors(wr, base + (2 * wave + c) * 64, w_off[c] + (st < steps ? (unsigned)st * 1024u : kSkip));
+        else if (c < 2 + L::kXCopies)           // past K the codes are the next row's and may be NaN
+            copy_vectors(xr, base + L::kX + (wave + 8 * (c - 2)) * 64,
+                         x_off[c < 2 ? 0 : c - 2 < L::kXCopies ? c - 2 : 0] +
+                             (st * 128 + 16 * chunk < a.x_bytes ? (unsigned)st * 128u : kSkip));
+        else if (st % 2 == 0)
+            copy_words(wsr, ring + L::kPowers + place * L::kUnitVecs + wave * 16,
+                       ws_off + (st < steps ? (unsigned)st * 128u : kSkip));
+        else
+            copy_xs(st / 2 + 1, place);
+    };
+    f32x4 acc[4][T0];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
+            acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 wf[4], xf[T0];
+    float wp[4], xp[T0];
+    const auto read_w = [&](int buf, int k, int place) __attribute__((always_inline)) {
+        const u32x4 *at = ring + buf * L::kVecs + lane + 4 * quarter * 64;
+        const unsigned *p = reinterpret_cast<const unsigned *>(ring + L::kPowers + place * L::kUnitVecs) +
+                            2 * quarter * 64 + lane;
+        const unsigned s[2] = {p[0], p[64]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wf[i] = at[i * 64];
+            wp[i] = power_of(s[i / 2] >> (16 * (i & 1) + 8 * k) & 0xFFu);
+        }
+    };
+    const auto read_powers = [&](int t, int k, int unit, int place) __attribute__((always_inline)) {
+        const int row = 16 * T0 * half + (lane & 15);
+        const unsigned off = WORDS ? 0u : (shift + (unsigned)(row * (int)a.ldxs)) & 3u;
+        const unsigned char *p = reinterpret_cast<const unsigned char *>(ring + L::kPowers + place * L::kUnitVecs + 128) +
+                                 (WORDS ? 8 : 16) * row + off + 4 * k + g;
+        const bool own = WORDS || kUnitBlocks * unit + 4 * k + g < a.blocks;
+        xp[t] = power_of(own ? (unsigned)p[(WORDS ? 128 : 256) * t] : 0u);
+    };
+    // Half `h` (16 values of its block for each lane) of token tile t.
+    const auto read_x = [&](int t, int buf, int h) __attribute__((always_inline)) {
+        xf[t] = (ring + buf * L::kVecs + L::kX + T0 * half * 128 + 8 * (lane & 15) + ((2 * g + h) ^ (lane & 7)))[t * 128];
+    };
+#pragma unroll
+    for (int st = 0; st < kStages; ++st) {
+        if (st == 0)
+            copy_xs(0, 0);
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+            copy(c, st, st, (st + 1) / 2 % L::kUnits);
+    }
+    // step st takes buffer st % kStages, unit u place u % kUnits
+    int buf = 0, place = 0;
+    int ahead = (kStages + 1) / 2 % L::kUnits;  // of the unit whose powers go with step st + kStages
+    for (int st = 0; st < steps; ++st) {
+        const int k = st & 1, unit = st / 2;
+        // this wave's copies of this step have landed, and everyone's
+        landed<(kStages - 1) * kCopies, 0>();
+        read_w(buf, k, place);
+#pragma unroll
+        for (int t = 0; t < T0; ++t) {
+            read_x(t, buf, 0);
+            read_powers(t, k, unit, place);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            bf16x8 wb[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    wb[j][i] = bf16_of_4(wf[i][2 * h + j], wp[i]);
+#pragma unroll
+            for (int t = 0; t < T0; ++t) {
+                bf16x8 xb[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    xb[j] = bf16_of_8(xf[t][2 * j], xf[t][2 * j + 1], xp[t]);
+                if (h == 0)
+                    read_x(t, buf, 1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][i], xb[j], acc[i][t], 0, 0, 0);
+            }
+        }
+        // all waves have read this step's operands: its buffer is free
+        landed<(kStages - 1) * kCopies, 0>();
+        const bool ws_next = ((st + kStages) & 1) == 0;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+            copy(c, st + kStages, buf, ahead);
+        // places go on after the later of a unit's two powers
+        if (ws_next)
+            ahead = ahead + 1 < L::kUnits ? ahead + 1 : 0;
+        buf = buf + 1 < kStages ? buf + 1 : 0;
+        if (k)
+            place = place + 1 < L::kUnits ? place + 1 : 0;
+    }
+    __builtin_amdgcn_s_waitcnt(wait_for(0, 15));        // no copy outlives its workgroup's LDS
+#pragma unroll
+    for (int t = 0; t < T0; ++t) {
+        const int m = m0 + 16 * (T0 * half + t) + (lane & 15);
+        if (m >= a.M)
+            continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 64 * quarter + 16 * i + 4 * g;
+            if (n < a.N)
+                store4(a, m, n, acc[i][t]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -823,27 +1005,34 @@ const void *rows_kernel(int rt, int mt, int tokens)
 constexpr int kAnyTiles = 4;
 
 template <int T0>
-const void *tiles_fn(bool words)
+const void *tiles_fn(int bits, bool words)
 {
-    if constexpr (T0 > kAnyTiles)
-        return reinterpret_cast<const void *>(product_tiles<T0, true>);
-    else
-        return words ? reinterpret_cast<const void *>(product_tiles<T0, true>)
-                     : reinterpret_cast<const void *>(product_tiles<T0, false>);
+    if constexpr (T0 <= kAnyTiles)
+        if (!words)
+            return bits == 4 ? reinterpret_cast<const void *>(product_tiles<T0, false>)
+                             : reinterpret_cast<const void *>(product_tiles8<T0, false>);
+    return bits == 4 ? reinterpret_cast<const void *>(product_tiles<T0, true>)
+                     : reinterpret_cast<const void *>(product_tiles8<T0, true>);
 }
 
-const void *tiles_kernel(int t0, bool words)
+const void *tiles_kernel(int t0, int bits, bool words)
 {
-    return t0 == 1 ? tiles_fn<1>(words) : t0 == 2 ? tiles_fn<2>(words) : t0 == 3 ? tiles_fn<3>(words)
-         : t0 == 4 ? tiles_fn<4>(words) : t0 == 5 ? tiles_fn<5>(words) : t0 == 6 ? tiles_fn<6>(words)
-         : t0 == 7 ? tiles_fn<7>(words) : tiles_fn<8>(words);
+    return t0 == 1 ? tiles_fn<1>(bits, words) : t0 == 2 ? tiles_fn<2>(bits, words) : t0 == 3 ? tiles_fn<3>(bits, words)
+         : t0 == 4 ? tiles_fn<4>(bits, words) : t0 == 5 ? tiles_fn<5>(bits, words) : t0 == 6 ? tiles_fn<6>(bits, words)
+         : t0 == 7 ? tiles_fn<7>(bits, words) : tiles_fn<8>(bits, words);
 }
 
-int tiles_lds(int t0)
+template <int T0>
+int tiles_lds_of(int bits)
 {
-    return t0 == 1 ? TilesLayout<1>::kBytes : t0 == 2 ? TilesLayout<2>::kBytes : t0 == 3 ? TilesLayout<3>::kBytes
-         : t0 == 4 ? TilesLayout<4>::kBytes : t0 == 5 ? TilesLayout<5>::kBytes : t0 == 6 ? TilesLayout<6>::kBytes
-         : t0 == 7 ? TilesLayout<7>::kBytes : TilesLayout<8>::kBytes;
+    return bits == 4 ? TilesLayout<T0>::kBytes : Tiles8Layout<T0>::kBytes;
+}
+
+int tiles_lds(int t0, int bits)
+{
+    return t0 == 1 ? tiles_lds_of<1>(bits) : t0 == 2 ? tiles_lds_of<2>(bits) : t0 == 3 ? tiles_lds_of<3>(bits)
+         : t0 == 4 ? tiles_lds_of<4>(bits) : t0 == 5 ? tiles_lds_of<5>(bits) : t0 == 6 ? tiles_lds_of<6>(bits)
+         : t0 == 7 ? tiles_lds_of<7>(bits) : tiles_lds_of<8>(bits);
 }
 
 // A tile shape and the time of its rounds over 256 CUs, in us over K = 7168.
@@ -852,13 +1041,14 @@ struct Tiling {
     float us;
 };
 
-Tiling tiles_tiling(int M, int N, bool words)
+Tiling tiles_tiling(int M, int N, int bits, bool words)
 {
-    static const float round_us[9] = {0.0f, 18.0f, 21.0f, 24.0f, 26.0f, 37.0f, 38.0f, 42.0f, 45.0f};
+    static const float us4[9] = {0.0f, 22.0f, 23.5f, 27.0f, 30.4f, 35.5f, 39.3f, 43.5f, 47.6f};
+    static const float us8[9] = {0.0f, 24.0f, 34.0f, 44.0f, 54.0f, 64.0f, 74.0f, 84.0f, 94.0f};
     Tiling best{0, 0, 0.0f};
     for (int t = words ? 8 : kAnyTiles; t >= 1; --t) {
         const long long count = ((long long)N + 255) / 256 * ((M + 32 * t - 1) / (32 * t));
-        const float us = (float)((count + 255) / 256) * round_us[t];
+        const float us = (float)((count + 255) / 256) * (bits == 4 ? us4 : us8)[t];
         if (!best.r || us < best.us)
             best = Tiling{16, t, us};
     }
@@ -874,7 +1064,7 @@ Tiling rows_tiling(int M, int N, int bits)
     static const struct {
         int r, t;
         float us4, us8;
-    } kTiles[] = {{1, 1, 1.65f, 2.45f}, {2, 1, 2.05f, 3.2f}, {4, 1, 3.2f, 5.2f}, {2, 2, 3.05f, 5.3f}, {4, 2, 5.45f, 9.7f}};
+    } kTiles[] = {{1, 1, 1.65f, 2.45f}, {2, 1, 2.05f, 3.2f}, {4, 1, 3.4f, 5.2f}, {2, 2, 3.2f, 5.3f}, {4, 2, 4.6f, 9.7f}};
     Tiling best{0, 0, 0.0f};
     for (const auto &k : kTiles) {
         if (k.t == 2 && M <= 16)
@@ -894,7 +1084,7 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
     void *params[] = {&a};
     const bool words = a.words != 0;
     const Tiling rows = rows_tiling(a.M, a.N, bits);
-    const Tiling tiles = a.M > 64 && bits == 4 ? tiles_tiling(a.M, a.N, words) : rows;
+    const Tiling tiles = a.M > 64 ? tiles_tiling(a.M, a.N, bits, words) : rows;
     const bool many = tiles.us < rows.us;
     const int n_rows = many ? 256 : 16 * rows.r, tokens = many ? 32 * tiles.t : 16 * rows.t;
     const long long n_tiles = ((long long)a.N + n_rows - 1) / n_rows, m_tiles = ((long long)a.M + tokens - 1) / tokens;
@@ -926,20 +1116,21 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
     }
     a.n_tiles = (int)n_tiles;
     a.m_tiles = (int)m_tiles;
-    const void *fn = many        ? tiles_kernel(tiles.t, words)
+    const void *fn = many        ? tiles_kernel(tiles.t, bits, words)
                      : bits == 4 ? (a.m_tiles == 1 ? rows_kernel<4, true>(rows.r, rows.t, a.M) : rows_kernel<4, false>(rows.r, rows.t, a.M))
                                : (a.m_tiles == 1 ? rows_kernel<8, true>(rows.r, rows.t, a.M) : rows_kernel<8, false>(rows.r, rows.t, a.M));
     return hipLaunchKernel(fn, dim3((unsigned)(n_tiles * m_tiles)), dim3(kThreads), params,
-                           many ? (size_t)tiles_lds(tiles.t) : 0, stream);
+                           many ? (size_t)tiles_lds(tiles.t, bits) : 0, stream);
 }
 
 // Dynamic LDS past 64 KiB has to be asked for, on every device that the kernels run on.
 void raise_limits()
 {
     for (int t0 = 1; t0 <= 8; ++t0)
-        for (const bool words : {true, t0 > kAnyTiles})
-            (void)hipFuncSetAttribute(tiles_kernel(t0, words), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                      tiles_lds(t0));
+        for (const int bits : {4, 8})
+            for (const bool words : {false, true})
+                (void)hipFuncSetAttribute(tiles_kernel(t0, bits, words), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                          tiles_lds(t0, bits));
 }
 
 // fn(first vector, launch's end) over count vectors of 256-thread workgroups, in launches of fewer than 2^32 threads.
