@@ -828,7 +828,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
         copy_words(xsr, ring + L::kPowers + place * L::kUnitVecs + 128 + wave * 16,
                    xs_off + (b + xs_block < (unsigned)a.blocks ? b : kSkip));
     };
-    const auto copy = [&](int c, int st, int buf, int place) __attribute__((always_inline)) {
+    const auto copy = [&](int c, auto parity, int st, int buf, int place) __attribute__((always_inline)) {
         u32x4 *base = ring + buf * L::kVecs;
         if (c < 2)
             copy_vectors(wr, base + (2 * wave + c) * 64, w_off[c] + (st < steps ? (unsigned)st * 1024u : kSkip));
@@ -836,7 +836,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
             copy_vectors(xr, base + L::kX + (wave + 8 * (c - 2)) * 64,
                          x_off[c < 2 ? 0 : c - 2 < L::kXCopies ? c - 2 : 0] +
                              (st * 128 + 16 * chunk < a.x_bytes ? (unsigned)st * 128u : kSkip));
-        else if (st % 2 == 0)
+        else if (decltype(parity)::value == 0)
             copy_words(wsr, ring + L::kPowers + place * L::kUnitVecs + wave * 16,
                        ws_off + (st < steps ? (unsigned)st * 128u : kSkip));
         else
@@ -848,18 +848,15 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
 #pragma unroll
         for (int t = 0; t < T0; ++t)
             acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 wf[4], xf[T0];
-    float wp[4], xp[T0];
-    const auto read_w = [&](int buf, int k, int place) __attribute__((always_inline)) {
-        const u32x4 *at = ring + buf * L::kVecs + lane + 4 * quarter * 64;
-        const unsigned *p = reinterpret_cast<const unsigned *>(ring + L::kPowers + place * L::kUnitVecs) +
-                            2 * quarter * 64 + lane;
-        const unsigned s[2] = {p[0], p[64]};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            wf[i] = at[i * 64];
-            wp[i] = power_of(s[i / 2] >> (16 * (i & 1) + 8 * k) & 0xFFu);
-        }
+    u32x4 wf[4], xf[2][T0];
+    unsigned ws[2], xs[T0];
+    // A wave's operands of a step, each read one step ahead, into the registers
+    // that the step before has just converted from.
+    const auto read_w = [&](int i, int buf, int place) __attribute__((always_inline)) {
+        wf[i] = (ring + buf * L::kVecs + lane + 4 * quarter * 64)[i * 64];
+        if (i % 2 == 0)
+            ws[i / 2] = (reinterpret_cast<const unsigned *>(ring + L::kPowers + place * L::kUnitVecs) + 2 * quarter * 64 +
+                         lane)[i / 2 * 64];
     };
     const auto read_powers = [&](int t, int k, int unit, int place) __attribute__((always_inline)) {
         const int row = 16 * T0 * half + (lane & 15);
@@ -867,33 +864,44 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
         const unsigned char *p = reinterpret_cast<const unsigned char *>(ring + L::kPowers + place * L::kUnitVecs + 128) +
                                  (WORDS ? 8 : 16) * row + off + 4 * k + g;
         const bool own = WORDS || kUnitBlocks * unit + 4 * k + g < a.blocks;
-        xp[t] = power_of(own ? (unsigned)p[(WORDS ? 128 : 256) * t] : 0u);
+        xs[t] = own ? (unsigned)p[(WORDS ? 128 : 256) * t] : 0u;
     };
-    // Half `h` (16 values of its block for each lane) of token tile t.
+    // Half h (16 values of its block for each lane) of token tile t.
     const auto read_x = [&](int t, int buf, int h) __attribute__((always_inline)) {
-        xf[t] = (ring + buf * L::kVecs + L::kX + T0 * half * 128 + 8 * (lane & 15) + ((2 * g + h) ^ (lane & 7)))[t * 128];
+        xf[h][t] =
+            (ring + buf * L::kVecs + L::kX + T0 * half * 128 + 8 * (lane & 15) + ((2 * g + h) ^ (lane & 7)))[t * 128];
     };
+    copy_xs(0, 0);
 #pragma unroll
-    for (int st = 0; st < kStages; ++st) {
-        if (st == 0)
-            copy_xs(0, 0);
+    for (int st = 0; st < kStages; ++st)
 #pragma unroll
         for (int c = 0; c < kCopies; ++c)
-            copy(c, st, st, (st + 1) / 2 % L::kUnits);
-    }
-    // step st takes buffer st % kStages, unit u place u % kUnits
-    int buf = 0, place = 0;
-    int ahead = (kStages + 1) / 2 % L::kUnits;  // of the unit whose powers go with step st + kStages
-    for (int st = 0; st < steps; ++st) {
-        const int k = st & 1, unit = st / 2;
-        // this wave's copies of this step have landed, and everyone's
-        landed<(kStages - 1) * kCopies, 0>();
-        read_w(buf, k, place);
+            if (st % 2 == 0)
+                copy(c, Const<0>{}, st, st, (st + 1) / 2 % L::kUnits);
+            else
+                copy(c, Const<1>{}, st, st, (st + 1) / 2 % L::kUnits);
+    landed<(kStages - 1) * kCopies, 15>();
 #pragma unroll
-        for (int t = 0; t < T0; ++t) {
-            read_x(t, buf, 0);
-            read_powers(t, k, unit, place);
-        }
+    for (int i = 0; i < 4; ++i)
+        read_w(i, 0, 0);
+#pragma unroll
+    for (int t = 0; t < T0; ++t) {
+        read_x(t, 0, 0);
+        read_x(t, 0, 1);
+        read_powers(t, 0, 0, 0);
+    }
+    // A step's products, k its parity, with the copies of step `st` and the reads of
+    // the next step between them.
+    const auto run = [&](auto parity, int st, int buf, int st_place, int next, int unit, int place)
+                         __attribute__((always_inline)) {
+        constexpr int k = decltype(parity)::value;
+        float wp[4], xp[T0];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            wp[i] = power_of(ws[i / 2] >> (16 * (i & 1) + 8 * k) & 0xFFu);
+#pragma unroll
+        for (int t = 0; t < T0; ++t)
+            xp[t] = power_of(xs[t]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             bf16x8 wb[2][4];
@@ -907,9 +915,17 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
                 bf16x8 xb[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    xb[j] = bf16_of_8(xf[t][2 * j], xf[t][2 * j + 1], xp[t]);
-                if (h == 0)
-                    read_x(t, buf, 1);
+                    xb[j] = bf16_of_8(xf[h][t][2 * j], xf[h][t][2 * j + 1], xp[t]);
+#pragma unroll
+                for (int c = h * T0 + t; c < kCopies; c += 2 * T0)
+                    copy(c, Const<(k + kStages) % 2>{}, st, buf, st_place);
+                read_x(t, next, h);
+                if (h == 1) {
+#pragma unroll
+                    for (int i = t; i < 4; i += T0)
+                        read_w(i, next, place);
+                    read_powers(t, 1 - k, unit, place);
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -917,18 +933,24 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
                         acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][i], xb[j], acc[i][t], 0, 0, 0);
             }
         }
-        // all waves have read this step's operands: its buffer is free
-        landed<(kStages - 1) * kCopies, 0>();
-        const bool ws_next = ((st + kStages) & 1) == 0;
-#pragma unroll
-        for (int c = 0; c < kCopies; ++c)
-            copy(c, st + kStages, buf, ahead);
-        // places go on after the later of a unit's two powers
-        if (ws_next)
-            ahead = ahead + 1 < L::kUnits ? ahead + 1 : 0;
-        buf = buf + 1 < kStages ? buf + 1 : 0;
-        if (k)
-            place = place + 1 < L::kUnits ? place + 1 : 0;
+    };
+    // step st takes buffer st % kStages, unit u place u % kUnits
+    int buf = 0, place = 0;
+    int ahead = (kStages + 1) / 2 % L::kUnits;  // of the unit whose powers go with step st + kStages
+    for (int st = 0; st < steps; st += 2) {
+        const int unit = st / 2, next_place = place + 1 < L::kUnits ? place + 1 : 0;
+        const int next_ahead = ahead + 1 < L::kUnits ? ahead + 1 : 0;
+        int next = buf + 1 < kStages ? buf + 1 : 0;
+        // this wave's copies of the next step have landed, and it has read all of this one
+        landed<(kStages - 2) * kCopies, 0>();
+        run(Const<0>{}, st + kStages, buf, ahead, next, unit, place);
+        buf = next;
+        next = buf + 1 < kStages ? buf + 1 : 0;
+        landed<(kStages - 2) * kCopies, 0>();
+        run(Const<1>{}, st + 1 + kStages, buf, kStages % 2 ? ahead : next_ahead, next, unit + 1, next_place);
+        buf = next;
+        place = next_place;
+        ahead = next_ahead;
     }
     __builtin_amdgcn_s_waitcnt(wait_for(0, 15));        // no copy outlives its workgroup's LDS
 #pragma unroll
@@ -1001,8 +1023,9 @@ const void *rows_kernel(int rt, int mt, int tokens)
                                                                        : rows_kernel_of<4, BITS, NT>(mt, tokens);
 }
 
-// Powers of any alignment take more registers: tiles of up to 32 * kAnyTiles tokens fit.
-constexpr int kAnyTiles = 4;
+// The largest tiles whose registers fit: 32 * 8 4-bit tokens, 32 * 6 8-bit ones,
+// 32 * 4 with powers of any alignment.
+constexpr int kTiles = 8, kTiles8 = 6, kAnyTiles = 4;
 
 template <int T0>
 const void *tiles_fn(int bits, bool words)
@@ -1011,8 +1034,10 @@ const void *tiles_fn(int bits, bool words)
         if (!words)
             return bits == 4 ? reinterpret_cast<const void *>(product_tiles<T0, false>)
                              : reinterpret_cast<const void *>(product_tiles8<T0, false>);
-    return bits == 4 ? reinterpret_cast<const void *>(product_tiles<T0, true>)
-                     : reinterpret_cast<const void *>(product_tiles8<T0, true>);
+    if constexpr (T0 <= kTiles8)
+        if (bits == 8)
+            return reinterpret_cast<const void *>(product_tiles8<T0, true>);
+    return reinterpret_cast<const void *>(product_tiles<T0, true>);
 }
 
 const void *tiles_kernel(int t0, int bits, bool words)
@@ -1044,9 +1069,9 @@ struct Tiling {
 Tiling tiles_tiling(int M, int N, int bits, bool words)
 {
     static const float us4[9] = {0.0f, 22.0f, 23.5f, 27.0f, 30.4f, 35.5f, 39.3f, 43.5f, 47.6f};
-    static const float us8[9] = {0.0f, 24.0f, 34.0f, 44.0f, 54.0f, 64.0f, 74.0f, 84.0f, 94.0f};
+    static const float us8[9] = {0.0f, 45.0f, 50.0f, 57.0f, 65.0f, 81.0f, 91.0f};
     Tiling best{0, 0, 0.0f};
-    for (int t = words ? 8 : kAnyTiles; t >= 1; --t) {
+    for (int t = !words ? kAnyTiles : bits == 4 ? kTiles : kTiles8; t >= 1; --t) {
         const long long count = ((long long)N + 255) / 256 * ((M + 32 * t - 1) / (32 * t));
         const float us = (float)((count + 255) / 256) * (bits == 4 ? us4 : us8)[t];
         if (!best.r || us < best.us)
@@ -1126,7 +1151,7 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
 // Dynamic LDS past 64 KiB has to be asked for, on every device that the kernels run on.
 void raise_limits()
 {
-    for (int t0 = 1; t0 <= 8; ++t0)
+    for (int t0 = 1; t0 <= kTiles; ++t0)
         for (const int bits : {4, 8})
             for (const bool words : {false, true})
                 (void)hipFuncSetAttribute(tiles_kernel(t0, bits, words), hipFuncAttributeMaxDynamicSharedMemorySize,
