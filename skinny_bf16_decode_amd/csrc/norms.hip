@@ -28,7 +28,7 @@ struct NormOut {
     unsigned char *q;
     void *scale;                // float [M], or bytes [M][lds]
     long long ldo, ldq, lds;
-    double eps;
+    double eps, inverse_K;
     int weight_type, out_type, q_kind;
 };
 
@@ -45,7 +45,7 @@ struct JArgs {
     void *out;
     long long ldr, ldy, ldg, ldo;
     NormOut n;                  // n.weight NULL: no norm of the result
-    double eps;
+    double eps, inverse_K;
     float alpha, beta;
     int residual_type, y_type, weight_type, gate_type, sigmoid;
     int M, K;
@@ -71,43 +71,70 @@ __device__ __forceinline__ Place place_of(int lanes, int M)
     return p;
 }
 
-// The sum of a row's threads' v, in every one of them.
-__device__ __forceinline__ double row_sum(double v, int lanes, const Place &p, double *shared)
+// v of the lane that a DPP control names.
+template <int CTRL>
+__device__ __forceinline__ unsigned lane_of(unsigned v)
 {
-    const int within = lanes < 64 ? lanes : 64;
-    for (int s = 1; s < within; s *= 2)
-        v += __shfl_xor(v, s, 64);
-    if (lanes > 64) {
-        const int wave = (int)threadIdx.x >> 6;
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0)
-            shared[wave] = v;
-        __syncthreads();
-        v = 0.0;
-        for (int w = 0; w < p.waves; ++w)
-            v += shared[p.first_wave + w];
-    }
-    return v;
+    return (unsigned)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ double lane_of(double v)
+{
+    const unsigned long long u = __double_as_longlong(v);
+    return __longlong_as_double((unsigned long long)lane_of<CTRL>((unsigned)(u >> 32)) << 32 | lane_of<CTRL>((unsigned)u));
 }
 
-__device__ __forceinline__ unsigned row_max(unsigned v, int lanes, const Place &p, double *shared)
+// Both halves' v: of the lanes whose number's bit 4 (5) is 0, and is 1.
+template <int BIT>
+__device__ __forceinline__ void halves(unsigned v, unsigned &a, unsigned &b)
 {
-    const int within = lanes < 64 ? lanes : 64;
-    for (int s = 1; s < within; s *= 2) {
-        const unsigned o = (unsigned)__shfl_xor((int)v, s, 64);
-        v = o > v ? o : v;
+    typedef __attribute__((ext_vector_type(2))) unsigned int pair;
+    const pair r = BIT == 4 ? __builtin_bit_cast(pair, __builtin_amdgcn_permlane16_swap(v, v, false, false))
+                            : __builtin_bit_cast(pair, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+    a = r[0];
+    b = r[1];
+}
+template <int BIT>
+__device__ __forceinline__ void halves(double v, double &a, double &b)
+{
+    const unsigned long long u = __double_as_longlong(v);
+    unsigned al, bl, ah, bh;
+    halves<BIT>((unsigned)u, al, bl);
+    halves<BIT>((unsigned)(u >> 32), ah, bh);
+    a = __longlong_as_double((unsigned long long)ah << 32 | al);
+    b = __longlong_as_double((unsigned long long)bh << 32 | bl);
+}
+
+__device__ __forceinline__ double both(double a, double b) { return a + b; }
+__device__ __forceinline__ unsigned both(unsigned a, unsigned b) { return a > b ? a : b; }
+
+// The sum (double) or maximum (unsigned) of a row's threads' v, in every one of
+// them: within 16 lanes by quad permutes and mirrors, then by halves of 32 and
+// 64, then over the row's waves through `shared`, which serves one call.
+template <typename T>
+__device__ __forceinline__ T over_row(T v, int lanes, const Place &p, T *shared)
+{
+    v = both(v, lane_of<0xB1>(v));              // lane ^ 1
+    v = both(v, lane_of<0x4E>(v));              // lane ^ 2
+    v = both(v, lane_of<0x141>(v));             // the other four of eight
+    v = both(v, lane_of<0x140>(v));             // the other eight of 16
+    if (lanes >= 32) {
+        T a, b;
+        halves<4>(v, a, b);
+        v = both(a, b);
+    }
+    if (lanes >= 64) {
+        T a, b;
+        halves<5>(v, a, b);
+        v = both(a, b);
     }
     if (lanes > 64) {
-        unsigned *tops = reinterpret_cast<unsigned *>(shared);
-        const int wave = (int)threadIdx.x >> 6;
-        __syncthreads();
         if ((threadIdx.x & 63) == 0)
-            tops[wave] = v;
+            shared[threadIdx.x >> 6] = v;
         __syncthreads();
-        for (int w = 0; w < p.waves; ++w) {
-            const unsigned o = tops[p.first_wave + w];
-            v = o > v ? o : v;
-        }
+        v = shared[p.first_wave];
+        for (int w = 1; w < p.waves; ++w)
+            v = both(v, shared[p.first_wave + w]);
     }
     return v;
 }
@@ -123,9 +150,17 @@ __device__ __forceinline__ double squares(const float (&f)[8])
     return s;
 }
 
-__device__ __forceinline__ float rms_factor(double sum, int K, double eps)
+// 1 / sqrt(sum / K + eps): the unit's reciprocal root (some 2^-26) and two steps
+// of Newton's, which leave 64 bits' rounding errors.  Past the normal range of
+// what they square, infinity and NaN among it, the unit's own result.
+__device__ __forceinline__ float rms_factor(double sum, double inverse_K, double eps)
 {
-    return (float)(1.0 / sqrt(sum / (double)K + eps));
+    const double v = fma(sum, inverse_K, eps);
+    const double y0 = __builtin_amdgcn_rsq(v);
+    const double h = 0.5 * v;
+    const double y1 = fma(y0, fma(-h * y0, y0, 0.5), y0);
+    const double y2 = fma(y1, fma(-h * y1, y1, 0.5), y1);
+    return (float)(v < 0x1p1000 ? y2 : y0);
 }
 
 __device__ __forceinline__ const char *at_row(const void *p, long long row, long long ld, int type)
@@ -133,22 +168,74 @@ __device__ __forceinline__ const char *at_row(const void *p, long long row, long
     return static_cast<const char *>(p) + row * ld * (type == SKINNY_TYPE_F32 ? 4 : 2);
 }
 
+// Octet i of this thread's, zero past the row: as many as it has at most lie
+// `lanes` octets apart.
+template <bool VEC>
+__device__ __forceinline__ Octet own_octet(const void *row, int type, int i, int K, int lanes, const Place &p)
+{
+    const int o = p.t + i * lanes;
+    Octet v;
+    v.a = v.b = u32x4{0u, 0u, 0u, 0u};
+    if (o < (K + 7) / 8)
+        v = load_octet<VEC>(row, type, o, K);
+    return v;
+}
+
+// What is written of octet o of a norm, f, which is zero past the row.
+template <bool VEC>
+__device__ __forceinline__ void write_octet(const NormOut &n, int o, bool here, int K, const Place &p,
+                                            const RowScale &scale8, float (&f)[8])
+{
+    if (n.q_kind == SKINNY_ROWS_MX4 || n.q_kind == SKINNY_ROWS_MX8) {
+        unsigned byte;
+        unsigned char *q = n.q + p.row * n.ldq;
+        if (n.q_kind == SKINNY_ROWS_MX4) {
+            const u32x2 codes = block_codes<4>(f, byte);
+            if (here)
+                store_codes<VEC, 4>(q, o, codes);
+        } else {
+            const u32x2 codes = block_codes<8>(f, byte);
+            if (here)
+                store_codes<VEC, 8>(q, o, codes);
+        }
+        if (here && (o & 3) == 0)
+            static_cast<unsigned char *>(n.scale)[p.row * n.lds + (o >> 2)] = (unsigned char)byte;
+    } else if (n.q_kind == SKINNY_ROWS_INT8 && here) {
+        unsigned char *q = n.q + p.row * n.ldq;
+        u32x2 codes;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4)
+            codes[e / 4] = (unsigned)(to_int8(f[e], scale8) & 0xFF) | (unsigned)(to_int8(f[e + 1], scale8) & 0xFF) << 8 |
+                           (unsigned)(to_int8(f[e + 2], scale8) & 0xFF) << 16 | (unsigned)to_int8(f[e + 3], scale8) << 24;
+        if constexpr (VEC) {
+            store_codes<true, 8>(q, o, codes);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned w = codes[e / 4];
+                if (8LL * o + e < K)
+                    q[8LL * o + e] = (unsigned char)(w >> (8 * (e & 3)));
+            }
+        }
+    }
+    if (n.out && here) {
+        const Octet y = pack_octet(n.out_type, f);
+        store_octet<VEC>(const_cast<char *>(at_row(n.out, p.row, n.ldo, n.out_type)), n.out_type, o, K, y);
+    }
+}
+
 // The norm of a row whose octets get(i, f) gives, i = 0, 1, ... for the octets
-// t + i lanes of this thread; f is zero past the row.  OCTETS: how many at most, 0: any.
+// t + i lanes of this thread; f is zero past the row.  OCTETS: how many at most,
+// 0: any.  `first` is the weight's octet 0; the others are loaded one ahead.
 template <bool VEC, int OCTETS, typename Get>
 __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, int lanes, const Place &p,
-                                           double *shared, Get get)
+                                           unsigned *tops, const Octet &first, Get get)
 {
     const int octets = (K + 7) / 8, turns = OCTETS ? OCTETS : (octets + lanes - 1) / lanes;
-    const float r = rms_factor(sum, K, n.eps);
-    const auto value = [&](int i, float (&f)[8]) {
-        const int o = p.t + i * lanes;
+    const float r = rms_factor(sum, n.inverse_K, n.eps);
+    const auto value = [&](int i, const Octet &raw, float (&f)[8]) {
         get(i, f);
         float w[8];
-        Octet raw;
-        raw.a = raw.b = u32x4{0u, 0u, 0u, 0u};
-        if (o < octets)
-            raw = load_octet<VEC>(n.weight, n.weight_type, o, K);
         unpack_octet(raw, n.weight_type, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -159,10 +246,12 @@ __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, 
     scale8.fine = false;
     if (n.q_kind == SKINNY_ROWS_INT8) {
         unsigned top = 0;
+        Octet w = first;
 #pragma unroll
         for (int i = 0; i < turns; ++i) {
+            const Octet next = i + 1 < turns ? own_octet<VEC>(n.weight, n.weight_type, i + 1, K, lanes, p) : w;
             float f[8];
-            value(i, f);
+            value(i, w, f);
             // past the row the weight is zero, and r may be infinite or NaN
             const int left = K - 8 * (p.t + i * lanes);
 #pragma unroll
@@ -170,74 +259,39 @@ __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, 
                 const unsigned m = e < left ? mag(f[e]) : 0u;
                 top = m > top ? m : top;
             }
+            w = next;
+            __builtin_amdgcn_sched_barrier(0);
         }
         float scale;
-        scale8 = row_scale(row_max(top, lanes, p, shared), scale);
+        scale8 = row_scale(over_row(top, lanes, p, tops), scale);
         if (p.in && p.t == 0)
             static_cast<float *>(n.scale)[p.row] = scale;
     }
+    Octet w = first;
 #pragma unroll
     for (int i = 0; i < turns; ++i) {
         const int o = p.t + i * lanes;
+        const Octet next = i + 1 < turns ? own_octet<VEC>(n.weight, n.weight_type, i + 1, K, lanes, p) : w;
         float f[8];
-        value(i, f);
-        const bool here = p.in && o < octets;
-        if (n.q_kind == SKINNY_ROWS_MX4 || n.q_kind == SKINNY_ROWS_MX8) {
-            unsigned byte;
-            unsigned char *q = n.q + p.row * n.ldq;
-            if (n.q_kind == SKINNY_ROWS_MX4) {
-                const u32x2 codes = block_codes<4>(f, byte);
-                if (here)
-                    store_codes<VEC, 4>(q, o, codes);
-            } else {
-                const u32x2 codes = block_codes<8>(f, byte);
-                if (here)
-                    store_codes<VEC, 8>(q, o, codes);
-            }
-            if (here && (o & 3) == 0)
-                static_cast<unsigned char *>(n.scale)[p.row * n.lds + (o >> 2)] = (unsigned char)byte;
-        } else if (n.q_kind == SKINNY_ROWS_INT8 && here) {
-            unsigned char *q = n.q + p.row * n.ldq;
-            u32x2 codes;
-#pragma unroll
-            for (int e = 0; e < 8; e += 4)
-                codes[e / 4] = (unsigned)(to_int8(f[e], scale8) & 0xFF) | (unsigned)(to_int8(f[e + 1], scale8) & 0xFF) << 8 |
-                               (unsigned)(to_int8(f[e + 2], scale8) & 0xFF) << 16 | (unsigned)to_int8(f[e + 3], scale8) << 24;
-            if constexpr (VEC) {
-                store_codes<true, 8>(q, o, codes);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const unsigned w = codes[e / 4];
-                    if (8LL * o + e < K)
-                        q[8LL * o + e] = (unsigned char)(w >> (8 * (e & 3)));
-                }
-            }
-        }
-        if (n.out && here) {
-            const Octet y = pack_octet(n.out_type, f);
-            store_octet<VEC>(const_cast<char *>(at_row(n.out, p.row, n.ldo, n.out_type)), n.out_type, o, K, y);
-        }
+        value(i, w, f);
+        write_octet<VEC>(n, o, p.in && o < octets, K, p, scale8, f);
+        w = next;
+        // one after the other, so that the registers of one serve the next
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
 // A row's octets stay in registers between the sum and the norm (OCTETS = 0:
 // the row is longer than that, and read again).
-template <int OCTETS, bool VEC>
+template <int OCTETS, bool VEC, int type>
 __global__ __launch_bounds__(1024) void norm_kernel(NArgs a)
 {
-    __shared__ double shared[16];
+    __shared__ double sums[16];
+    __shared__ unsigned tops[16];
     const Place p = place_of(a.lanes, a.M);
-    const char *x = at_row(a.x, p.row, a.ldx, a.type);
+    const char *x = at_row(a.x, p.row, a.ldx, type);
     const int octets = (a.K + 7) / 8, turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
-    const auto load = [&](int i) {
-        const int o = p.t + i * a.lanes;
-        Octet v;
-        v.a = v.b = u32x4{0u, 0u, 0u, 0u};
-        if (o < octets)
-            v = load_octet<VEC>(x, a.type, o, a.K);
-        return v;
-    };
+    const auto load = [&](int i) { return own_octet<VEC>(x, type, i, a.K, a.lanes, p); };
     Octet keep[OCTETS ? OCTETS : 1];
     double sum = 0.0;
     if constexpr (OCTETS > 0) {
@@ -248,91 +302,107 @@ __global__ __launch_bounds__(1024) void norm_kernel(NArgs a)
 #pragma unroll
     for (int i = 0; i < turns; ++i) {
         float f[8];
-        unpack_octet(OCTETS ? keep[OCTETS ? i : 0] : load(i), a.type, f);
+        unpack_octet(OCTETS ? keep[OCTETS ? i : 0] : load(i), type, f);
         sum += squares(f);
     }
-    sum = row_sum(sum, a.lanes, p, shared);
-    write_norm<VEC, OCTETS>(a.n, sum, a.K, a.lanes, p, shared, [&](int i, float (&f)[8]) {
-        unpack_octet(OCTETS ? keep[OCTETS ? i : 0] : load(i), a.type, f);
+    const Octet first = own_octet<VEC>(a.n.weight, a.n.weight_type, 0, a.K, a.lanes, p);
+    sum = over_row(sum, a.lanes, p, sums);
+    write_norm<VEC, OCTETS>(a.n, sum, a.K, a.lanes, p, tops, first, [&](int i, float (&f)[8]) {
+        unpack_octet(OCTETS ? keep[OCTETS ? i : 0] : load(i), type, f);
     });
 }
 
-template <int OCTETS, bool VEC>
+template <int OCTETS, bool VEC, int y_type, int residual_type>
 __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
 {
-    __shared__ double shared[16];
+    __shared__ double sums[32];
+    __shared__ unsigned tops[16];
     const Place p = place_of(a.lanes, a.M);
-    const char *y = at_row(a.y, p.row, a.ldy, a.y_type);
-    const char *res = at_row(a.residual, p.row, a.ldr, a.residual_type);
+    const char *y = at_row(a.y, p.row, a.ldy, y_type);
+    const char *res = at_row(a.residual, p.row, a.ldr, residual_type);
     const char *gate = a.gate ? at_row(a.gate, p.row, a.ldg, a.gate_type) : nullptr;
-    char *out = const_cast<char *>(at_row(a.out, p.row, a.ldo, a.residual_type));
+    char *out = const_cast<char *>(at_row(a.out, p.row, a.ldo, residual_type));
     const int octets = (a.K + 7) / 8, turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
-    const auto load = [&](const void *row, int type, int i) {
-        const int o = p.t + i * a.lanes;
-        Octet v;
-        v.a = v.b = u32x4{0u, 0u, 0u, 0u};
-        if (o < octets)
-            v = load_octet<VEC>(row, type, o, a.K);
-        return v;
-    };
+    const auto load = [&](const void *row, int type, int i) { return own_octet<VEC>(row, type, i, a.K, a.lanes, p); };
     Octet ys[OCTETS ? OCTETS : 1], hs[OCTETS ? OCTETS : 1];
     if constexpr (OCTETS > 0) {
 #pragma unroll
         for (int i = 0; i < OCTETS; ++i) {
-            ys[i] = load(y, a.y_type, i);
-            hs[i] = load(res, a.residual_type, i);
+            ys[i] = load(y, y_type, i);
+            hs[i] = load(res, residual_type, i);
         }
     }
+    // of the weights and the gate, the first octet now and the others one ahead
+    Octet w = Octet{}, g = Octet{}, first = Octet{};
+    if (a.weight)
+        w = load(a.weight, a.weight_type, 0);
+    if (gate)
+        g = load(gate, a.gate_type, 0);
+    if (a.n.weight)
+        first = load(a.n.weight, a.n.weight_type, 0);
     float r = 1.0f;
     if (a.weight) {
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < turns; ++i) {
             float f[8];
-            unpack_octet(OCTETS ? ys[OCTETS ? i : 0] : load(y, a.y_type, i), a.y_type, f);
+            unpack_octet(OCTETS ? ys[OCTETS ? i : 0] : load(y, y_type, i), y_type, f);
             sum += squares(f);
         }
-        r = rms_factor(row_sum(sum, a.lanes, p, shared), a.K, a.eps);
+        r = rms_factor(over_row(sum, a.lanes, p, sums), a.inverse_K, a.eps);
     }
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < turns; ++i) {
         const int o = p.t + i * a.lanes;
-        float z[8], h[8];
-        unpack_octet(OCTETS ? ys[OCTETS ? i : 0] : load(y, a.y_type, i), a.y_type, z);
-        unpack_octet(OCTETS ? hs[OCTETS ? i : 0] : load(res, a.residual_type, i), a.residual_type, h);
+        Octet next_w = w, next_g = g;
+        if (i + 1 < turns) {
+            if (a.weight)
+                next_w = load(a.weight, a.weight_type, i + 1);
+            if (gate)
+                next_g = load(gate, a.gate_type, i + 1);
+        }
+        float z[8], h[8], c[8];
+        unpack_octet(OCTETS ? ys[OCTETS ? i : 0] : load(y, y_type, i), y_type, z);
+        unpack_octet(OCTETS ? hs[OCTETS ? i : 0] : load(res, residual_type, i), residual_type, h);
         if (a.weight) {
-            float w[8];
-            unpack_octet(load(a.weight, a.weight_type, i), a.weight_type, w);
+            unpack_octet(w, a.weight_type, c);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                z[e] = z[e] * r * w[e];
+                z[e] = z[e] * r * c[e];
         }
         if (gate) {
-            float g[8];
-            unpack_octet(load(gate, a.gate_type, i), a.gate_type, g);
+            unpack_octet(g, a.gate_type, c);
+            if (a.sigmoid) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    c[e] = 1.0f / (1.0f + expf(-c[e]));
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                z[e] *= a.sigmoid ? 1.0f / (1.0f + expf(-g[e])) : g[e];
+                z[e] *= c[e];
         }
         const int left = a.K - 8 * o;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             h[e] = e < left ? h[e] * a.beta + z[e] * a.alpha : 0.0f;
         // as it is held from here on
-        const Octet v = pack_octet(a.residual_type, h);
+        const Octet v = pack_octet(residual_type, h);
         if (OCTETS)
             hs[OCTETS ? i : 0] = v;
         if (p.in && o < octets)
-            store_octet<VEC>(out, a.residual_type, o, a.K, v);
+            store_octet<VEC>(out, residual_type, o, a.K, v);
         sum += squares(h);
+        w = next_w;
+        g = next_g;
+        __builtin_amdgcn_sched_barrier(0);
     }
     if (!a.n.weight)
         return;
-    sum = row_sum(sum, a.lanes, p, shared);
+    sum = over_row(sum, a.lanes, p, sums + 16);
     // without registers: what this thread has written
-    write_norm<VEC, OCTETS>(a.n, sum, a.K, a.lanes, p, shared, [&](int i, float (&f)[8]) {
-        unpack_octet(OCTETS ? hs[OCTETS ? i : 0] : load(out, a.residual_type, i), a.residual_type, f);
+    write_norm<VEC, OCTETS>(a.n, sum, a.K, a.lanes, p, tops, first, [&](int i, float (&f)[8]) {
+        unpack_octet(OCTETS ? hs[OCTETS ? i : 0] : load(out, residual_type, i), residual_type, f);
     });
 }
 
@@ -363,20 +433,51 @@ Shape shape_of(int M, int K)
     return Shape{per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 0, lanes, lanes < 256 ? 256 : lanes};
 }
 
-#define SKINNY_PICK(kernel)                                                                          \
-    const void *pick_##kernel(int octets, bool vec)                                                  \
-    {                                                                                                \
-        if (vec)                                                                                     \
-            return octets == 1   ? reinterpret_cast<const void *>(kernel<1, true>)                   \
-                   : octets == 2 ? reinterpret_cast<const void *>(kernel<2, true>)                   \
-                   : octets == 4 ? reinterpret_cast<const void *>(kernel<4, true>)                   \
-                                 : reinterpret_cast<const void *>(kernel<0, true>);                  \
-        return octets == 1 ? reinterpret_cast<const void *>(kernel<1, false>)                        \
-                           : reinterpret_cast<const void *>(kernel<0, false>);                       \
-    }
-SKINNY_PICK(norm_kernel)
-SKINNY_PICK(join_kernel)
-#undef SKINNY_PICK
+template <int X>
+const void *norm_fn(int octets, bool vec)
+{
+    if (!vec)
+        return octets == 1 ? reinterpret_cast<const void *>(norm_kernel<1, false, X>)
+                           : reinterpret_cast<const void *>(norm_kernel<0, false, X>);
+    return octets == 1   ? reinterpret_cast<const void *>(norm_kernel<1, true, X>)
+           : octets == 2 ? reinterpret_cast<const void *>(norm_kernel<2, true, X>)
+           : octets == 4 ? reinterpret_cast<const void *>(norm_kernel<4, true, X>)
+                         : reinterpret_cast<const void *>(norm_kernel<0, true, X>);
+}
+
+template <int Y, int R>
+const void *join_fn(int octets, bool vec)
+{
+    if (!vec)
+        return octets == 1 ? reinterpret_cast<const void *>(join_kernel<1, false, Y, R>)
+                           : reinterpret_cast<const void *>(join_kernel<0, false, Y, R>);
+    return octets == 1   ? reinterpret_cast<const void *>(join_kernel<1, true, Y, R>)
+           : octets == 2 ? reinterpret_cast<const void *>(join_kernel<2, true, Y, R>)
+           : octets == 4 ? reinterpret_cast<const void *>(join_kernel<4, true, Y, R>)
+                         : reinterpret_cast<const void *>(join_kernel<0, true, Y, R>);
+}
+
+const void *pick_norm_kernel(int octets, bool vec, int type)
+{
+    return type == SKINNY_TYPE_F32   ? norm_fn<SKINNY_TYPE_F32>(octets, vec)
+           : type == SKINNY_TYPE_F16 ? norm_fn<SKINNY_TYPE_F16>(octets, vec)
+                                     : norm_fn<SKINNY_TYPE_BF16>(octets, vec);
+}
+
+template <int Y>
+const void *pick_join_of(int octets, bool vec, int residual_type)
+{
+    return residual_type == SKINNY_TYPE_F32   ? join_fn<Y, SKINNY_TYPE_F32>(octets, vec)
+           : residual_type == SKINNY_TYPE_F16 ? join_fn<Y, SKINNY_TYPE_F16>(octets, vec)
+                                              : join_fn<Y, SKINNY_TYPE_BF16>(octets, vec);
+}
+
+const void *pick_join_kernel(int octets, bool vec, int y_type, int residual_type)
+{
+    return y_type == SKINNY_TYPE_F32   ? pick_join_of<SKINNY_TYPE_F32>(octets, vec, residual_type)
+           : y_type == SKINNY_TYPE_F16 ? pick_join_of<SKINNY_TYPE_F16>(octets, vec, residual_type)
+                                       : pick_join_of<SKINNY_TYPE_BF16>(octets, vec, residual_type);
+}
 
 // What both entries ask of a norm's weight and places; K and M are checked.
 skinny_status check_norm(const NormOut &n, int K)
@@ -428,7 +529,7 @@ void advance(NormOut &n, int rows)
 }
 
 NormOut norm_out(const void *weight, int weight_type, void *out, int out_type, long long ldo, int q_kind, void *q,
-                 long long ldq, void *scale, long long lds, double eps)
+                 long long ldq, void *scale, long long lds, double eps, int K)
 {
     NormOut n{};
     n.weight = weight;
@@ -442,6 +543,7 @@ NormOut norm_out(const void *weight, int weight_type, void *out, int out_type, l
     n.scale = scale;
     n.lds = lds;
     n.eps = eps;
+    n.inverse_K = 1.0 / K;
     return n;
 }
 
@@ -473,7 +575,7 @@ skinny_status skinny_norm_rows(const skinny_norm_args *p, void *stream)
         return bad(SKINNY_ERR_ALIGN, "x must be aligned to its elements");
     NArgs a{};
     a.n = norm_out(p->weight, p->weight_type, p->out, p->out_type, p->ldo, p->q_kind, p->q, p->ldq, p->scale, p->lds,
-                   p->eps);
+                   p->eps, p->K);
     const skinny_status st = check_norm(a.n, p->K);
     if (st != SKINNY_OK)
         return st;
@@ -484,7 +586,7 @@ skinny_status skinny_norm_rows(const skinny_norm_args *p, void *stream)
     a.type = p->x_type;
     a.K = p->K;
     a.lanes = s.lanes;
-    const void *fn = pick_norm_kernel(s.octets, vec);
+    const void *fn = pick_norm_kernel(s.octets, vec, a.type);
     const int most = rows_of_launch(s), per_group = s.threads / s.lanes;
     for (int left = p->M; left > 0; left -= most) {
         a.M = left < most ? left : most;
@@ -526,7 +628,7 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
     const bool next = p->next_weight != nullptr;
     if (next) {
         a.n = norm_out(p->next_weight, p->next_weight_type, p->next_out, p->next_type, p->ldn, p->q_kind, p->q, p->ldq,
-                       p->scale, p->lds, p->eps);
+                       p->scale, p->lds, p->eps, p->K);
         const skinny_status st = check_norm(a.n, p->K);
         if (st != SKINNY_OK)
             return st;
@@ -548,6 +650,7 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
     a.ldg = p->ldg;
     a.ldo = p->ldo;
     a.eps = p->eps;
+    a.inverse_K = 1.0 / p->K;
     a.alpha = p->alpha;
     a.beta = p->beta;
     a.residual_type = p->residual_type;
@@ -557,7 +660,7 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
     a.sigmoid = p->sigmoid != 0;
     a.K = p->K;
     a.lanes = s.lanes;
-    const void *fn = pick_join_kernel(s.octets, vec);
+    const void *fn = pick_join_kernel(s.octets, vec, a.y_type, a.residual_type);
     const int most = rows_of_launch(s), per_group = s.threads / s.lanes;
     for (int left = p->M; left > 0; left -= most) {
         a.M = left < most ? left : most;
