@@ -87,10 +87,15 @@ __global__ __launch_bounds__(256) void quantize_octets(BArgs a)
         unpack_octet(x[u], TYPE, f);
         if (GATE) {
             float h[8];
-            unpack_octet(g[u], TYPE, h);
+            float gate[8];
+            unpack_octet(g[u], TYPE, gate);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                f[e] *= h[e] / (1.0f + expf(-h[e]));
+                h[e] = gate[e];
+            sigmoid(h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] *= gate[e] * h[e];
         }
         unsigned byte;
         const u32x2 codes = block_codes<BITS>(f, byte);

@@ -168,66 +168,124 @@ __device__ __forceinline__ const char *at_row(const void *p, long long row, long
     return static_cast<const char *>(p) + row * ld * (type == SKINNY_TYPE_F32 ? 4 : 2);
 }
 
-// Octet i of this thread's, zero past the row: as many as it has at most lie
-// `lanes` octets apart.
-template <bool VEC>
+// How a row's elements go to its threads, eight a turn: neighbours in whole
+// 16-byte vectors; neighbours one by one (blocks at unaligned places); or lanes
+// side by side, so that a load of single elements takes whole lines (4000 x 4097
+// in FP16: FIGURE).
+enum Mode { kVectors, kElements, kStrided };
+
+// Element e of turn i.
+template <Mode MODE>
+__device__ __forceinline__ unsigned index_of(int i, int e, int lanes, const Place &p)
+{
+    // below K + 8 * 1024
+    return MODE == kStrided ? (8u * i + e) * (unsigned)lanes + p.t : 8u * (p.t + (unsigned)i * lanes) + e;
+}
+
+// This thread's eight elements of turn i, zero past the row.
+template <Mode MODE>
 __device__ __forceinline__ Octet own_octet(const void *row, int type, int i, int K, int lanes, const Place &p)
 {
-    const int o = p.t + i * lanes;
     Octet v;
     v.a = v.b = u32x4{0u, 0u, 0u, 0u};
-    if (o < (K + 7) / 8)
-        v = load_octet<VEC>(row, type, o, K);
+    if constexpr (MODE == kStrided) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const unsigned k = index_of<MODE>(i, e, lanes, p);
+            unsigned u = 0u;
+            if (k < (unsigned)K)
+                u = type == SKINNY_TYPE_F32 ? static_cast<const unsigned *>(row)[k]
+                                            : static_cast<const unsigned short *>(row)[k];
+            if (type != SKINNY_TYPE_F32)
+                v.a[e / 2] |= u << (16 * (e & 1));
+            else if (e < 4)
+                v.a[e] = u;
+            else
+                v.b[e - 4] = u;
+        }
+    } else {
+        const int o = p.t + i * lanes;
+        if (o < (K + 7) / 8)
+            v = load_octet<MODE == kVectors>(row, type, o, K);
+    }
     return v;
 }
 
-// What is written of octet o of a norm, f, which is zero past the row.
-template <bool VEC>
-__device__ __forceinline__ void write_octet(const NormOut &n, int o, bool here, int K, const Place &p,
+template <Mode MODE>
+__device__ __forceinline__ void put_octet(void *row, int type, int i, int K, int lanes, const Place &p, const Octet &v)
+{
+    if constexpr (MODE == kStrided) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const unsigned k = index_of<MODE>(i, e, lanes, p);
+            if (k >= (unsigned)K)
+                continue;
+            if (type == SKINNY_TYPE_F32)
+                static_cast<unsigned *>(row)[k] = e < 4 ? v.a[e & 3] : v.b[e & 3];
+            else
+                static_cast<unsigned short *>(row)[k] = (unsigned short)(v.a[e / 2] >> (16 * (e & 1)));
+        }
+    } else {
+        const int o = p.t + i * lanes;
+        if (o < (K + 7) / 8)
+            store_octet<MODE == kVectors>(row, type, o, K, v);
+    }
+}
+
+// What is written of a thread's eight elements f of turn i of a norm.
+template <Mode MODE>
+__device__ __forceinline__ void write_octet(const NormOut &n, int i, int K, int lanes, const Place &p,
                                             const RowScale &scale8, float (&f)[8])
 {
     if (n.q_kind == SKINNY_ROWS_MX4 || n.q_kind == SKINNY_ROWS_MX8) {
-        unsigned byte;
-        unsigned char *q = n.q + p.row * n.ldq;
-        if (n.q_kind == SKINNY_ROWS_MX4) {
-            const u32x2 codes = block_codes<4>(f, byte);
-            if (here)
-                store_codes<VEC, 4>(q, o, codes);
-        } else {
-            const u32x2 codes = block_codes<8>(f, byte);
-            if (here)
-                store_codes<VEC, 8>(q, o, codes);
+        if constexpr (MODE != kStrided) {       // whole blocks are asked for
+            const int o = p.t + i * lanes;
+            const bool here = p.in && o < K / 8;
+            unsigned byte;
+            unsigned char *q = n.q + p.row * n.ldq;
+            if (n.q_kind == SKINNY_ROWS_MX4) {
+                const u32x2 codes = block_codes<4>(f, byte);
+                if (here)
+                    store_codes<MODE == kVectors, 4>(q, o, codes);
+            } else {
+                const u32x2 codes = block_codes<8>(f, byte);
+                if (here)
+                    store_codes<MODE == kVectors, 8>(q, o, codes);
+            }
+            if (here && (o & 3) == 0)
+                static_cast<unsigned char *>(n.scale)[p.row * n.lds + (o >> 2)] = (unsigned char)byte;
         }
-        if (here && (o & 3) == 0)
-            static_cast<unsigned char *>(n.scale)[p.row * n.lds + (o >> 2)] = (unsigned char)byte;
-    } else if (n.q_kind == SKINNY_ROWS_INT8 && here) {
+    } else if (n.q_kind == SKINNY_ROWS_INT8 && p.in) {
         unsigned char *q = n.q + p.row * n.ldq;
-        u32x2 codes;
+        if constexpr (MODE == kVectors) {
+            const int o = p.t + i * lanes;
+            u32x2 codes;
 #pragma unroll
-        for (int e = 0; e < 8; e += 4)
-            codes[e / 4] = (unsigned)(to_int8(f[e], scale8) & 0xFF) | (unsigned)(to_int8(f[e + 1], scale8) & 0xFF) << 8 |
-                           (unsigned)(to_int8(f[e + 2], scale8) & 0xFF) << 16 | (unsigned)to_int8(f[e + 3], scale8) << 24;
-        if constexpr (VEC) {
-            store_codes<true, 8>(q, o, codes);
+            for (int e = 0; e < 8; e += 4)
+                codes[e / 4] = (unsigned)(to_int8(f[e], scale8) & 0xFF) | (unsigned)(to_int8(f[e + 1], scale8) & 0xFF) << 8 |
+                               (unsigned)(to_int8(f[e + 2], scale8) & 0xFF) << 16 |
+                               (unsigned)to_int8(f[e + 3], scale8) << 24;
+            if (o < K / 8)
+                store_codes<true, 8>(q, o, codes);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const unsigned w = codes[e / 4];
-                if (8LL * o + e < K)
-                    q[8LL * o + e] = (unsigned char)(w >> (8 * (e & 3)));
+                const unsigned k = index_of<MODE>(i, e, lanes, p);
+                if (k < (unsigned)K)
+                    q[k] = (unsigned char)to_int8(f[e], scale8);
             }
         }
     }
-    if (n.out && here) {
+    if (n.out && p.in) {
         const Octet y = pack_octet(n.out_type, f);
-        store_octet<VEC>(const_cast<char *>(at_row(n.out, p.row, n.ldo, n.out_type)), n.out_type, o, K, y);
+        put_octet<MODE>(const_cast<char *>(at_row(n.out, p.row, n.ldo, n.out_type)), n.out_type, i, K, lanes, p, y);
     }
 }
 
 // The norm of a row whose octets get(i, f) gives, i = 0, 1, ... for the octets
 // t + i lanes of this thread; f is zero past the row.  OCTETS: how many at most,
 // 0: any.  `first` is the weight's octet 0; the others are loaded one ahead.
-template <bool VEC, int OCTETS, typename Get>
+template <Mode MODE, int OCTETS, typename Get>
 __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, int lanes, const Place &p,
                                            unsigned *tops, const Octet &first, Get get)
 {
@@ -247,16 +305,15 @@ __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, 
     if (n.q_kind == SKINNY_ROWS_INT8) {
         unsigned top = 0;
         Octet w = first;
-#pragma unroll
+#pragma unroll OCTETS ? OCTETS : 1
         for (int i = 0; i < turns; ++i) {
-            const Octet next = i + 1 < turns ? own_octet<VEC>(n.weight, n.weight_type, i + 1, K, lanes, p) : w;
+            const Octet next = i + 1 < turns ? own_octet<MODE>(n.weight, n.weight_type, i + 1, K, lanes, p) : w;
             float f[8];
             value(i, w, f);
             // past the row the weight is zero, and r may be infinite or NaN
-            const int left = K - 8 * (p.t + i * lanes);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const unsigned m = e < left ? mag(f[e]) : 0u;
+                const unsigned m = index_of<MODE>(i, e, lanes, p) < (unsigned)K ? mag(f[e]) : 0u;
                 top = m > top ? m : top;
             }
             w = next;
@@ -268,13 +325,12 @@ __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, 
             static_cast<float *>(n.scale)[p.row] = scale;
     }
     Octet w = first;
-#pragma unroll
+#pragma unroll OCTETS ? OCTETS : 1
     for (int i = 0; i < turns; ++i) {
-        const int o = p.t + i * lanes;
-        const Octet next = i + 1 < turns ? own_octet<VEC>(n.weight, n.weight_type, i + 1, K, lanes, p) : w;
+        const Octet next = i + 1 < turns ? own_octet<MODE>(n.weight, n.weight_type, i + 1, K, lanes, p) : w;
         float f[8];
         value(i, w, f);
-        write_octet<VEC>(n, o, p.in && o < octets, K, p, scale8, f);
+        write_octet<MODE>(n, i, K, lanes, p, scale8, f);
         w = next;
         // one after the other, so that the registers of one serve the next
         __builtin_amdgcn_sched_barrier(0);
@@ -283,7 +339,7 @@ __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, 
 
 // A row's octets stay in registers between the sum and the norm (OCTETS = 0:
 // the row is longer than that, and read again).
-template <int OCTETS, bool VEC, int type>
+template <int OCTETS, Mode MODE, int type>
 __global__ __launch_bounds__(1024) void norm_kernel(NArgs a)
 {
     __shared__ double sums[16];
@@ -291,7 +347,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NArgs a)
     const Place p = place_of(a.lanes, a.M);
     const char *x = at_row(a.x, p.row, a.ldx, type);
     const int octets = (a.K + 7) / 8, turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
-    const auto load = [&](int i) { return own_octet<VEC>(x, type, i, a.K, a.lanes, p); };
+    const auto load = [&](int i) { return own_octet<MODE>(x, type, i, a.K, a.lanes, p); };
     Octet keep[OCTETS ? OCTETS : 1];
     double sum = 0.0;
     if constexpr (OCTETS > 0) {
@@ -299,20 +355,20 @@ __global__ __launch_bounds__(1024) void norm_kernel(NArgs a)
         for (int i = 0; i < OCTETS; ++i)
             keep[i] = load(i);
     }
-#pragma unroll
+#pragma unroll OCTETS ? OCTETS : 1
     for (int i = 0; i < turns; ++i) {
         float f[8];
         unpack_octet(OCTETS ? keep[OCTETS ? i : 0] : load(i), type, f);
         sum += squares(f);
     }
-    const Octet first = own_octet<VEC>(a.n.weight, a.n.weight_type, 0, a.K, a.lanes, p);
+    const Octet first = own_octet<MODE>(a.n.weight, a.n.weight_type, 0, a.K, a.lanes, p);
     sum = over_row(sum, a.lanes, p, sums);
-    write_norm<VEC, OCTETS>(a.n, sum, a.K, a.lanes, p, tops, first, [&](int i, float (&f)[8]) {
+    write_norm<MODE, OCTETS>(a.n, sum, a.K, a.lanes, p, tops, first, [&](int i, float (&f)[8]) {
         unpack_octet(OCTETS ? keep[OCTETS ? i : 0] : load(i), type, f);
     });
 }
 
-template <int OCTETS, bool VEC, int y_type, int residual_type>
+template <int OCTETS, Mode MODE, int y_type, int residual_type>
 __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
 {
     __shared__ double sums[32];
@@ -323,7 +379,7 @@ __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
     const char *gate = a.gate ? at_row(a.gate, p.row, a.ldg, a.gate_type) : nullptr;
     char *out = const_cast<char *>(at_row(a.out, p.row, a.ldo, residual_type));
     const int octets = (a.K + 7) / 8, turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
-    const auto load = [&](const void *row, int type, int i) { return own_octet<VEC>(row, type, i, a.K, a.lanes, p); };
+    const auto load = [&](const void *row, int type, int i) { return own_octet<MODE>(row, type, i, a.K, a.lanes, p); };
     Octet ys[OCTETS ? OCTETS : 1], hs[OCTETS ? OCTETS : 1];
     if constexpr (OCTETS > 0) {
 #pragma unroll
@@ -343,7 +399,7 @@ __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
     float r = 1.0f;
     if (a.weight) {
         double sum = 0.0;
-#pragma unroll
+#pragma unroll OCTETS ? OCTETS : 1
         for (int i = 0; i < turns; ++i) {
             float f[8];
             unpack_octet(OCTETS ? ys[OCTETS ? i : 0] : load(y, y_type, i), y_type, f);
@@ -352,9 +408,8 @@ __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
         r = rms_factor(over_row(sum, a.lanes, p, sums), a.inverse_K, a.eps);
     }
     double sum = 0.0;
-#pragma unroll
+#pragma unroll OCTETS ? OCTETS : 1
     for (int i = 0; i < turns; ++i) {
-        const int o = p.t + i * a.lanes;
         Octet next_w = w, next_g = g;
         if (i + 1 < turns) {
             if (a.weight)
@@ -373,25 +428,21 @@ __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
         }
         if (gate) {
             unpack_octet(g, a.gate_type, c);
-            if (a.sigmoid) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    c[e] = 1.0f / (1.0f + expf(-c[e]));
-            }
+            if (a.sigmoid)
+                sigmoid(c);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 z[e] *= c[e];
         }
-        const int left = a.K - 8 * o;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            h[e] = e < left ? h[e] * a.beta + z[e] * a.alpha : 0.0f;
+            h[e] = index_of<MODE>(i, e, a.lanes, p) < (unsigned)a.K ? h[e] * a.beta + z[e] * a.alpha : 0.0f;
         // as it is held from here on
         const Octet v = pack_octet(residual_type, h);
         if (OCTETS)
             hs[OCTETS ? i : 0] = v;
-        if (p.in && o < octets)
-            store_octet<VEC>(out, residual_type, o, a.K, v);
+        if (p.in)
+            put_octet<MODE>(out, residual_type, i, a.K, a.lanes, p, v);
         sum += squares(h);
         w = next_w;
         g = next_g;
@@ -401,9 +452,304 @@ __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
         return;
     sum = over_row(sum, a.lanes, p, sums + 16);
     // without registers: what this thread has written
-    write_norm<VEC, OCTETS>(a.n, sum, a.K, a.lanes, p, tops, first, [&](int i, float (&f)[8]) {
+    write_norm<MODE, OCTETS>(a.n, sum, a.K, a.lanes, p, tops, first, [&](int i, float (&f)[8]) {
         unpack_octet(OCTETS ? hs[OCTETS ? i : 0] : load(out, residual_type, i), residual_type, f);
     });
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: workgroups go from row to row
+// ---------------------------------------------------------------------------
+//
+// A thread has the same C octets of every row, so that their weights (and a
+// channel's gate) stay in its registers: read again for each row, from L2, they
+// cost a fifth of the time (4003 x 7168 to BF16: 29.3 against 23.5 us).  R rows go
+// together, the next R are loaded before the reduction of these.
+
+// lanes of the lower half: x of both halves, of the upper half: y of both (BIT 4: within each 32 lanes)
+template <int BIT>
+__device__ __forceinline__ void swap_halves(unsigned &x, unsigned &y)
+{
+    typedef __attribute__((ext_vector_type(2))) unsigned int pair;
+    const pair r = BIT == 4 ? __builtin_bit_cast(pair, __builtin_amdgcn_permlane16_swap(x, y, false, false))
+                            : __builtin_bit_cast(pair, __builtin_amdgcn_permlane32_swap(x, y, false, false));
+    x = r[0];
+    y = r[1];
+}
+template <int BIT>
+__device__ __forceinline__ unsigned joined(unsigned x, unsigned y)
+{
+    swap_halves<BIT>(x, y);
+    return both(x, y);
+}
+template <int BIT>
+__device__ __forceinline__ double joined(double x, double y)
+{
+    const unsigned long long u = __double_as_longlong(x), v = __double_as_longlong(y);
+    unsigned xl = (unsigned)u, yl = (unsigned)v, xh = (unsigned)(u >> 32), yh = (unsigned)(v >> 32);
+    swap_halves<BIT>(xl, yl);
+    swap_halves<BIT>(xh, yh);
+    return both(__longlong_as_double((unsigned long long)xh << 32 | xl),
+                __longlong_as_double((unsigned long long)yh << 32 | yl));
+}
+
+// The lane that has row j's result of over_rows.
+template <int R>
+__device__ __forceinline__ constexpr int lane_with(int j)
+{
+    return R == 4 ? 32 * (j & 1) + 16 * (j >> 1) : 32 * j;
+}
+
+// The sums (double) or maxima (unsigned) over the workgroup of R rows' v: in
+// lanes lane_with<R>(j) .. + 15 those of row j.  Rows share the steps: two of them
+// take half of the lanes each.  `shared` [4][16] serves every second call.
+template <int R, typename T>
+__device__ __forceinline__ T over_rows(const T (&v)[R], int waves, T (*shared)[16])
+{
+    T x;
+    if constexpr (R == 4)
+        x = joined<4>(joined<5>(v[0], v[1]), joined<5>(v[2], v[3]));
+    else if constexpr (R == 2)
+        x = joined<5>(v[0], v[1]);
+    else
+        x = joined<5>(v[0], v[0]);
+    if constexpr (R < 4)
+        x = joined<4>(x, x);
+    const auto within16 = [](T y) {
+        y = both(y, lane_of<0xB1>(y));
+        y = both(y, lane_of<0x4E>(y));
+        y = both(y, lane_of<0x141>(y));
+        return both(y, lane_of<0x140>(y));
+    };
+    x = within16(x);
+    if (waves > 1) {
+        const int lane = threadIdx.x & 63;
+        if ((lane & 15) == 0)
+            shared[lane >> 4][threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = within16((lane & 15) < waves ? shared[lane >> 4][lane & 15] : T(0));
+    }
+    return x;
+}
+
+__device__ __forceinline__ float from_lane(float v, int lane)
+{
+    return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
+// Octet i of this thread's in a row, zero past its end or without a row.
+template <int TYPE>
+__device__ __forceinline__ Octet octet_of(const void *base, long long row, long long ld, int type, bool in, int o)
+{
+    Octet v;
+    v.a = v.b = u32x4{0u, 0u, 0u, 0u};
+    if (in)
+        v = load_octet<true>(at_row(base, row, ld, type), type, o, 0);
+    return v;
+}
+
+// The norms of R rows from `first` on, of which f gives octet i of row j.
+template <int C, int R, typename Get>
+__device__ __forceinline__ void write_norms(const NormOut &n, const double (&squares_of)[R], const float (&w)[C][8],
+                                            int octets, int K, long long first, int M, int waves,
+                                            double (*sums)[16], unsigned (*tops)[16], Get get)
+{
+    const float rl = rms_factor(over_rows<R>(squares_of, waves, sums), n.inverse_K, n.eps);
+    float r[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        r[j] = from_lane(rl, lane_with<R>(j));
+    RowScale scale8[R];
+    if (n.q_kind == SKINNY_ROWS_INT8) {
+        unsigned top[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            top[j] = 0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                float f[8];
+                get(j, i, f);
+                const bool here = (int)threadIdx.x + i * (int)blockDim.x < octets;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const unsigned m = here ? mag(f[e] * r[j] * w[i][e]) : 0u;
+                    top[j] = m > top[j] ? m : top[j];
+                }
+            }
+        }
+        const unsigned all = over_rows<R>(top, waves, tops);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            float scale;
+            scale8[j] = row_scale((unsigned)__builtin_amdgcn_readlane((int)all, lane_with<R>(j)), scale);
+            if (threadIdx.x == 0 && first + j < M)
+                static_cast<float *>(n.scale)[first + j] = scale;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            float f[8];
+            get(j, i, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = f[e] * r[j] * w[i][e];
+            Place p;
+            p.row = (int)(first + j);
+            p.t = (int)threadIdx.x;
+            p.in = first + j < M;
+            write_octet<kVectors>(n, i, K, (int)blockDim.x, p, scale8[j], f);
+            // one after the other, so that the registers of one serve the next
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
+template <int C, int R, int type>
+__global__ __launch_bounds__(1024) void norm_stream(NArgs a)
+{
+    __shared__ double sums[2][4][16];
+    __shared__ unsigned tops[2][4][16];
+    const int octets = a.K / 8, waves = (int)blockDim.x / 64;
+    float w[C][8];
+    const auto load = [&](Octet (&x)[R][C], long long first) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int o = (int)threadIdx.x + i * (int)blockDim.x;
+                x[j][i] = octet_of<type>(a.x, first + j, a.ldx, type, o < octets && first + j < a.M, o);
+            }
+    };
+    long long first = (long long)blockIdx.x * R;
+    const long long stride = (long long)gridDim.x * R;
+    Octet x[R][C], next[R][C];
+    load(x, first);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int o = (int)threadIdx.x + i * (int)blockDim.x;
+        unpack_octet(octet_of<type>(a.n.weight, 0, 0, a.n.weight_type, o < octets, o), a.n.weight_type, w[i]);
+    }
+    for (int turn = 0; first < a.M; first += stride, turn ^= 1) {
+        load(next, first + stride);
+        double sum[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            sum[j] = 0.0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                float f[8];
+                unpack_octet(x[j][i], type, f);
+                sum[j] += squares(f);
+            }
+        }
+        write_norms<C, R>(a.n, sum, w, octets, a.K, first, a.M, waves, sums[turn], tops[turn],
+                          [&](int j, int i, float (&f)[8]) { unpack_octet(x[j][i], type, f); });
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                x[j][i] = next[j][i];
+    }
+}
+
+template <int C, int R, int y_type, int residual_type>
+__global__ __launch_bounds__(1024) void join_stream(JArgs a)
+{
+    __shared__ double sums[4][4][16];
+    __shared__ unsigned tops[2][4][16];
+    const int octets = a.K / 8, waves = (int)blockDim.x / 64;
+    long long first = (long long)blockIdx.x * R;
+    const long long stride = (long long)gridDim.x * R;
+    Octet ys[R][C], hs[R][C], next_y[R][C], next_h[R][C];
+    const auto load = [&](Octet (&y)[R][C], Octet (&h)[R][C], long long from) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int o = (int)threadIdx.x + i * (int)blockDim.x;
+                const bool in = o < octets && from + j < a.M;
+                y[j][i] = octet_of<y_type>(a.y, from + j, a.ldy, y_type, in, o);
+                h[j][i] = octet_of<y_type>(a.residual, from + j, a.ldr, residual_type, in, o);
+            }
+    };
+    load(ys, hs, first);
+    float w[C][8], c[C][8], nw[C][8];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int o = (int)threadIdx.x + i * (int)blockDim.x;
+        const bool in = o < octets;
+        unpack_octet(octet_of<y_type>(a.weight, 0, 0, a.weight_type, in && a.weight, o), a.weight_type, w[i]);
+        unpack_octet(octet_of<y_type>(a.n.weight, 0, 0, a.n.weight_type, in && a.n.weight, o), a.n.weight_type, nw[i]);
+        unpack_octet(octet_of<y_type>(a.gate, 0, 0, a.gate_type, in && a.gate, o), a.gate_type, c[i]);
+        if (a.sigmoid)
+            sigmoid(c[i]);
+    }
+    for (int turn = 0; first < a.M; first += stride, turn ^= 1) {
+        load(next_y, next_h, first + stride);
+        float r[R];
+        double sum[R];
+        if (a.weight) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                sum[j] = 0.0;
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    float f[8];
+                    unpack_octet(ys[j][i], y_type, f);
+                    sum[j] += squares(f);
+                }
+            }
+            const float rl = rms_factor(over_rows<R>(sum, waves, sums[turn]), a.inverse_K, a.eps);
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                r[j] = from_lane(rl, lane_with<R>(j));
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            sum[j] = 0.0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int o = (int)threadIdx.x + i * (int)blockDim.x;
+                float z[8], h[8];
+                unpack_octet(ys[j][i], y_type, z);
+                unpack_octet(hs[j][i], residual_type, h);
+                if (a.weight) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        z[e] = z[e] * r[j] * w[i][e];
+                }
+                if (a.gate) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        z[e] *= c[i][e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[e] = h[e] * a.beta + z[e] * a.alpha;
+                // as it is held from here on
+                const Octet v = pack_octet(residual_type, h);
+                hs[j][i] = v;
+                const bool here = o < octets && first + j < a.M;
+                if (here) {
+                    store_octet<true>(const_cast<char *>(at_row(a.out, first + j, a.ldo, residual_type)), residual_type,
+                                      o, 0, v);
+                    sum[j] += squares(h);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (a.n.weight)
+            write_norms<C, R>(a.n, sum, nw, octets, a.K, first, a.M, waves, sums[2 + turn], tops[turn],
+                              [&](int j, int i, float (&f)[8]) { unpack_octet(hs[j][i], residual_type, f); });
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                ys[j][i] = next_y[j][i];
+                hs[j][i] = next_h[j][i];
+            }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -416,16 +762,22 @@ bool whole_octets(const void *p, long long ld, int type)
     return (uintptr_t)p % 16 == 0 && ld * type_bytes(type) % 16 == 0;
 }
 
+Mode mode_of(bool vec, int q_kind)
+{
+    return vec ? kVectors : q_kind == SKINNY_ROWS_MX4 || q_kind == SKINNY_ROWS_MX8 ? kElements : kStrided;
+}
+
 // Octets a thread keeps and threads a row.
 struct Shape {
     int octets, lanes, threads;
 };
 
-Shape shape_of(int M, int K)
+Shape shape_of(int M, int K, Mode mode)
 {
     const int octets = (K + 7) / 8;
-    // few rows: one octet a thread; many: up to four, so that a workgroup has more loads under way
-    const int each = M <= 512 ? 1 : 4;
+    // few rows: one octet a thread; many: up to four, so that a workgroup has more
+    // loads under way (single elements have eight times the loads anyway)
+    const int each = M <= 512 || mode != kVectors ? 1 : 4;
     int lanes = 16;
     while (lanes < 1024 && lanes * each < octets)
         lanes *= 2;
@@ -433,50 +785,115 @@ Shape shape_of(int M, int K)
     return Shape{per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 0, lanes, lanes < 256 ? 256 : lanes};
 }
 
-template <int X>
-const void *norm_fn(int octets, bool vec)
+// Rows at a time of the kernels for many rows, by what their registers hold.
+template <int C, int X>
+constexpr int kNormRows = C > 1 ? 1 : X == SKINNY_TYPE_F32 ? 2 : 4;
+// One of fp32 rows; two of others (4000 x 7168 in BF16 50.0 against 54.5 us).
+constexpr int join_rows_of(int y_type, int residual_type)
 {
-    if (!vec)
-        return octets == 1 ? reinterpret_cast<const void *>(norm_kernel<1, false, X>)
-                           : reinterpret_cast<const void *>(norm_kernel<0, false, X>);
-    return octets == 1   ? reinterpret_cast<const void *>(norm_kernel<1, true, X>)
-           : octets == 2 ? reinterpret_cast<const void *>(norm_kernel<2, true, X>)
-           : octets == 4 ? reinterpret_cast<const void *>(norm_kernel<4, true, X>)
-                         : reinterpret_cast<const void *>(norm_kernel<0, true, X>);
+    return y_type == SKINNY_TYPE_F32 || residual_type == SKINNY_TYPE_F32 ? 1 : 2;
+}
+
+template <int X>
+const void *norm_stream_fn(int c)
+{
+    return c == 1   ? reinterpret_cast<const void *>(norm_stream<1, kNormRows<1, X>, X>)
+           : c == 2 ? reinterpret_cast<const void *>(norm_stream<2, kNormRows<2, X>, X>)
+                    : reinterpret_cast<const void *>(norm_stream<3, kNormRows<3, X>, X>);
 }
 
 template <int Y, int R>
-const void *join_fn(int octets, bool vec)
+const void *join_stream_fn()
 {
-    if (!vec)
-        return octets == 1 ? reinterpret_cast<const void *>(join_kernel<1, false, Y, R>)
-                           : reinterpret_cast<const void *>(join_kernel<0, false, Y, R>);
-    return octets == 1   ? reinterpret_cast<const void *>(join_kernel<1, true, Y, R>)
-           : octets == 2 ? reinterpret_cast<const void *>(join_kernel<2, true, Y, R>)
-           : octets == 4 ? reinterpret_cast<const void *>(join_kernel<4, true, Y, R>)
-                         : reinterpret_cast<const void *>(join_kernel<0, true, Y, R>);
+    return reinterpret_cast<const void *>(join_stream<1, join_rows_of(Y, R), Y, R>);
 }
 
-const void *pick_norm_kernel(int octets, bool vec, int type)
+constexpr int kMany = 1024;
+
+// Octets a thread, threads a row and workgroups of the kernels for many rows; c = 0: not for these.
+struct Stream {
+    int c, threads, groups;
+};
+
+Stream stream_of(int M, int K, bool vec, int most, int rows)
 {
-    return type == SKINNY_TYPE_F32   ? norm_fn<SKINNY_TYPE_F32>(octets, vec)
-           : type == SKINNY_TYPE_F16 ? norm_fn<SKINNY_TYPE_F16>(octets, vec)
-                                     : norm_fn<SKINNY_TYPE_BF16>(octets, vec);
+    const int octets = K / 8, c = (octets + 1023) / 1024;
+    // shorter rows go several to a wave; fewer rows than the chip takes at once, one by one
+    if (!vec || octets <= 32 || c > most || M < kMany)
+        return Stream{0, 0, 0};
+    const int threads = ((octets + c - 1) / c + 63) / 64 * 64;
+    // as many as the chip has places for: 16 waves a CU
+    const int places = 256 * (1024 / threads), batches = (int)(((long long)M + rows - 1) / rows);
+    return Stream{c, threads, batches < places ? batches : places};
+}
+
+template <int X>
+const void *norm_fn(int octets, Mode mode)
+{
+    if (mode == kElements)
+        return octets == 1 ? reinterpret_cast<const void *>(norm_kernel<1, kElements, X>)
+                           : reinterpret_cast<const void *>(norm_kernel<0, kElements, X>);
+    if (mode == kStrided)
+        return octets == 1   ? reinterpret_cast<const void *>(norm_kernel<1, kStrided, X>)
+               : octets == 2 ? reinterpret_cast<const void *>(norm_kernel<2, kStrided, X>)
+                             : reinterpret_cast<const void *>(norm_kernel<0, kStrided, X>);
+    return octets == 1   ? reinterpret_cast<const void *>(norm_kernel<1, kVectors, X>)
+           : octets == 2 ? reinterpret_cast<const void *>(norm_kernel<2, kVectors, X>)
+           : octets == 4 ? reinterpret_cast<const void *>(norm_kernel<4, kVectors, X>)
+                         : reinterpret_cast<const void *>(norm_kernel<0, kVectors, X>);
+}
+
+template <int Y, int R>
+const void *join_fn(int octets, Mode mode)
+{
+    if (mode == kElements)
+        return octets == 1 ? reinterpret_cast<const void *>(join_kernel<1, kElements, Y, R>)
+                           : reinterpret_cast<const void *>(join_kernel<0, kElements, Y, R>);
+    if (mode == kStrided)
+        return octets == 1   ? reinterpret_cast<const void *>(join_kernel<1, kStrided, Y, R>)
+               : octets == 2 ? reinterpret_cast<const void *>(join_kernel<2, kStrided, Y, R>)
+                             : reinterpret_cast<const void *>(join_kernel<0, kStrided, Y, R>);
+    return octets == 1   ? reinterpret_cast<const void *>(join_kernel<1, kVectors, Y, R>)
+           : octets == 2 ? reinterpret_cast<const void *>(join_kernel<2, kVectors, Y, R>)
+           : octets == 4 ? reinterpret_cast<const void *>(join_kernel<4, kVectors, Y, R>)
+                         : reinterpret_cast<const void *>(join_kernel<0, kVectors, Y, R>);
+}
+
+const void *pick_norm_kernel(int octets, Mode mode, int type)
+{
+    return type == SKINNY_TYPE_F32   ? norm_fn<SKINNY_TYPE_F32>(octets, mode)
+           : type == SKINNY_TYPE_F16 ? norm_fn<SKINNY_TYPE_F16>(octets, mode)
+                                     : norm_fn<SKINNY_TYPE_BF16>(octets, mode);
 }
 
 template <int Y>
-const void *pick_join_of(int octets, bool vec, int residual_type)
+const void *pick_join_of(int octets, Mode mode, int residual_type)
 {
-    return residual_type == SKINNY_TYPE_F32   ? join_fn<Y, SKINNY_TYPE_F32>(octets, vec)
-           : residual_type == SKINNY_TYPE_F16 ? join_fn<Y, SKINNY_TYPE_F16>(octets, vec)
-                                              : join_fn<Y, SKINNY_TYPE_BF16>(octets, vec);
+    return residual_type == SKINNY_TYPE_F32   ? join_fn<Y, SKINNY_TYPE_F32>(octets, mode)
+           : residual_type == SKINNY_TYPE_F16 ? join_fn<Y, SKINNY_TYPE_F16>(octets, mode)
+                                              : join_fn<Y, SKINNY_TYPE_BF16>(octets, mode);
 }
 
-const void *pick_join_kernel(int octets, bool vec, int y_type, int residual_type)
+const void *pick_join_kernel(int octets, Mode mode, int y_type, int residual_type)
 {
-    return y_type == SKINNY_TYPE_F32   ? pick_join_of<SKINNY_TYPE_F32>(octets, vec, residual_type)
-           : y_type == SKINNY_TYPE_F16 ? pick_join_of<SKINNY_TYPE_F16>(octets, vec, residual_type)
-                                       : pick_join_of<SKINNY_TYPE_BF16>(octets, vec, residual_type);
+    return y_type == SKINNY_TYPE_F32   ? pick_join_of<SKINNY_TYPE_F32>(octets, mode, residual_type)
+           : y_type == SKINNY_TYPE_F16 ? pick_join_of<SKINNY_TYPE_F16>(octets, mode, residual_type)
+                                       : pick_join_of<SKINNY_TYPE_BF16>(octets, mode, residual_type);
+}
+
+template <int Y>
+const void *join_stream_of(int residual_type)
+{
+    return residual_type == SKINNY_TYPE_F32   ? join_stream_fn<Y, SKINNY_TYPE_F32>()
+           : residual_type == SKINNY_TYPE_F16 ? join_stream_fn<Y, SKINNY_TYPE_F16>()
+                                              : join_stream_fn<Y, SKINNY_TYPE_BF16>();
+}
+
+const void *pick_join_stream(int y_type, int residual_type)
+{
+    return y_type == SKINNY_TYPE_F32   ? join_stream_of<SKINNY_TYPE_F32>(residual_type)
+           : y_type == SKINNY_TYPE_F16 ? join_stream_of<SKINNY_TYPE_F16>(residual_type)
+                                       : join_stream_of<SKINNY_TYPE_BF16>(residual_type);
 }
 
 // What both entries ask of a norm's weight and places; K and M are checked.
@@ -579,14 +996,26 @@ skinny_status skinny_norm_rows(const skinny_norm_args *p, void *stream)
     const skinny_status st = check_norm(a.n, p->K);
     if (st != SKINNY_OK)
         return st;
-    const Shape s = shape_of(p->M, p->K);
     const bool vec = p->K % 8 == 0 && whole_octets(p->x, p->ldx, p->x_type) && norm_octets(a.n);
     a.x = p->x;
     a.ldx = p->ldx;
     a.type = p->x_type;
     a.K = p->K;
+    const Stream stream_shape = stream_of(p->M, p->K, vec, 3, p->K > 8192 ? 1 : a.type == SKINNY_TYPE_F32 ? 2 : 4);
+    if (stream_shape.c) {
+        a.M = p->M;
+        const void *many = a.type == SKINNY_TYPE_F32   ? norm_stream_fn<SKINNY_TYPE_F32>(stream_shape.c)
+                           : a.type == SKINNY_TYPE_F16 ? norm_stream_fn<SKINNY_TYPE_F16>(stream_shape.c)
+                                                       : norm_stream_fn<SKINNY_TYPE_BF16>(stream_shape.c);
+        void *params[] = {&a};
+        const hipError_t e = hipLaunchKernel(many, dim3((unsigned)stream_shape.groups),
+                                             dim3((unsigned)stream_shape.threads), params, 0, (hipStream_t)stream);
+        return e == hipSuccess ? SKINNY_OK : hip_bad(e, "norm launch");
+    }
+    const Mode mode = mode_of(vec, a.n.q_kind);
+    const Shape s = shape_of(p->M, p->K, mode);
     a.lanes = s.lanes;
-    const void *fn = pick_norm_kernel(s.octets, vec, a.type);
+    const void *fn = pick_norm_kernel(s.octets, mode, a.type);
     const int most = rows_of_launch(s), per_group = s.threads / s.lanes;
     for (int left = p->M; left > 0; left -= most) {
         a.M = left < most ? left : most;
@@ -635,7 +1064,6 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
     } else if (p->next_out || p->q_kind != SKINNY_ROWS_NONE) {
         return bad(SKINNY_ERR_INVALID_ARG, "a place for the next norm without its weight");
     }
-    const Shape s = shape_of(p->M, p->K);
     const bool vec = p->K % 8 == 0 && whole_octets(p->residual, p->ldr, p->residual_type) &&
                      whole_octets(p->y, p->ldy, p->y_type) && whole_octets(p->out, p->ldo, p->residual_type) &&
                      (!p->gate || whole_octets(p->gate, p->ldg, p->gate_type)) &&
@@ -659,8 +1087,21 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
     a.gate_type = p->gate_type;
     a.sigmoid = p->sigmoid != 0;
     a.K = p->K;
+    // a gate for each token fills the registers: row by row (4000 x 7168 66 against 70 us)
+    const Stream stream_shape = stream_of(p->M, p->K, vec && !(p->gate && p->ldg != 0), 1,
+                                          join_rows_of(p->y_type, p->residual_type));
+    if (stream_shape.c) {
+        a.M = p->M;
+        void *params[] = {&a};
+        const hipError_t e = hipLaunchKernel(pick_join_stream(a.y_type, a.residual_type),
+                                             dim3((unsigned)stream_shape.groups), dim3((unsigned)stream_shape.threads),
+                                             params, 0, (hipStream_t)stream);
+        return e == hipSuccess ? SKINNY_OK : hip_bad(e, "join launch");
+    }
+    const Mode mode = mode_of(vec, a.n.q_kind);
+    const Shape s = shape_of(p->M, p->K, mode);
     a.lanes = s.lanes;
-    const void *fn = pick_join_kernel(s.octets, vec, a.y_type, a.residual_type);
+    const void *fn = pick_join_kernel(s.octets, mode, a.y_type, a.residual_type);
     const int most = rows_of_launch(s), per_group = s.threads / s.lanes;
     for (int left = p->M; left > 0; left -= most) {
         a.M = left < most ? left : most;
