@@ -171,7 +171,7 @@ __device__ __forceinline__ const char *at_row(const void *p, long long row, long
 // How a row's elements go to its threads, eight a turn: neighbours in whole
 // 16-byte vectors; neighbours one by one (blocks at unaligned places); or lanes
 // side by side, so that a load of single elements takes whole lines (4000 x 4097
-// in FP16: FIGURE).
+// in FP16: 34.7 against 57 us).
 enum Mode { kVectors, kElements, kStrided };
 
 // Element e of turn i.
@@ -785,21 +785,23 @@ Shape shape_of(int M, int K, Mode mode)
     return Shape{per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 0, lanes, lanes < 256 ? 256 : lanes};
 }
 
-// Rows at a time of the kernels for many rows, by what their registers hold.
-template <int C, int X>
-constexpr int kNormRows = C > 1 ? 1 : X == SKINNY_TYPE_F32 ? 2 : 4;
+// The norm's kernel for many rows: one row at a time, or four of 16-bit values
+// in up to 1024 octets.
+template <int X>
+const void *norm_stream_fn(int c, int rows)
+{
+    if constexpr (X != SKINNY_TYPE_F32)
+        if (rows == 4)
+            return reinterpret_cast<const void *>(norm_stream<1, 4, X>);
+    return c == 1   ? reinterpret_cast<const void *>(norm_stream<1, 1, X>)
+           : c == 2 ? reinterpret_cast<const void *>(norm_stream<2, 1, X>)
+                    : reinterpret_cast<const void *>(norm_stream<3, 1, X>);
+}
+
 // One of fp32 rows; two of others (4000 x 7168 in BF16 50.0 against 54.5 us).
 constexpr int join_rows_of(int y_type, int residual_type)
 {
     return y_type == SKINNY_TYPE_F32 || residual_type == SKINNY_TYPE_F32 ? 1 : 2;
-}
-
-template <int X>
-const void *norm_stream_fn(int c)
-{
-    return c == 1   ? reinterpret_cast<const void *>(norm_stream<1, kNormRows<1, X>, X>)
-           : c == 2 ? reinterpret_cast<const void *>(norm_stream<2, kNormRows<2, X>, X>)
-                    : reinterpret_cast<const void *>(norm_stream<3, kNormRows<3, X>, X>);
 }
 
 template <int Y, int R>
@@ -808,23 +810,50 @@ const void *join_stream_fn()
     return reinterpret_cast<const void *>(join_stream<1, join_rows_of(Y, R), Y, R>);
 }
 
-constexpr int kMany = 1024;
-
-// Octets a thread, threads a row and workgroups of the kernels for many rows; c = 0: not for these.
+// Octets a thread, threads a row, rows at a time and workgroups of the kernels for
+// many rows; c = 0: not for these.
 struct Stream {
-    int c, threads, groups;
+    int c, threads, rows, groups;
 };
 
-Stream stream_of(int M, int K, bool vec, int most, int rows)
+// `most` octets a thread at most, `waves` of a CU.
+Stream stream_of(int M, int K, bool vec, int most, int rows, int waves)
 {
     const int octets = K / 8, c = (octets + 1023) / 1024;
-    // shorter rows go several to a wave; fewer rows than the chip takes at once, one by one
-    if (!vec || octets <= 32 || c > most || M < kMany)
-        return Stream{0, 0, 0};
+    // shorter rows go several to a wave
+    if (!vec || octets <= 32 || c > most)
+        return Stream{0, 0, 0, 0};
     const int threads = ((octets + c - 1) / c + 63) / 64 * 64;
-    // as many as the chip has places for: 16 waves a CU
-    const int places = 256 * (1024 / threads), batches = (int)(((long long)M + rows - 1) / rows);
-    return Stream{c, threads, batches < places ? batches : places};
+    const int places = 256 * (64 * waves / threads), batches = (int)(((long long)M + rows - 1) / rows);
+    return Stream{c, threads, rows, batches < places ? batches : places};
+}
+
+// From 256 rows on; four at a time where they fill the chip's turns to within a
+// twentieth (4003 x 7168 with fp32 weights: 34.5 against 36.3 us one at a time on
+// twice the workgroups; 2500: 23.6 against 21.5; row by row 37.7 and 21.6).
+Stream norm_stream_of(int M, int K, int type, bool vec)
+{
+    if (M < 256)
+        return Stream{0, 0, 0, 0};
+    if (K > 8192)
+        return stream_of(M, K, vec, 3, 1, 16);
+    const Stream four = stream_of(M, K, vec, 1, 4, 16);
+    if (four.c && type != SKINNY_TYPE_F32) {
+        const long long turn = 4LL * 256 * (1024 / four.threads), whole = (M + turn - 1) / turn * turn;
+        if (M >= 3 * turn && 20 * whole <= 21LL * M)
+            return four;
+    }
+    return stream_of(M, K, vec, 1, 1, 32);
+}
+
+// From 1024 rows on (600 x 7168: 14.9 us against 12.7 row by row, 1500: 20.3
+// against 22.0), but not with a gate for each token, which fills the registers
+// (4000 x 7168: 70 against 66 us).
+Stream join_stream_of(int M, int K, int y_type, int residual_type, bool vec, bool token_gate)
+{
+    if (M < 1024 || token_gate)
+        return Stream{0, 0, 0, 0};
+    return stream_of(M, K, vec, 1, join_rows_of(y_type, residual_type), 16);
 }
 
 template <int X>
@@ -882,7 +911,7 @@ const void *pick_join_kernel(int octets, Mode mode, int y_type, int residual_typ
 }
 
 template <int Y>
-const void *join_stream_of(int residual_type)
+const void *join_stream_type(int residual_type)
 {
     return residual_type == SKINNY_TYPE_F32   ? join_stream_fn<Y, SKINNY_TYPE_F32>()
            : residual_type == SKINNY_TYPE_F16 ? join_stream_fn<Y, SKINNY_TYPE_F16>()
@@ -891,9 +920,9 @@ const void *join_stream_of(int residual_type)
 
 const void *pick_join_stream(int y_type, int residual_type)
 {
-    return y_type == SKINNY_TYPE_F32   ? join_stream_of<SKINNY_TYPE_F32>(residual_type)
-           : y_type == SKINNY_TYPE_F16 ? join_stream_of<SKINNY_TYPE_F16>(residual_type)
-                                       : join_stream_of<SKINNY_TYPE_BF16>(residual_type);
+    return y_type == SKINNY_TYPE_F32   ? join_stream_type<SKINNY_TYPE_F32>(residual_type)
+           : y_type == SKINNY_TYPE_F16 ? join_stream_type<SKINNY_TYPE_F16>(residual_type)
+                                       : join_stream_type<SKINNY_TYPE_BF16>(residual_type);
 }
 
 // What both entries ask of a norm's weight and places; K and M are checked.
@@ -1001,12 +1030,12 @@ skinny_status skinny_norm_rows(const skinny_norm_args *p, void *stream)
     a.ldx = p->ldx;
     a.type = p->x_type;
     a.K = p->K;
-    const Stream stream_shape = stream_of(p->M, p->K, vec, 3, p->K > 8192 ? 1 : a.type == SKINNY_TYPE_F32 ? 2 : 4);
+    const Stream stream_shape = norm_stream_of(p->M, p->K, a.type, vec);
     if (stream_shape.c) {
         a.M = p->M;
-        const void *many = a.type == SKINNY_TYPE_F32   ? norm_stream_fn<SKINNY_TYPE_F32>(stream_shape.c)
-                           : a.type == SKINNY_TYPE_F16 ? norm_stream_fn<SKINNY_TYPE_F16>(stream_shape.c)
-                                                       : norm_stream_fn<SKINNY_TYPE_BF16>(stream_shape.c);
+        const void *many = a.type == SKINNY_TYPE_F32   ? norm_stream_fn<SKINNY_TYPE_F32>(stream_shape.c, stream_shape.rows)
+                           : a.type == SKINNY_TYPE_F16 ? norm_stream_fn<SKINNY_TYPE_F16>(stream_shape.c, stream_shape.rows)
+                                                       : norm_stream_fn<SKINNY_TYPE_BF16>(stream_shape.c, stream_shape.rows);
         void *params[] = {&a};
         const hipError_t e = hipLaunchKernel(many, dim3((unsigned)stream_shape.groups),
                                              dim3((unsigned)stream_shape.threads), params, 0, (hipStream_t)stream);
@@ -1087,9 +1116,7 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
     a.gate_type = p->gate_type;
     a.sigmoid = p->sigmoid != 0;
     a.K = p->K;
-    // a gate for each token fills the registers: row by row (4000 x 7168 66 against 70 us)
-    const Stream stream_shape = stream_of(p->M, p->K, vec && !(p->gate && p->ldg != 0), 1,
-                                          join_rows_of(p->y_type, p->residual_type));
+    const Stream stream_shape = join_stream_of(p->M, p->K, p->y_type, p->residual_type, vec, p->gate && p->ldg != 0);
     if (stream_shape.c) {
         a.M = p->M;
         void *params[] = {&a};

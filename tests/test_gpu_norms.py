@@ -202,6 +202,51 @@ def test_norm_quantized_into_pitched_places(op, q, off):
     assert bool((wide[:, :off] == 0x55).all()) and bool((wide[:, off + width:] == 0x55).all())
 
 
+STREAMS = [(255, 520), (256, 520), (257, 1536), (300, 8192), (1023, 7168), (1025, 512), (3072, 7168), (3073, 7168),
+           (4003, 4096), (5000, 264), (300, 8200), (260, 16384), (259, 24576), (256, 24584), (2100, 1544)]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("m,k", STREAMS)
+def test_norm_many_rows(op, kind, m, k):
+    """Around the sizes at which rows go otherwise: from workgroup to workgroup, four at a time, one octet to three a
+    thread."""
+    x, w = rows(m, k, kind, m + k), weights(k, list(TYPES)[m % 3], k)
+    out = torch.full((m + 1, k), 3.0, dtype=TYPES[kind], device="cuda")
+    n = torch.empty(m, k, device="cuda")
+    got = quantized_places("int8", m, k)
+    op.norm_rows(x, w, out=out)
+    op.norm_rows(x, w, out=n, q=got[0], scale=got[1])
+    want = exact_norm(x, w)
+    close(out[:m], want, 3 * H * want.abs(), TYPES[kind])
+    close(n, want, 3 * H * want.abs(), torch.float32)
+    assert bool((out[m] == 3).all())
+    same_rows(got, quantized("int8", n))
+    if k % 32 == 0:
+        for q in ("mx4", "mx8"):
+            got = quantized_places(q, m, k)
+            op.norm_rows(x, w, q=got[0], scale=got[1])
+            same_rows(got, quantized(q, n))
+
+
+def test_norm_many_rows_that_go_wrong(op):
+    """A row of NaN, infinity, zeros, the largest and the smallest values among others that are not touched by it."""
+    m, k = 4100, 1024
+    x = rows(m, k, "bf16", 1)
+    x[7], x[1030, 5], x[2050, 9], x[4099, 3] = 0, math.nan, math.inf, -math.inf
+    x[8], x[9] = torch.finfo(torch.bfloat16).max, 2.0 ** -133
+    w = weights(k, "f32", 1)
+    want = exact_norm(x, w)
+    for q in ("int8", "mx4", "mx8"):
+        n = torch.empty(m, k, device="cuda")
+        got = quantized_places(q, m, k)
+        op.norm_rows(x, w, out=n, q=got[0], scale=got[1])
+        assert torch.equal(n.isnan(), want.isnan())
+        fine = torch.isfinite(want)
+        close(n[fine], want[fine], 3 * H * want[fine].abs(), torch.float32)
+        same_rows(got, quantized(q, n))
+
+
 def test_no_rows(op):
     x, w = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda")
     op.norm_rows(x, w, out=torch.empty(0, 64, device="cuda"))
@@ -246,8 +291,34 @@ def test_join_sizes(op, m, k, weight, gate, sigmoid):
     assert bool((out[m] == 3).all()) and bool((nxt[m] == 4).all())
 
 
+@pytest.mark.parametrize("gate,sigmoid", [(None, False), ("channel", True), ("token", True)])
+@pytest.mark.parametrize("weight", [None, "bf16"])
+@pytest.mark.parametrize("rk", TYPES)
+@pytest.mark.parametrize("m,k", [(1023, 520), (1024, 520), (1025, 7168), (2600, 264), (1500, 8192), (1030, 8200)])
+def test_join_many_rows(op, m, k, rk, weight, gate, sigmoid):
+    yk = ["bf16", "f32", "f16"][(m + k) % 3]
+    res, y = rows(m, k, rk, 1, 0.5), rows(m, k, yk, 2, 0.5)
+    w = None if weight is None else weights(k, weight, 1)
+    g = {None: None, "channel": weights(k, "f16", 4), "token": rows(m, k, "bf16", 3, 0.1)}[gate]
+    nw = weights(k, "f32", 6)
+    out = torch.full((m + 1, k), 3.0, dtype=TYPES[rk], device="cuda")
+    nxt, n = torch.full((m + 1, k), 4.0, dtype=torch.float16, device="cuda"), torch.empty(m, k, device="cuda")
+    op.join_rows(res, y, out, weight=w, gate=g, sigmoid=sigmoid, alpha=0.375, beta=1.25, next_weight=nw, next_out=nxt)
+    h, tol = exact_join(res, y, w, g, sigmoid, 0.375, 1.25)
+    close(out[:m], h, tol + H * h.abs(), TYPES[rk])
+    want = exact_norm(out[:m], nw)
+    close(nxt[:m], want, 3 * H * want.abs(), torch.float16)
+    assert bool((out[m] == 3).all()) and bool((nxt[m] == 4).all())
+    got = quantized_places("int8", m, k)
+    again = res.clone()
+    op.join_rows(again, y, again, weight=w, gate=g, sigmoid=sigmoid, alpha=0.375, beta=1.25, next_weight=nw, next_out=n,
+                 q=got[0], scale=got[1])
+    assert torch.equal(again, out[:m])
+    same_rows(got, quantized("int8", n))
+
+
 @pytest.mark.parametrize("q", ["int8", "mx4", "mx8"])
-@pytest.mark.parametrize("m,k", [(1, 32), (4, 7168), (2, 40960), (700, 544)])
+@pytest.mark.parametrize("m,k", [(1, 32), (4, 7168), (2, 40960), (700, 544), (1100, 2048)])
 @pytest.mark.parametrize("rk", TYPES)
 def test_join_next_is_norm_rows_of_what_is_held(op, rk, m, k, q):
     res, y = rows(m, k, rk, 1, 0.5), rows(m, k, "bf16", 2, 0.5)
