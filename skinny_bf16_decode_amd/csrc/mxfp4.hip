@@ -471,12 +471,19 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
             xf[d][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_off[t] + xo, 0, 0);
         const unsigned so = (unsigned)(kUnitBlocks * u);
         if (a.words) {
-            const bool both = kUnitBlocks * u + 4 < a.blocks;
+            if (kUnitBlocks * u + 4 < a.blocks) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(xsr, xs_off[t] + so, 0, 0);
-                xs[d][0][t] = v[0];
-                xs[d][1][t] = both ? v[1] : 0u;
+                for (int t = 0; t < MT; ++t) {
+                    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(xsr, xs_off[t] + so, 0, 0);
+                    xs[d][0][t] = v[0];
+                    xs[d][1][t] = v[1];
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    xs[d][0][t] = __builtin_amdgcn_raw_buffer_load_b32(xsr, xs_off[t] + so, 0, 0);
+                    xs[d][1][t] = 0u;
+                }
             }
         } else {
             const int b = kUnitBlocks * u + g;

@@ -274,6 +274,54 @@ def test_product_sizes(op, m, n, k, bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("m", [1, 6, 13, 20, 50, 90, 400, 1100])
+@pytest.mark.parametrize("n,k", [(1536, 128), (50, 384), (4000, 640), (300, 1152), (260, 2176)])
+def test_product_half_units(op, m, n, k, bits):
+    """Whole dwords of powers that end in the middle of a unit of 256."""
+    run_case(op, m, n, k, bits, "f32", False, m + k)
+
+
+@pytest.mark.parametrize("m", [2, 40, 200])
+@pytest.mark.parametrize("xb,wb", [(7, 127), (1, 140), (0, 160), (10, 120), (127, 3), (140, 0), (236, 60), (60, 240),
+                                   (240, 20)])
+def test_product_powers_at_their_ends(op, m, xb, wb):
+    """Values at the ends of what a power can hold: 8-bit ones above 2^-126, the smallest normal, are exact, and 4-bit
+    ones at any power (their products are left to fp32's range)."""
+    n, k = 70, 256
+    g = torch.Generator().manual_seed(m)
+    for bits in (4, 8):
+        xc, _ = exact_codes(g, m, k, bits)
+        wc, _ = exact_codes(g, n, k, 4)
+        xs, ws = torch.full((m, k // 32), xb, dtype=torch.uint8), torch.full((n, k // 32), wb, dtype=torch.uint8)
+        plan = op.PreparedMxfp4(*on_gpu(wc, ws, 4), out_dtype=torch.float32)
+        got = torch.empty(m, n, device="cuda")
+        plan.run(*on_gpu(xc, xs, bits), got)
+        y, _ = reference(xc, xs, wc, ws, bits)
+        if bits == 8 and min(xb, wb) < 2:
+            continue                                    # values below BF16's normal range
+        got = got.cpu().numpy().astype(np.float64)
+        assert (np.abs(got - y) <= 2.0 ** -149).all(), (bits, np.abs(got - y).max(), np.abs(y).max())
+
+
+def test_four_bit_type(op):
+    """torch's own type of two 4-bit values a byte."""
+    g = torch.Generator().manual_seed(4)
+    x, w = torch.randn(5, 256, generator=g).cuda(), torch.randn(48, 256, generator=g).cuda()
+    made = []
+    for t in (torch.uint8, torch.float4_e2m1fn_x2):
+        xq, xs = places(5, 256, 4)
+        wq, ws = places(48, 256, 4)
+        xs, ws = (xs, ws) if t == torch.uint8 else (xs.view(torch.float8_e8m0fnu), ws.view(torch.float8_e8m0fnu))
+        op.quantize_blocks(x, xq.view(t), xs)
+        op.quantize_blocks(w, wq.view(t), ws)
+        out = torch.empty(5, 48, device="cuda")
+        op.PreparedMxfp4(wq.view(t), ws, out_dtype=torch.float32).run(xq.view(t), xs, out)
+        made.append((xq, raw(xs), out, op.expand_blocks(xq.view(t), xs, torch.empty(5, 256, device="cuda"))))
+    assert torch.equal(made[0][0], made[1][0]) and np.array_equal(made[0][1], made[1][1])
+    assert torch.equal(made[0][2], made[1][2]) and torch.equal(made[0][3], made[1][3])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("m", [3, 40, 300])
 @pytest.mark.parametrize("k", [160, 288, 1024])
 @pytest.mark.parametrize("off", [1, 2, 3, 4])
