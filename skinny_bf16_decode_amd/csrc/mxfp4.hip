@@ -315,12 +315,21 @@ __device__ __forceinline__ bf16x8 bf16_of_8(unsigned lo, unsigned hi, float powe
                                    0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// The 16-byte chunk of a row's unit (8 of them in 4 bits, 16 in 8) that is part
-// `part` of lane group g's operand at step s: block 4 s + g.
+// Where a row's 16-byte chunks lie in LDS, before the row's own order (^ row % 8):
+// part `part` of lane group g's operand at step s, block 4 s + g, at 4 s + g in 4
+// bits and at 8 s + 4 part + g in 8, so that the four lane groups read side by
+// side (2 part + g there: bank conflicts in a tenth of the cycles).
 template <int BITS>
-__device__ __forceinline__ int chunk_of(int g, int s, int part)
+__device__ __forceinline__ int place_in_row(int g, int s, int part)
 {
-    return BITS / 4 * (4 * s + g) + part;
+    return BITS == 4 ? 4 * s + g : 8 * s + 4 * part + g;
+}
+
+// The same of chunk c in memory.
+template <int BITS>
+__device__ __forceinline__ int place_of_chunk(int c)
+{
+    return BITS == 4 ? c : (c & 8) + 4 * (c & 1) + (c >> 1 & 3);
 }
 
 // A buffer load whose offset is past its resource reads zero and touches no
@@ -495,8 +504,7 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
                         xsr, xs_off[t] + (b + 4 * k < a.blocks ? so + 4u * k : kSkip), 0, 0);
         }
     };
-    // 16-byte chunk c of row r lies at c ^ (r % 8): written a row at a time and
-    // read a column at a time without bank conflicts
+    // written a row at a time and read a column at a time without bank conflicts
     u32x4 *mine = shared + wave * kTile;
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -518,14 +526,14 @@ __global__ __launch_bounds__(512) void product_rows(PArgs a)
 #pragma unroll
                 for (int j = 0; j < kLoads; ++j) {
                     const int row = kRows * j + sub;
-                    mine[row * kPerRow + (slot ^ (row & 7))] = xf[d][t * kLoads + j];
+                    mine[row * kPerRow + (place_of_chunk<BITS>(slot) ^ (row & 7))] = xf[d][t * kLoads + j];
                 }
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int p = 0; p < BITS / 4; ++p)
-                        x[k][t].v[p] = mine[(lane & 15) * kPerRow + (chunk_of<BITS>(g, k, p) ^ (lane & 7))];
+                        x[k][t].v[p] = mine[(lane & 15) * kPerRow + (place_in_row<BITS>(g, k, p) ^ (lane & 7))];
                 __builtin_amdgcn_wave_barrier();
             }
             multiply<RT, MT, BITS>(acc, wf[d], x, ws[d], xp);
@@ -818,7 +826,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
     for (int j = 0; j < 2; ++j)
         w_off[j] = (unsigned)((2 * wave + j) * a.units) * 2048u + 16u * lane;
     ws_off = (unsigned)(wave * a.units) * 256u + 4u * lane;
-    const int chunk = (lane & 7) ^ (lane >> 3);         // of a row's 128 bytes, at c ^ (r % 8)
+    const int at = (lane & 7) ^ (lane >> 3), chunk = 2 * (at & 3) + (at >> 2);  // of a row's 128 bytes: as place_of_chunk
 #pragma unroll
     for (int j = 0; j < L::kXCopies; ++j) {
         const int row = 8 * (wave + 8 * j) + (lane >> 3);
@@ -830,9 +838,9 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
         xs_off = row < rows ? (unsigned)(row * a.ldxs) + xs_block : kSkip;
     } else {
         const int row = 16 * wave + (lane >> 2);
-        const unsigned at = shift + (unsigned)(row * a.ldxs), word = lane & 3;
-        xs_off = row < rows && word < 3 ? (at & ~3u) + 4u * word : kSkip;
-        xs_block = 4u * word > (at & 3u) ? 4u * word - (at & 3u) : 0u;
+        const unsigned from = shift + (unsigned)(row * a.ldxs), word = lane & 3;
+        xs_off = row < rows && word < 3 ? (from & ~3u) + 4u * word : kSkip;
+        xs_block = 4u * word > (from & 3u) ? 4u * word - (from & 3u) : 0u;
     }
     const int steps = 2 * a.units;
     const auto copy_xs = [&](int unit, int place) __attribute__((always_inline)) {
@@ -881,7 +889,7 @@ __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
     // Half h (16 values of its block for each lane) of token tile t.
     const auto read_x = [&](int t, int buf, int h) __attribute__((always_inline)) {
         xf[h][t] =
-            (ring + buf * L::kVecs + L::kX + T0 * half * 128 + 8 * (lane & 15) + ((2 * g + h) ^ (lane & 7)))[t * 128];
+            (ring + buf * L::kVecs + L::kX + T0 * half * 128 + 8 * (lane & 15) + (place_in_row<8>(g, 0, h) ^ (lane & 7)))[t * 128];
     };
     copy_xs(0, 0);
 #pragma unroll
