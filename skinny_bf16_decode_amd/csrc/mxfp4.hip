@@ -57,7 +57,11 @@ __device__ __forceinline__ unsigned quotient(unsigned x, const FastDiv &f)
     return (t + ((x - t) >> f.s1)) >> f.s2;
 }
 
-// Eight values a thread, four threads a block, U times 256 threads a workgroup.
+// Eight values a thread, four threads a block, U times 256 threads a workgroup; no
+// barrier and no LDS: the largest of a block goes around its four lanes.  Rows one
+// after the other are taken as one.  Bound by bytes: 6001 x 7168 in BF16 to 4
+// bits 23.3 us, 4.7 TB/s, to 8 bits 26.6; 1000 x 18432 gated, in FP16 to 8 bits,
+// 18.6 us, 5.0 TB/s; 4 rows 1.9 us.
 template <int TYPE, int BITS, bool GATE, bool VEC, int U>
 __global__ __launch_bounds__(256) void quantize_octets(BArgs a)
 {
@@ -114,6 +118,8 @@ struct XArgs {
     FastDiv by_row;
 };
 
+// Eight values a thread.  Bound by bytes: 6001 x 7168 from 4 bits to BF16 26 us alone
+// (4.2 TB/s), 17.8 where the codes were just written and lie in the caches.
 template <int BITS, bool VEC>
 __global__ __launch_bounds__(256) void expand_octets(XArgs a)
 {
@@ -293,8 +299,9 @@ __device__ __forceinline__ f32x4 mma128(u32x4 w, u32x4 x, f32x4 c, unsigned ws, 
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widened(w), widened(x), c, 4, 4, WB, (int)ws, 0, (int)xs);
 }
 
-// Eight values times their power in BF16, which holds a code of either type
-// times any power that a block may have (8-bit values below 2^-133 apart).
+// Eight values times their power in BF16, which holds a code of 4 bits with powers
+// of 2^-125 to 2^125 and one of 8 with 2^-117 to 2^119: all that a block of normal
+// values gets.
 __device__ __forceinline__ bf16x8 bf16_of_4(unsigned w, float power)
 {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 0);
@@ -318,7 +325,7 @@ __device__ __forceinline__ bf16x8 bf16_of_8(unsigned lo, unsigned hi, float powe
 // Where a row's 16-byte chunks lie in LDS, before the row's own order (^ row % 8):
 // part `part` of lane group g's operand at step s, block 4 s + g, at 4 s + g in 4
 // bits and at 8 s + 4 part + g in 8, so that the four lane groups read side by
-// side (2 part + g there: bank conflicts in a tenth of the cycles).
+// side (memory's order has bank conflicts in a thirteenth of the cycles).
 template <int BITS>
 __device__ __forceinline__ int place_in_row(int g, int s, int part)
 {
@@ -406,8 +413,16 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[RT][MT], const u32x4 (&w)[
 // 16 RT weight rows by 16 MT tokens a workgroup, its eight waves taking every
 // eighth unit of 256 k: each holds all sums of the tile, which are added at the
 // end through LDS in a fixed order.  Loads go into registers, D units ahead.  x
-// is read in whole lines and passes through the wave's own LDS on its way into
-// operands, a token tile at a time.
+// is read in whole lines, XR rows of a tile (the tokens that there are), and passes
+// through the wave's own LDS on its way into operands, a token tile at a time.
+// Bound by the loads' way from memory: with none of x 6288 x 7168 takes one token
+// 6.0 us of 6.3, 7168 x 18432 64 tokens 14.3 of 17.1.  One token of 6288 x 7168 takes
+// 6.2 us in 4 bits and 6.5 in 8 (24 MB at 3.8 TB/s, with a launch's 2 us), of 7168 x
+// 18432 12.5 us (5.6 TB/s).  Units past the last are not loaded, which made 8.5 us
+// of 6.9; four units ahead cost as much again.  NT: the weight passes by once (a
+// single token tile) and need not stay in the caches: with more weights than these
+// hold 6.2 against 6.6 us for one token, 8.4 against 8.9 for 16; where a few weights
+// are read again and again it is up to 1.3 us slower (2048 x 7168).
 template <int RT, int MT, int BITS, int D, int XR, bool NT>
 __global__ __launch_bounds__(512) void product_rows(PArgs a)
 {
@@ -613,6 +628,15 @@ struct TilesLayout {
 // products.  WORDS: rows of x's powers are whole aligned dwords, two a row and
 // unit; otherwise the three aligned dwords around them are copied (each holds a
 // byte of the row, so that none lies outside its memory's page).
+//
+// 4000 x 6288 x 7168: 100 to 105 us, 3.4 to 3.6 PFLOP/s (a library product of 4096 x
+// 6400 x 7168 149 us); 8192 x 8192 x 8192 295 us, 3.7 PFLOP/s.  Bound by the matrix units,
+// which are busy for half of the time, and what a step of theirs waits for: of the
+// 1650 cycles of a step of 256 tokens, 1024 are products and 320 the barrier.  The
+// units alone, on random data, reach 7.5 PFLOP/s at the clock that they leave.
+// Copies and reads all at the start of a step: 5 % slower.  Steps of 256 k in two
+// stages: the same.  Four waves of 128 rows: 40 % slower (sums go back and forth
+// between register files); two workgroups of 128 rows a CU: 16 % slower.
 template <int T0, bool WORDS>
 __global__ __launch_bounds__(512, 2) void product_tiles(PArgs a)
 {
@@ -797,7 +821,12 @@ struct Tiles8Layout {
 
 // Many 8-bit tokens: product_tiles' workgroup, with both operands converted to
 // BF16 on their way from LDS to the matrix units (see multiply): a wave's w once for
-// its 16 T0 tokens, x once for its 64 rows.
+// its 16 T0 tokens, x once for its 64 rows.  1501 x 6288 x 7168: 107 to 112 us, 1.2 to
+// 1.26 PFLOP/s (BF16 units alone: 1.97 on random data, a library product in BF16
+// 1.48).  The matrix units are busy for 60 % of the time; a step's conversions, some
+// 150 a wave, run beside the other wave's products but for its first ones.  With
+// two barriers a step and operands read in it 124 us; waves of other priorities: no
+// change, or 10 % slower.
 template <int T0, bool WORDS>
 __global__ __launch_bounds__(512, 2) void product_tiles8(PArgs a)
 {
@@ -1086,6 +1115,10 @@ struct Tiling {
     float us;
 };
 
+// product_tiles and product_tiles8: a round on the scale of rows_tiling, 8-bit
+// tokens' a fifth below what it takes alone.  Over 512 to 6288 rows, 65 to 2000 tokens
+// and K = 1536 to 18432 the kernel taken was within a geometric mean of 0.1 % (4
+// bits) and 0.8 % (8 bits) of the fastest, at worst 2 and 10 %.
 Tiling tiles_tiling(int M, int N, int bits, bool words)
 {
     static const float us4[9] = {0.0f, 22.0f, 23.5f, 27.0f, 30.4f, 35.5f, 39.3f, 43.5f, 47.6f};
@@ -1122,6 +1155,8 @@ Tiling rows_tiling(int M, int N, int bits)
     return best;
 }
 
+// Up to 64 tokens product_rows, above the shorter of both: 400 tokens of 6288 x 7168
+// 27.7 against 23.6 us in 4 bits, of 1536 x 7168 12.1 against 21.2.
 hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
 {
     constexpr unsigned kThreads = 512;
@@ -1241,7 +1276,7 @@ skinny_status skinny_quantize_blocks(const void *x, skinny_type type, int M, int
         // rows one after the other are one long row
         a.per_row = whole ? a.octets : (unsigned)per_row;
         a.by_row = make_fastdiv(a.per_row);
-        // several octets a thread once they fill the chip's threads all the same
+        // several octets a thread once they fill the chip's threads all the same: more loads under way
         const bool many = a.octets >= 1u << 20;
         const unsigned per_group = 256u * (!vec || !many ? 1u : gate ? 2u : 4u);
         const void *fn = bits == 4 ? quantize_kernel_of<4>((int)type, gate != nullptr, vec, many)
