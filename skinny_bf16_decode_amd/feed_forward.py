@@ -65,9 +65,9 @@ class FeedForward:
         self.gate_up.run(*entered, rows)
         y = torch.empty(tokens, self.hidden, dtype=torch.bfloat16, device=h.device)
         self.down.run(*self._quantized(rows[:, self.inner:], self.bits, gate=rows[:, :self.inner]), y)
-        if following is None:
+        if following is None or following.eps != self.eps:      # join_rows has one eps for both its norms
             join_rows(h, y, h, weight=self.post_weight, alpha=self.alpha, eps=self.eps)
-            return None
+            return None if following is None else following.enter(h)
         q, scale = token_places(tokens, self.hidden, following.bits, h.device)
         join_rows(h, y, h, weight=self.post_weight, alpha=self.alpha, next_weight=following.norm_weight, q=q,
                   scale=scale, eps=self.eps)

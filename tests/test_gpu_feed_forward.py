@@ -173,3 +173,20 @@ def test_refusals(ff):
 def test_command(ff, capsys):
     ff.main()
     assert capsys.readouterr().out.count(" us") == 2
+
+
+@pytest.mark.parametrize("post", [True, False])
+def test_blocks_of_unlike_eps(ff, post):
+    """Each block's norms have that block's eps: run together the same bits as
+    entered one by one, from rows so small that eps is most of what they are
+    divided by (squares of 2^-20 next to eps 2^-14 and 2^-24: a factor above 4)."""
+    blocks = [b for b, _ in make(ff, 8, post)]
+    blocks[0].eps, blocks[1].eps = 2.0 ** -14, 2.0 ** -24
+    h = (stream_of(5, 3) * 2.0 ** -10).bfloat16()
+    want = h.clone()
+    for b in blocks:
+        b.run(want, b.enter(want))
+    got = ff.run_blocks(blocks, h.clone())
+    assert torch.equal(got, want)
+    blocks[1].eps = blocks[0].eps               # the border between the blocks sees the difference
+    assert not torch.equal(ff.run_blocks(blocks, h.clone()), want)
