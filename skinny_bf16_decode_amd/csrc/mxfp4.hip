@@ -419,7 +419,9 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[RT][MT], const u32x4 (&w)[
 // 6.0 us of 6.3, 7168 x 18432 64 tokens 14.3 of 17.1.  One token of 6288 x 7168 takes
 // 6.2 us in 4 bits and 6.5 in 8 (24 MB at 3.8 TB/s, with a launch's 2 us), of 7168 x
 // 18432 12.5 us (5.6 TB/s).  Units past the last are not loaded, which made 8.5 us
-// of 6.9; four units ahead cost as much again.  NT: the weight passes by once (a
+// of 6.9; four units ahead cost as much again, two with more tokens up to a quarter
+// (64 x 6288 x 7168 in 8 bits 12.2 against 13.1 us, at 64 rows by 16 tokens 13.8 against
+// 16.8), and so does x asked for before the products and w after them.  NT: the weight passes by once (a
 // single token tile) and need not stay in the caches: with more weights than these
 // hold 6.2 against 6.6 us for one token, 8.4 against 8.9 for 16; where a few weights
 // are read again and again it is up to 1.3 us slower (2048 x 7168).
@@ -1136,13 +1138,14 @@ Tiling tiles_tiling(int M, int N, int bits, bool words)
 // product_rows: what each further workgroup of a CU adds, measured at K = 7168
 // over 1024 to 14336 rows and 1 to 128 tokens (both grow with K alike).  16 x 32
 // tiles and those of 48 and 64 tokens were never the fastest (64 x 6288 x 7168:
-// 64 rows by 32 tokens 8.8 us, by 64 14.8).
+// 64 rows by 32 tokens 8.8 us, by 64 14.8).  32 rows by 32 8-bit tokens take as many rounds
+// as 64 by 16 and are a little ahead: 37 x 3584 x 7168 9.0 against 9.2 us.
 Tiling rows_tiling(int M, int N, int bits)
 {
     static const struct {
         int r, t;
         float us4, us8;
-    } kTiles[] = {{1, 1, 1.65f, 2.45f}, {2, 1, 2.05f, 3.2f}, {4, 1, 3.4f, 5.2f}, {2, 2, 3.2f, 5.3f}, {4, 2, 4.6f, 9.7f}};
+    } kTiles[] = {{1, 1, 1.65f, 2.45f}, {2, 1, 2.05f, 3.2f}, {4, 1, 3.4f, 5.35f}, {2, 2, 3.2f, 5.2f}, {4, 2, 4.6f, 9.7f}};
     Tiling best{0, 0, 0.0f};
     for (const auto &k : kTiles) {
         if (k.t == 2 && M <= 16)
