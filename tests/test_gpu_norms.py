@@ -202,7 +202,7 @@ def test_norm_quantized_into_pitched_places(op, q, off):
     assert bool((wide[:, :off] == 0x55).all()) and bool((wide[:, off + width:] == 0x55).all())
 
 
-STREAMS = [(255, 520), (256, 520), (257, 1536), (300, 8192), (1023, 7168), (1025, 512), (3072, 7168), (3073, 7168),
+STREAMS = [(255, 520), (256, 520), (257, 1536), (300, 8192), (1023, 7168), (1025, 512), (4096, 7168), (3073, 7168),
            (4003, 4096), (5000, 264), (300, 8200), (260, 16384), (259, 24576), (256, 24584), (2100, 1544)]
 
 
