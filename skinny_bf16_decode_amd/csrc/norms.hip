@@ -11,6 +11,7 @@
 // last place of r would carry a 4-bit value to the next one.
 #include <hip/hip_runtime.h>
 
+#include "norm_shape.h"
 #include "operators.h"
 #include "rows.h"
 #include "skinny_internal.h"
@@ -168,12 +169,6 @@ __device__ __forceinline__ const char *at_row(const void *p, long long row, long
     return static_cast<const char *>(p) + row * ld * (type == SKINNY_TYPE_F32 ? 4 : 2);
 }
 
-// How a row's elements go to its threads, eight a turn: neighbours in whole
-// 16-byte vectors; neighbours one by one (blocks at unaligned places); or lanes
-// side by side, so that a load of single elements takes whole lines (4000 x 4097
-// in FP16: 34.7 against 57 us).
-enum Mode { kVectors, kElements, kStrided };
-
 // Element e of turn i.
 template <Mode MODE>
 __device__ __forceinline__ unsigned index_of(int i, int e, int lanes, const Place &p)
@@ -205,7 +200,7 @@ __device__ __forceinline__ Octet own_octet(const void *row, int type, int i, int
         }
     } else {
         const int o = p.t + i * lanes;
-        if (o < (K + 7) / 8)
+        if (o < octets_of(K))
             v = load_octet<MODE == kVectors>(row, type, o, K);
     }
     return v;
@@ -227,7 +222,7 @@ __device__ __forceinline__ void put_octet(void *row, int type, int i, int K, int
         }
     } else {
         const int o = p.t + i * lanes;
-        if (o < (K + 7) / 8)
+        if (o < octets_of(K))
             store_octet<MODE == kVectors>(row, type, o, K, v);
     }
 }
@@ -289,7 +284,7 @@ template <Mode MODE, int OCTETS, typename Get>
 __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, int lanes, const Place &p,
                                            unsigned *tops, const Octet &first, Get get)
 {
-    const int octets = (K + 7) / 8, turns = OCTETS ? OCTETS : (octets + lanes - 1) / lanes;
+    const int octets = octets_of(K), turns = OCTETS ? OCTETS : (octets + lanes - 1) / lanes;
     const float r = rms_factor(sum, n.inverse_K, n.eps);
     const auto value = [&](int i, const Octet &raw, float (&f)[8]) {
         get(i, f);
@@ -347,7 +342,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NArgs a)
     __shared__ unsigned tops[16];
     const Place p = place_of(a.lanes, a.M);
     const char *x = at_row(a.x, p.row, a.ldx, type);
-    const int octets = (a.K + 7) / 8, turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
+    const int octets = octets_of(a.K), turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
     const auto load = [&](int i) { return own_octet<MODE>(x, type, i, a.K, a.lanes, p); };
     Octet keep[OCTETS ? OCTETS : 1];
     double sum = 0.0;
@@ -381,7 +376,7 @@ __global__ __launch_bounds__(1024) void join_kernel(JArgs a)
     const char *res = at_row(a.residual, p.row, a.ldr, residual_type);
     const char *gate = a.gate ? at_row(a.gate, p.row, a.ldg, a.gate_type) : nullptr;
     char *out = const_cast<char *>(at_row(a.out, p.row, a.ldo, residual_type));
-    const int octets = (a.K + 7) / 8, turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
+    const int octets = octets_of(a.K), turns = OCTETS ? OCTETS : (octets + a.lanes - 1) / a.lanes;
     const auto load = [&](const void *row, int type, int i) { return own_octet<MODE>(row, type, i, a.K, a.lanes, p); };
     Octet ys[OCTETS ? OCTETS : 1], hs[OCTETS ? OCTETS : 1];
     if constexpr (OCTETS > 0) {
@@ -767,29 +762,6 @@ bool whole_octets(const void *p, long long ld, int type)
     return (uintptr_t)p % 16 == 0 && ld * type_bytes(type) % 16 == 0;
 }
 
-Mode mode_of(bool vec, int q_kind)
-{
-    return vec ? kVectors : q_kind == SKINNY_ROWS_MX4 || q_kind == SKINNY_ROWS_MX8 ? kElements : kStrided;
-}
-
-// Octets a thread keeps and threads a row.
-struct Shape {
-    int octets, lanes, threads;
-};
-
-Shape shape_of(int M, int K, Mode mode)
-{
-    const int octets = (K + 7) / 8;
-    // few rows: one octet a thread; many: up to four, so that a workgroup has more
-    // loads under way (single elements have eight times the loads anyway)
-    const int each = M <= 512 || mode != kVectors ? 1 : 4;
-    int lanes = 16;
-    while (lanes < 1024 && lanes * each < octets)
-        lanes *= 2;
-    const int per = (octets + lanes - 1) / lanes;
-    return Shape{per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 0, lanes, lanes < 256 ? 256 : lanes};
-}
-
 // The norm's kernel for many rows: one row at a time, or four of 16-bit values
 // in up to 1024 octets.
 template <int X>
@@ -803,62 +775,10 @@ const void *norm_stream_fn(int c, int rows)
                     : reinterpret_cast<const void *>(norm_stream<3, 1, X>);
 }
 
-// One of fp32 rows; two of others (4000 x 7168 in BF16 50.0 against 54.5 us).
-constexpr int join_rows_of(int y_type, int residual_type)
-{
-    return y_type == SKINNY_TYPE_F32 || residual_type == SKINNY_TYPE_F32 ? 1 : 2;
-}
-
 template <int Y, int R>
 const void *join_stream_fn()
 {
     return reinterpret_cast<const void *>(join_stream<1, join_rows_of(Y, R), Y, R>);
-}
-
-// Octets a thread, threads a row, rows at a time and workgroups of the kernels for
-// many rows; c = 0: not for these.
-struct Stream {
-    int c, threads, rows, groups;
-};
-
-// `most` octets a thread at most, `waves` of a CU.
-Stream stream_of(int M, int K, bool vec, int most, int rows, int waves)
-{
-    const int octets = K / 8, c = (octets + 1023) / 1024;
-    // shorter rows go several to a wave
-    if (!vec || octets <= 32 || c > most)
-        return Stream{0, 0, 0, 0};
-    const int threads = ((octets + c - 1) / c + 63) / 64 * 64;
-    const int places = 256 * (64 * waves / threads), batches = (int)(((long long)M + rows - 1) / rows);
-    return Stream{c, threads, rows, batches < places ? batches : places};
-}
-
-// From 256 rows on; four at a time where they fill the chip's turns to within a
-// twentieth (4003 x 7168 with fp32 weights: 34.5 against 36.3 us one at a time on
-// twice the workgroups; 2500: 23.6 against 21.5; row by row 37.7 and 21.6).
-Stream norm_stream_of(int M, int K, int type, bool vec)
-{
-    if (M < 256)
-        return Stream{0, 0, 0, 0};
-    if (K > 8192)
-        return stream_of(M, K, vec, 3, 1, 16);
-    const Stream four = stream_of(M, K, vec, 1, 4, 16);
-    if (four.c && type != SKINNY_TYPE_F32) {
-        const long long turn = 4LL * 256 * (1024 / four.threads), whole = (M + turn - 1) / turn * turn;
-        if (M >= 3 * turn && 20 * whole <= 21LL * M)
-            return four;
-    }
-    return stream_of(M, K, vec, 1, 1, 32);
-}
-
-// From 1024 rows on (600 x 7168: 14.9 us against 12.7 row by row, 1500: 20.3
-// against 22.0), but not with a gate for each token, which fills the registers
-// (4000 x 7168: 70 against 66 us).
-Stream join_stream_of(int M, int K, int y_type, int residual_type, bool vec, bool token_gate)
-{
-    if (M < 1024 || token_gate)
-        return Stream{0, 0, 0, 0};
-    return stream_of(M, K, vec, 1, join_rows_of(y_type, residual_type), 16);
 }
 
 template <int X>
@@ -998,9 +918,6 @@ NormOut norm_out(const void *weight, int weight_type, void *out, int out_type, l
     return n;
 }
 
-// Rows of a launch of fewer than 2^32 threads.
-int rows_of_launch(const Shape &s) { return (int)(0xFFFFFFFFu / (unsigned)s.threads - 1u) * (s.threads / s.lanes); }
-
 }  // namespace
 }  // namespace skinny
 
@@ -1035,7 +952,7 @@ skinny_status skinny_norm_rows(const skinny_norm_args *p, void *stream)
     a.ldx = p->ldx;
     a.type = p->x_type;
     a.K = p->K;
-    const Stream stream_shape = norm_stream_of(p->M, p->K, a.type, vec);
+    const RowStream stream_shape = norm_stream_of(p->M, p->K, a.type, vec);
     if (stream_shape.c) {
         a.M = p->M;
         const void *many = a.type == SKINNY_TYPE_F32   ? norm_stream_fn<SKINNY_TYPE_F32>(stream_shape.c, stream_shape.rows)
@@ -1047,7 +964,7 @@ skinny_status skinny_norm_rows(const skinny_norm_args *p, void *stream)
         return e == hipSuccess ? SKINNY_OK : hip_bad(e, "norm launch");
     }
     const Mode mode = mode_of(vec, a.n.q_kind);
-    const Shape s = shape_of(p->M, p->K, mode);
+    const RowShape s = row_shape_of(p->M, p->K, mode);
     a.lanes = s.lanes;
     const void *fn = pick_norm_kernel(s.octets, mode, a.type);
     const int most = rows_of_launch(s), per_group = s.threads / s.lanes;
@@ -1121,7 +1038,7 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
     a.gate_type = p->gate_type;
     a.sigmoid = p->sigmoid != 0;
     a.K = p->K;
-    const Stream stream_shape = join_stream_of(p->M, p->K, p->y_type, p->residual_type, vec, p->gate && p->ldg != 0);
+    const RowStream stream_shape = join_stream_of(p->M, p->K, p->y_type, p->residual_type, vec, p->gate && p->ldg != 0);
     if (stream_shape.c) {
         a.M = p->M;
         void *params[] = {&a};
@@ -1131,7 +1048,7 @@ skinny_status skinny_join_rows(const skinny_join_args *p, void *stream)
         return e == hipSuccess ? SKINNY_OK : hip_bad(e, "join launch");
     }
     const Mode mode = mode_of(vec, a.n.q_kind);
-    const Shape s = shape_of(p->M, p->K, mode);
+    const RowShape s = row_shape_of(p->M, p->K, mode);
     a.lanes = s.lanes;
     const void *fn = pick_join_kernel(s.octets, mode, a.y_type, a.residual_type);
     const int most = rows_of_launch(s), per_group = s.threads / s.lanes;
