@@ -119,17 +119,18 @@ __global__ __launch_bounds__(1024) void quantize_vector(QArgs a)
     }
 }
 
-// Any K, pitch and alignment, an element at a time.
+// Any K, pitch and alignment, an element at a time.  An index past the longest
+// rows' end does not fit 31 bits.
 template <int TYPE>
 __global__ __launch_bounds__(256) void quantize_element(QArgs a)
 {
     using E = Elem<TYPE>;
     __shared__ unsigned tops[4];
-    const int tid = threadIdx.x;
+    const unsigned tid = threadIdx.x, K = (unsigned)a.K;
     const typename E::raw *x = static_cast<const typename E::raw *>(a.x) + blockIdx.x * a.ldx;
     signed char *q = a.q + blockIdx.x * a.ldq;
     unsigned top = 0;
-    for (int i = tid; i < a.K; i += 256) {
+    for (unsigned i = tid; i < K; i += 256) {
         const unsigned m = mag(E::get(x[i]));
         top = m > top ? m : top;
     }
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(256) void quantize_element(QArgs a)
     const RowScale r = row_scale(top, scale);
     if (tid == 0)
         a.scale[blockIdx.x] = scale;
-    for (int i = tid; i < a.K; i += 256)
+    for (unsigned i = tid; i < K; i += 256)
         q[i] = (signed char)to_int8(E::get(x[i]), r);
 }
 
