@@ -12,6 +12,7 @@
 
 #include <new>
 
+#include "mxfp4_tiles.h"
 #include "operators.h"
 #include "rows.h"
 #include "skinny_internal.h"
@@ -1056,27 +1057,24 @@ const void *rows_fn()
     return reinterpret_cast<const void *>(product_rows<RT, MT, BITS, BITS == 8 && XR == 4 && RT <= 2 ? 2 : 1, XR, NT>);
 }
 
-template <int RT, int BITS, bool NT>
-const void *rows_kernel_of(int mt, int tokens)
+// A single token tile takes the weight past by; several have whole tiles of x.
+template <int RT, int BITS>
+const void *rows_kernel_of(const Product &p)
 {
     if constexpr (RT > 1)
-        if (mt == 2)
-            return rows_fn<RT, 2, BITS, 16, NT>();
-    return tokens <= 4   ? rows_fn<RT, 1, BITS, 4, NT>()
-           : tokens <= 8 ? rows_fn<RT, 1, BITS, 8, NT>()
-                         : rows_fn<RT, 1, BITS, 16, NT>();
+        if (p.t == 2)
+            return p.once ? rows_fn<RT, 2, BITS, 16, true>() : rows_fn<RT, 2, BITS, 16, false>();
+    return !p.once          ? rows_fn<RT, 1, BITS, 16, false>()
+           : p.x_rows == 4  ? rows_fn<RT, 1, BITS, 4, true>()
+           : p.x_rows == 8  ? rows_fn<RT, 1, BITS, 8, true>()
+                            : rows_fn<RT, 1, BITS, 16, true>();
 }
 
-template <int BITS, bool NT>
-const void *rows_kernel(int rt, int mt, int tokens)
+template <int BITS>
+const void *rows_kernel(const Product &p)
 {
-    return rt == 1 ? rows_kernel_of<1, BITS, NT>(mt, tokens) : rt == 2 ? rows_kernel_of<2, BITS, NT>(mt, tokens)
-                                                                       : rows_kernel_of<4, BITS, NT>(mt, tokens);
+    return p.r == 1 ? rows_kernel_of<1, BITS>(p) : p.r == 2 ? rows_kernel_of<2, BITS>(p) : rows_kernel_of<4, BITS>(p);
 }
-
-// The largest tiles whose registers fit: 32 * 8 4-bit tokens, 32 * 6 8-bit ones,
-// 32 * 4 with powers of any alignment.
-constexpr int kTiles = 8, kTiles8 = 6, kAnyTiles = 4;
 
 template <int T0>
 const void *tiles_fn(int bits, bool words)
@@ -1091,11 +1089,12 @@ const void *tiles_fn(int bits, bool words)
     return reinterpret_cast<const void *>(product_tiles<T0, true>);
 }
 
+// t0 from kFewest to most_tiles(bits, words).
 const void *tiles_kernel(int t0, int bits, bool words)
 {
-    return t0 == 1 ? tiles_fn<1>(bits, words) : t0 == 2 ? tiles_fn<2>(bits, words) : t0 == 3 ? tiles_fn<3>(bits, words)
-         : t0 == 4 ? tiles_fn<4>(bits, words) : t0 == 5 ? tiles_fn<5>(bits, words) : t0 == 6 ? tiles_fn<6>(bits, words)
-         : t0 == 7 ? tiles_fn<7>(bits, words) : tiles_fn<8>(bits, words);
+    return t0 == 2 ? tiles_fn<2>(bits, words) : t0 == 3 ? tiles_fn<3>(bits, words) : t0 == 4 ? tiles_fn<4>(bits, words)
+         : t0 == 5 ? tiles_fn<5>(bits, words) : t0 == 6 ? tiles_fn<6>(bits, words) : t0 == 7 ? tiles_fn<7>(bits, words)
+                                                                                           : tiles_fn<8>(bits, words);
 }
 
 template <int T0>
@@ -1106,72 +1105,19 @@ int tiles_lds_of(int bits)
 
 int tiles_lds(int t0, int bits)
 {
-    return t0 == 1 ? tiles_lds_of<1>(bits) : t0 == 2 ? tiles_lds_of<2>(bits) : t0 == 3 ? tiles_lds_of<3>(bits)
-         : t0 == 4 ? tiles_lds_of<4>(bits) : t0 == 5 ? tiles_lds_of<5>(bits) : t0 == 6 ? tiles_lds_of<6>(bits)
-         : t0 == 7 ? tiles_lds_of<7>(bits) : tiles_lds_of<8>(bits);
+    return t0 == 2 ? tiles_lds_of<2>(bits) : t0 == 3 ? tiles_lds_of<3>(bits) : t0 == 4 ? tiles_lds_of<4>(bits)
+         : t0 == 5 ? tiles_lds_of<5>(bits) : t0 == 6 ? tiles_lds_of<6>(bits) : t0 == 7 ? tiles_lds_of<7>(bits)
+                                                                                     : tiles_lds_of<8>(bits);
 }
 
-// A tile shape and the time of its rounds over 256 CUs, in us over K = 7168.
-struct Tiling {
-    int r, t;                   // 16 r rows by 16 t tokens, or 256 rows by 32 t tokens
-    float us;
-};
-
-// product_tiles and product_tiles8: a round on the scale of rows_tiling, 8-bit
-// tokens' a fifth below what it takes alone.  Over 512 to 6288 rows, 65 to 2000 tokens
-// and K = 1536 to 18432 the kernel taken was within a geometric mean of 0.1 % (4
-// bits) and 0.8 % (8 bits) of the fastest, at worst 2 and 10 %.
-Tiling tiles_tiling(int M, int N, int bits, bool words)
-{
-    static const float us4[9] = {0.0f, 22.0f, 23.5f, 27.0f, 30.4f, 35.5f, 39.3f, 43.5f, 47.6f};
-    static const float us8[9] = {0.0f, 45.0f, 50.0f, 57.0f, 65.0f, 81.0f, 91.0f};
-    Tiling best{0, 0, 0.0f};
-    for (int t = !words ? kAnyTiles : bits == 4 ? kTiles : kTiles8; t >= 1; --t) {
-        const long long count = ((long long)N + 255) / 256 * ((M + 32 * t - 1) / (32 * t));
-        const float us = (float)((count + 255) / 256) * (bits == 4 ? us4 : us8)[t];
-        if (!best.r || us < best.us)
-            best = Tiling{16, t, us};
-    }
-    return best;
-}
-
-// product_rows: what each further workgroup of a CU adds, measured at K = 7168
-// over 1024 to 14336 rows and 1 to 128 tokens (both grow with K alike).  16 x 32
-// tiles and those of 48 and 64 tokens were never the fastest (64 x 6288 x 7168:
-// 64 rows by 32 tokens 8.8 us, by 64 14.8).  32 rows by 32 8-bit tokens take as many rounds
-// as 64 by 16 and are a little ahead: 37 x 3584 x 7168 9.0 against 9.2 us.
-Tiling rows_tiling(int M, int N, int bits)
-{
-    static const struct {
-        int r, t;
-        float us4, us8;
-    } kTiles[] = {{1, 1, 1.65f, 2.45f}, {2, 1, 2.05f, 3.2f}, {4, 1, 3.4f, 5.35f}, {2, 2, 3.2f, 5.2f}, {4, 2, 4.6f, 9.7f}};
-    Tiling best{0, 0, 0.0f};
-    for (const auto &k : kTiles) {
-        if (k.t == 2 && M <= 16)
-            continue;
-        const long long count = ((long long)N + 16 * k.r - 1) / (16 * k.r) * ((M + 16 * k.t - 1) / (16 * k.t));
-        const float us = (float)((count + 255) / 256) * (bits == 4 ? k.us4 : k.us8);
-        if (!best.r || us < best.us)
-            best = Tiling{k.r, k.t, us};
-    }
-    return best;
-}
-
-// Up to 64 tokens product_rows, above the shorter of both: 400 tokens of 6288 x 7168
-// 27.7 against 23.6 us in 4 bits, of 1536 x 7168 12.1 against 21.2.
 hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
 {
     constexpr unsigned kThreads = 512;
     constexpr int kSplit = 256;                 // rows and tokens of the largest tile: both halves begin on one
     void *params[] = {&a};
     const bool words = a.words != 0;
-    const Tiling rows = rows_tiling(a.M, a.N, bits);
-    const Tiling tiles = a.M > 64 ? tiles_tiling(a.M, a.N, bits, words) : rows;
-    const bool many = tiles.us < rows.us;
-    const int n_rows = many ? 256 : 16 * rows.r, tokens = many ? 32 * tiles.t : 16 * rows.t;
-    const long long n_tiles = ((long long)a.N + n_rows - 1) / n_rows, m_tiles = ((long long)a.M + tokens - 1) / tokens;
-    if (n_tiles * m_tiles > kMostThreads / kThreads) {
+    const Product p = product_of(a.M, a.N, bits, words);
+    if (p.n_tiles * p.m_tiles > kMostThreads / kThreads) {
         // more threads than a launch may have: the two halves of the longer side, one after the other
         const int bytes = type_bytes(a.type);
         PArgs second = a;
@@ -1197,23 +1143,25 @@ hipError_t launch_product(PArgs a, int bits, hipStream_t stream)
         const hipError_t e = launch_product(a, bits, stream);
         return e == hipSuccess ? launch_product(second, bits, stream) : e;
     }
-    a.n_tiles = (int)n_tiles;
-    a.m_tiles = (int)m_tiles;
-    const void *fn = many        ? tiles_kernel(tiles.t, bits, words)
-                     : bits == 4 ? (a.m_tiles == 1 ? rows_kernel<4, true>(rows.r, rows.t, a.M) : rows_kernel<4, false>(rows.r, rows.t, a.M))
-                               : (a.m_tiles == 1 ? rows_kernel<8, true>(rows.r, rows.t, a.M) : rows_kernel<8, false>(rows.r, rows.t, a.M));
-    return hipLaunchKernel(fn, dim3((unsigned)(n_tiles * m_tiles)), dim3(kThreads), params,
-                           many ? (size_t)tiles_lds(tiles.t, bits) : 0, stream);
+    a.n_tiles = (int)p.n_tiles;
+    a.m_tiles = (int)p.m_tiles;
+    const void *fn = p.many ? tiles_kernel(p.t, bits, words) : bits == 4 ? rows_kernel<4>(p) : rows_kernel<8>(p);
+    return hipLaunchKernel(fn, dim3((unsigned)(p.n_tiles * p.m_tiles)), dim3(kThreads), params,
+                           p.many ? (size_t)tiles_lds(p.t, bits) : 0, stream);
 }
 
 // Dynamic LDS past 64 KiB has to be asked for, on every device that the kernels run on.
-void raise_limits()
+hipError_t raise_limits()
 {
-    for (int t0 = 1; t0 <= kTiles; ++t0)
-        for (const int bits : {4, 8})
-            for (const bool words : {false, true})
-                (void)hipFuncSetAttribute(tiles_kernel(t0, bits, words), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                          tiles_lds(t0, bits));
+    for (const int bits : {4, 8})
+        for (const bool words : {false, true})
+            for (int t0 = kFewest; t0 <= most_tiles(bits, words); ++t0) {
+                const hipError_t e = hipFuncSetAttribute(
+                    tiles_kernel(t0, bits, words), hipFuncAttributeMaxDynamicSharedMemorySize, tiles_lds(t0, bits));
+                if (e != hipSuccess)
+                    return e;
+            }
+    return hipSuccess;
 }
 
 // fn(first vector, launch's end) over count vectors of 256-thread workgroups, in launches of fewer than 2^32 threads.
@@ -1376,8 +1324,9 @@ skinny_status skinny_mxfp4_prepare(const void *Wq, int N, int K, long long ldw, 
         delete p;
         return st;
     }
-    raise_limits();
-    hipError_t e = hipMalloc(&p->w, (size_t)count * 16);
+    hipError_t e = raise_limits();
+    if (e == hipSuccess)
+        e = hipMalloc(&p->w, (size_t)count * 16);
     if (e == hipSuccess)
         e = hipMalloc(reinterpret_cast<void **>(&p->w_scale), (size_t)scales * 4);
     const hipStream_t s = (hipStream_t)stream;
