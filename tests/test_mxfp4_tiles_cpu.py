@@ -55,3 +55,15 @@ def test_the_library_has_the_kernels_that_are_reached(reached):
         elif name != "product_rows" and len(a) == 2:
             built.add(f"tiles {a[0]} bits {8 if name.endswith('8') else 4} {'words' if a[1] == 'true' else 'any'}")
     assert built == reached
+
+
+def test_gpu_tests_reach_every_kernel(check, reached):
+    """The sizes of test_gpu_mxfp4_tiles.py, in the ways in which it lays out powers."""
+    from . import test_gpu_mxfp4_tiles as t
+    calls = [(m, n, bits, 1) for m, n in t.ROWS for bits in (4, 8)]
+    calls += [(m, n, bits, words) for bits, m, n in t.BOTH for words in (0, 1)]
+    calls += [(m, n, bits, 1) for bits in (4, 8) for m, n in t.WORDS[bits]]
+    names = check("name", text="".join("%d %d %d %d\n" % c for c in calls))
+    assert len(names) == len(calls)
+    assert all(name.startswith("rows" if c[:2] in t.ROWS else "tiles") for c, name in zip(calls, names))
+    assert set(names) == reached
