@@ -568,9 +568,10 @@ skinny_status skinny_mxfp4_prepare(const void *Wq, int N, int K, long long ldw, 
  *
  * xq: codes of `bits` (4 or 8), row m at m * ldx bytes, 16-byte aligned,
  * ldx % 16 == 0 and <= 2^22; x_scale: row m at m * ldxs, <= 2^22, any alignment.
- * Products are exact and sums fp32, in an order that depends on the sizes alone
- * (8-bit tokens go through BF16: their powers have to lie from 2^-117 to 2^119 and
- * w's from 2^-125 to 2^125; values outside are rounded or infinite).  residual
+ * Products are exact and sums fp32, in an order that depends on the sizes alone.
+ * 8-bit tokens go through BF16: with powers below 2^-124 (blocks with nothing
+ * above 2^-116) their values are rounded to multiples of 2^-133, and powers above
+ * 2^119, of w above 2^125, which no finite fp32 values get, make infinities.  residual
  * (NULL for none) and out have the plan's out type, elements m * ldr + n and
  * m * ldo + n; residual may be out itself (ldr == ldo) but must not otherwise
  * overlap out.  A NaN (a power of 255, an 8-bit code) reaches the outputs that

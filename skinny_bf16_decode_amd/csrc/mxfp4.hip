@@ -300,9 +300,10 @@ __device__ __forceinline__ f32x4 mma128(u32x4 w, u32x4 x, f32x4 c, unsigned ws, 
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widened(w), widened(x), c, 4, 4, WB, (int)ws, 0, (int)xs);
 }
 
-// Eight values times their power in BF16, which holds a code of 4 bits with powers
-// of 2^-125 to 2^125 and one of 8 with 2^-117 to 2^119: all that a block of normal
-// values gets.
+// Eight values times their power in BF16, whose subnormals reach down to 2^-133 and are
+// kept: exact for codes of 4 bits with powers of 2^-127 to 2^125 and of 8 with 2^-124
+// to 2^119.  Blocks of finite fp32 values get no larger ones; 8-bit blocks with nothing above
+// 2^-116 may get smaller ones, and their values are rounded to multiples of 2^-133.
 __device__ __forceinline__ bf16x8 bf16_of_4(unsigned w, float power)
 {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 0);

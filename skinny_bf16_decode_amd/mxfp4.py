@@ -138,7 +138,13 @@ class PreparedMxfp4:
         on the current (or given) stream; returns out.  xq: codes of 8 or 4 bits
         (quantize_blocks' types), 16-byte aligned with a pitch that is a
         multiple of 16 bytes; x_scale [>= M, K / 32]; out and residual:
-        out_dtype [>= M, N], may be row-pitched; residual may be out itself."""
+        out_dtype [>= M, N], may be row-pitched; residual may be out itself.
+
+        8-bit tokens go through BF16: with powers below 2^-124 (byte 3; blocks
+        with nothing above 2^-116) their values are rounded to multiples of
+        2^-133; powers above 2^119 (byte 246), of the weight above 2^125 (252),
+        which quantize_blocks never gives, make infinities.  4-bit tokens are
+        exact at every power."""
         if not self._plan:
             raise ValueError("the plan is closed")
         m = xq.shape[0]
