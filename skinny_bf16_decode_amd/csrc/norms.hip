@@ -305,10 +305,10 @@ __device__ __forceinline__ void write_norm(const NormOut &n, double sum, int K, 
             const Octet next = i + 1 < turns ? own_octet<MODE>(n.weight, n.weight_type, i + 1, K, lanes, p) : w;
             float f[8];
             value(i, w, f);
-            // past the row the weight is zero, and r may be infinite or NaN
+            // past the row f is zero, but where r is NaN, and all of the row with it (eps keeps r below 2^60)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const unsigned m = index_of<MODE>(i, e, lanes, p) < (unsigned)K ? mag(f[e]) : 0u;
+                const unsigned m = mag(f[e]);
                 top = m > top ? m : top;
             }
             w = next;
@@ -551,8 +551,8 @@ __device__ __forceinline__ Octet octet_of(const void *base, long long row, long 
 // The norms of R rows from `first` on, of which f gives octet i of row j.
 template <int C, int R, typename Get>
 __device__ __forceinline__ void write_norms(const NormOut &n, const double (&squares_of)[R], const float (&w)[C][8],
-                                            int octets, int K, long long first, int M, int waves,
-                                            double (*sums)[16], unsigned (*tops)[16], Get get)
+                                            int K, long long first, int M, int waves, double (*sums)[16],
+                                            unsigned (*tops)[16], Get get)
 {
     const float rl = rms_factor(over_rows<R>(squares_of, waves, sums), n.inverse_K, n.eps);
     float r[R];
@@ -569,10 +569,10 @@ __device__ __forceinline__ void write_norms(const NormOut &n, const double (&squ
             for (int i = 0; i < C; ++i) {
                 float f[8];
                 get(j, i, f);
-                const bool here = (int)threadIdx.x + i * (int)blockDim.x < octets;
+                // as in write_norm, past the row zero
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const unsigned m = here ? mag(f[e] * r[j] * w[i][e]) : 0u;
+                    const unsigned m = mag(f[e] * r[j] * w[i][e]);
                     top[j] = m > top[j] ? m : top[j];
                 }
             }
@@ -643,7 +643,7 @@ __global__ __launch_bounds__(1024) void norm_stream(NArgs a)
                 sum[j] += squares(f);
             }
         }
-        write_norms<C, R>(a.n, sum, w, octets, a.K, first, a.M, waves, sums[turn], tops[turn],
+        write_norms<C, R>(a.n, sum, w, a.K, first, a.M, waves, sums[turn], tops[turn],
                           [&](int j, int i, float (&f)[8]) { unpack_octet(x[j][i], type, f); });
 #pragma unroll
         for (int j = 0; j < R; ++j)
@@ -740,7 +740,7 @@ __global__ __launch_bounds__(1024) void join_stream(JArgs a)
             }
         }
         if (a.n.weight)
-            write_norms<C, R>(a.n, sum, nw, octets, a.K, first, a.M, waves, sums[2 + turn], tops[turn],
+            write_norms<C, R>(a.n, sum, nw, a.K, first, a.M, waves, sums[2 + turn], tops[turn],
                               [&](int j, int i, float (&f)[8]) { unpack_octet(hs[j][i], residual_type, f); });
 #pragma unroll
         for (int j = 0; j < R; ++j)
