@@ -67,3 +67,13 @@ def test_gpu_tests_reach_every_kernel(check, reached):
     assert len(names) == len(calls)
     assert all(name.startswith("rows" if c[:2] in t.ROWS else "tiles") for c, name in zip(calls, names))
     assert set(names) == reached
+
+
+def test_sizes_past_one_launch(check):
+    """The sizes of test_gpu_operator_launches.py make more workgroups of 512 threads than one launch may have."""
+    tiles = {"4 268436000": "rows 2x2", "8 134218000": "rows 1x1"}
+    for name, tokens in (("4 268436000", 32), ("8 134218000", 16)):
+        bits, m = map(int, name.split())
+        assert check("name", text=f"{m} 7 {bits} 0")[0].startswith(tiles[name]) and m // tokens > 0xFFFFFFFF // 512
+    for bits in (4, 8):
+        assert check("name", text=f"2 536872000 {bits} 0")[0].startswith("rows 4x1") and 536872000 // 64 > 0xFFFFFFFF // 512
