@@ -17,8 +17,9 @@ inline Mode mode_of(bool vec, int q_kind)
     return vec ? kVectors : q_kind == SKINNY_ROWS_MX4 || q_kind == SKINNY_ROWS_MX8 ? kElements : kStrided;
 }
 
-// Octets of a row of K elements, the last one part full.  K + 7 may pass 2^31.
-constexpr int octets_of(int K) { return (int)(((unsigned)K + 7u) / 8u); }
+// Octets of a row of K >= 1 elements, the last one part full.  K + 7 may pass 2^31; counted
+// unsigned for that, joins of 4000 x 7168 took 65.9 us in place of 65.4.
+constexpr int octets_of(int K) { return (K - 1) / 8 + 1; }
 
 // Octets a thread keeps (0: any number, read again) and threads a row.
 struct RowShape {
