@@ -119,21 +119,23 @@ __global__ __launch_bounds__(1024) void quantize_vector(QArgs a)
     }
 }
 
-// Any K, pitch and alignment, an element at a time.  An index past the longest
-// rows' end does not fit 31 bits.
+// Any K, pitch and alignment, an element at a time, in two parts past 2^30, in
+// which an index and 256 more fit 31 bits (unsigned, 4 x 7167 take 8.7 us in place of 8.0).
 template <int TYPE>
 __global__ __launch_bounds__(256) void quantize_element(QArgs a)
 {
     using E = Elem<TYPE>;
     __shared__ unsigned tops[4];
-    const unsigned tid = threadIdx.x, K = (unsigned)a.K;
+    const int tid = threadIdx.x;
     const typename E::raw *x = static_cast<const typename E::raw *>(a.x) + blockIdx.x * a.ldx;
     signed char *q = a.q + blockIdx.x * a.ldq;
+    constexpr int kPart = 1 << 30;
     unsigned top = 0;
-    for (unsigned i = tid; i < K; i += 256) {
-        const unsigned m = mag(E::get(x[i]));
-        top = m > top ? m : top;
-    }
+    for (int from = 0, n = min(a.K, kPart); n > 0; from += n, n = a.K - from)
+        for (int i = tid; i < n; i += 256) {
+            const unsigned m = mag(E::get((x + from)[i]));
+            top = m > top ? m : top;
+        }
     top = wave_max_u(top);
     if ((tid & 63) == 0)
         tops[tid >> 6] = top;
@@ -145,8 +147,9 @@ __global__ __launch_bounds__(256) void quantize_element(QArgs a)
     const RowScale r = row_scale(top, scale);
     if (tid == 0)
         a.scale[blockIdx.x] = scale;
-    for (unsigned i = tid; i < K; i += 256)
-        q[i] = (signed char)to_int8(E::get(x[i]), r);
+    for (int from = 0, n = min(a.K, kPart); n > 0; from += n, n = a.K - from)
+        for (int i = tid; i < n; i += 256)
+            (q + from)[i] = (signed char)to_int8(E::get((x + from)[i]), r);
 }
 
 // ---------------------------------------------------------------------------
