@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 
 # rows, length, at an unaligned place, quantized kind
-NORMS = [(5, 320, 0, "mx8"), (3, 12288, 0, "mx4"), (2, 30720, 0, "int8"), (515, 96, 0, "mx8"), (514, 9216, 0, None),
+NORMS = [(5, 320, 0, "mx8"), (3, 12288, 0, "mx4"), (2, 30816, 0, "int8"), (515, 96, 0, "mx8"), (514, 9216, 0, None),
          (513, 32768, 0, "mx4"), (3, 65536, 0, "mx8"),                     # whole vectors
          (7, 320, 1, "mx8"), (600, 96, 1, "mx4"), (3, 8224, 1, "mx8"), (2, 20000, 1, "mx4"),   # blocks, one element at a time
          (5, 333, 0, "int8"), (600, 77, 1, None), (3, 8201, 0, "int8"), (2, 12289, 1, None), (3, 16384, 1, "int8"),
@@ -26,7 +26,7 @@ NORMS = [(5, 320, 0, "mx8"), (3, 12288, 0, "mx4"), (2, 30720, 0, "int8"), (515, 
 STREAMED = [(4003, 7168), (3075, 7168), (12285, 2048), (4097, 4096), (3999, 7168), (4090, 8192), (2500, 7168), (300, 1544),
             (261, 12288), (259, 24576), (1027, 16640)]
 # more of each kind of join: rows, length, unaligned, kind, a gate for each token
-JOINS = [(5, 320, 0, "mx8", True), (3, 12288, 0, "mx4", False), (2, 30720, 0, "int8", True), (514, 9216, 0, None, True),
+JOINS = [(5, 320, 0, "mx8", True), (3, 12288, 0, "mx4", False), (2, 30816, 0, "int8", True), (514, 9216, 0, None, True),
          (3, 65536, 0, "mx8", False), (1300, 1056, 0, "mx4", True),
          (7, 320, 1, "mx8", False), (600, 96, 1, "mx4", True), (3, 8224, 1, "mx8", True), (2, 20000, 1, "mx4", False),
          (5, 333, 0, "int8", True), (3, 8201, 0, "int8", False), (2, 12289, 1, None, True), (520, 8193, 1, None, False),
